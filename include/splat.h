@@ -291,6 +291,88 @@ int splat_interpolate_bwd(const float *key_times, int n_keys, float t, int n, co
                           const float *d_pos, const float *d_rot, float *d_key_pos, float *d_key_rot,
                           hipStream_t stream);
 
+/* ---- learned appearance -----------------------------------------------------------
+ * What stands on either side of the renderer when a scene is trained: features read
+ * from a table that primitives share, the normalisation inside the network that turns
+ * a rendered feature image into colour (neural shading, Pulsar sec. 3), and the
+ * orthogonalised update of that network's matrices.
+ *
+ * Arrays are of a splat_dtype; strides are counted in elements, the innermost axis is
+ * contiguous, and every pointer is aligned to its element. Any stride and alignment is
+ * served; 16-byte alignment of rows is served fastest. Arithmetic is in fp32 (or more),
+ * with one rounding to the array's type at the end. Workspaces are caller-owned device
+ * memory of the queried size, 16-byte aligned, with no contents kept between calls. A
+ * size of zero is no error: the outputs that remain are written (gradients of nothing
+ * are zero). Sums run in a fixed order: equal inputs give equal bits. */
+typedef enum { SPLAT_F32 = 0, SPLAT_F16 = 1, SPLAT_BF16 = 2 } splat_dtype;
+typedef enum { SPLAT_I32 = 0, SPLAT_I64 = 1 } splat_itype;
+typedef enum {
+  SPLAT_ACT_NONE = 0,
+  SPLAT_ACT_RELU = 1,           /* max(z, 0); slope 0 at 0 */
+  SPLAT_ACT_SILU = 2,           /* z / (1 + exp(-z)) */
+  SPLAT_ACT_GELU = 3            /* z (1 + erf(z / sqrt 2)) / 2 */
+} splat_act;
+
+/* out[i] = scale * table[ids[i]]: rows of a shared feature table. An id outside
+ * [0, rows) reads nothing and gives a row of zeros (primitives without an entry).
+ * table [rows][dim] with row stride table_stride, ids [n] of itype, out [n][dim] with
+ * row stride out_stride. n < 2^31, dim <= 65536, |scale| finite. */
+int splat_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t table_stride, const void *ids,
+                 int itype, int64_t n, float scale, void *out, int64_t out_stride, hipStream_t stream);
+
+/* The table's gradient: d_table[v] = scale * (sum of d_out[i] over i with ids[i] = v),
+ * every row written (accumulate = 0) or added to (accumulate = 1). d_out [n][dim] and
+ * d_table [rows][dim] are of one dtype; sums are fp32. The tokens are sorted by id
+ * inside the call. n < 2^31, rows < 2^31 - 1, dim <= 65536.
+ * workspace: [splat_lookup_bwd_workspace_bytes] device bytes. */
+size_t splat_lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim);
+int splat_lookup_bwd(const void *d_out, int dtype, int64_t d_out_stride, const void *ids, int itype, int64_t n,
+                     int64_t rows, int dim, float scale, void *d_table, int64_t d_table_stride, int accumulate,
+                     void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* HOST struct: group norm with an activation over channels-last images [images][pixels]
+ * [channels]. The channels / groups channels of a group share mean and variance over an
+ * image's pixels. param_dtype (weight, bias and their gradients): SPLAT_F32 or dtype.
+ * The strides of x; of y (forward) or d_y (backward); and of d_x. channels a multiple of
+ * groups, channels <= 65536; eps >= 0, finite. */
+typedef struct {
+  int32_t dtype, param_dtype, act, channels, groups;
+  float eps;
+  int64_t images, pixels;
+  int64_t x_image_stride, x_pixel_stride;
+  int64_t y_image_stride, y_pixel_stride;
+  int64_t dx_image_stride, dx_pixel_stride;
+} splat_norm;
+
+/* Workspace bytes of either direction. */
+size_t splat_group_norm_workspace_bytes(const splat_norm *norm);
+
+/* y = act(weight (x - mean) rstd + bias), rstd = 1 / sqrt(var + eps). weight and bias
+ * [channels] may be NULL (1 and 0). mean, rstd [images][groups] fp32 receive the
+ * statistics, which splat_group_norm_bwd reads. */
+int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, const void *bias, void *y,
+                     float *mean, float *rstd, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Gradients w.r.t. x, weight and bias given d_y and the forward's x, mean and rstd
+ * (overwritten; a NULL output is not computed). */
+int splat_group_norm_bwd(const splat_norm *norm, const void *d_y, const void *x, const float *mean,
+                         const float *rstd, const void *weight, const void *bias, void *d_x, void *d_weight,
+                         void *d_bias, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Orthogonalised updates. For each matrix G [rows][cols] of the batch: X = G / (|G|_F +
+ * eps), transposed if rows > cols; `steps` times X <- (a I + b A + c A A) X with
+ * A = X X^T; out = scale X, transposed back. Usual coefficients: 3.4445, -4.7750, 2.0315
+ * with 5 steps, which bring singular values between about 0.01 and 1 to 0.7 .. 1.2.
+ * Products keep 22 bits of each factor and fp32 sums. 1 <= steps <= 64; rows, cols <=
+ * 65536; batch <= 65535; eps >= 0. Coefficients under which singular values could grow
+ * past 1e4 return SPLAT_ERR_UNSUPPORTED. out may not overlap g.
+ * workspace: [splat_orthogonalize_workspace_bytes] device bytes. */
+size_t splat_orthogonalize_workspace_bytes(int64_t batch, int rows, int cols);
+int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int cols, int64_t g_batch_stride,
+                        int64_t g_row_stride, int steps, float a, float b, float c, float eps, float scale,
+                        void *out, int64_t out_batch_stride, int64_t out_row_stride, void *workspace,
+                        size_t ws_bytes, hipStream_t stream);
+
 const char *splat_status_string(int status);
 
 #ifdef __cplusplus

@@ -17,13 +17,19 @@ SPLAT_OK, SPLAT_ERR_INVALID_ARG, SPLAT_ERR_CAPACITY, SPLAT_ERR_HIP, SPLAT_ERR_UN
 SPLAT_PRIM_GAUSS2D, SPLAT_PRIM_GAUSS3D, SPLAT_PRIM_SPHERE = 0, 1, 2
 SPLAT_CAM_PINHOLE, SPLAT_CAM_SPHERICAL = 0, 1
 SPLAT_MAX_VIEWS, SPLAT_MAX_CHANNELS = 16, 64
+SPLAT_F32, SPLAT_F16, SPLAT_BF16 = 0, 1, 2
+SPLAT_I32, SPLAT_I64 = 0, 1
+SPLAT_ACT_NONE, SPLAT_ACT_RELU, SPLAT_ACT_SILU, SPLAT_ACT_GELU = 0, 1, 2, 3
 
 # include/splat.h: size of the fixed device array splat_bin_sort_noalloc sorts in
 SPLAT_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTS = ["splat_projected_bytes", "splat_total_tiles", "splat_sort_workspace_bytes",
            "splat_bwd_workspace_bytes", "splat_project", "splat_bin_sort", "splat_bin_sort_noalloc", "splat_render_fwd",
-           "splat_render_bwd", "splat_interpolate", "splat_interpolate_bwd", "splat_status_string"]
+           "splat_render_bwd", "splat_interpolate", "splat_interpolate_bwd", "splat_lookup",
+           "splat_lookup_bwd_workspace_bytes", "splat_lookup_bwd", "splat_group_norm_workspace_bytes",
+           "splat_group_norm", "splat_group_norm_bwd", "splat_orthogonalize_workspace_bytes",
+           "splat_orthogonalize", "splat_status_string"]
 
 
 class splat_camera(C.Structure):
@@ -53,6 +59,14 @@ class splat_grads(C.Structure):
                 ("cam_t", C.c_void_p), ("cam_K", C.c_void_p), ("accumulate", C.c_int32),
                 ("normalize", C.c_int32), ("sums_cleared", C.c_int32),
                 ("atomic_direct_max", C.c_int32)]
+
+
+class splat_norm(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("param_dtype", C.c_int32), ("act", C.c_int32), ("channels", C.c_int32),
+                ("groups", C.c_int32), ("eps", C.c_float), ("images", C.c_int64), ("pixels", C.c_int64),
+                ("x_image_stride", C.c_int64), ("x_pixel_stride", C.c_int64),
+                ("y_image_stride", C.c_int64), ("y_pixel_stride", C.c_int64),
+                ("dx_image_stride", C.c_int64), ("dx_pixel_stride", C.c_int64)]
 
 
 class SplatError(RuntimeError):
@@ -98,6 +112,24 @@ def lib():
         L.splat_interpolate.argtypes = [fp, i32, C.c_float, i32, vp, vp, vp, vp, vp]
         L.splat_interpolate_bwd.restype = i32
         L.splat_interpolate_bwd.argtypes = [fp, i32, C.c_float, i32, vp, vp, vp, vp, vp, vp]
+        f32, norm_p = C.c_float, C.POINTER(splat_norm)
+        L.splat_lookup.restype = i32
+        L.splat_lookup.argtypes = [vp, i32, i64, i32, i64, vp, i32, i64, f32, vp, i64, vp]
+        L.splat_lookup_bwd_workspace_bytes.restype = sz
+        L.splat_lookup_bwd_workspace_bytes.argtypes = [i64, i64, i32]
+        L.splat_lookup_bwd.restype = i32
+        L.splat_lookup_bwd.argtypes = [vp, i32, i64, vp, i32, i64, i64, i32, f32, vp, i64, i32, vp, sz, vp]
+        L.splat_group_norm_workspace_bytes.restype = sz
+        L.splat_group_norm_workspace_bytes.argtypes = [norm_p]
+        L.splat_group_norm.restype = i32
+        L.splat_group_norm.argtypes = [norm_p, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.splat_group_norm_bwd.restype = i32
+        L.splat_group_norm_bwd.argtypes = [norm_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.splat_orthogonalize_workspace_bytes.restype = sz
+        L.splat_orthogonalize_workspace_bytes.argtypes = [i64, i32, i32]
+        L.splat_orthogonalize.restype = i32
+        L.splat_orthogonalize.argtypes = [vp, i32, i64, i32, i32, i64, i64, i32, f32, f32, f32, f32, f32, vp, i64,
+                                          i64, vp, sz, vp]
         L.splat_status_string.restype = C.c_char_p
         L.splat_status_string.argtypes = [i32]
         _L = L
@@ -181,3 +213,46 @@ def splat_interpolate_bwd(key_times, t, n, key_rot, d_pos, d_rot, d_key_pos, d_k
     kt, nk = _times(key_times)
     return _check("splat_interpolate_bwd", lib().splat_interpolate_bwd(kt, nk, float(t), n, key_rot, d_pos, d_rot,
                                                                        d_key_pos, d_key_rot, stream))
+
+
+def splat_lookup(table, dtype, rows, dim, table_stride, ids, itype, n, scale, out, out_stride, stream):
+    return _check("splat_lookup", lib().splat_lookup(table, dtype, rows, dim, table_stride, ids, itype, n, scale, out,
+                                                     out_stride, stream))
+
+
+def splat_lookup_bwd_workspace_bytes(n, rows, dim):
+    return lib().splat_lookup_bwd_workspace_bytes(n, rows, dim)
+
+
+def splat_lookup_bwd(d_out, dtype, d_out_stride, ids, itype, n, rows, dim, scale, d_table, d_table_stride, accumulate,
+                     workspace, ws_bytes, stream):
+    return _check("splat_lookup_bwd", lib().splat_lookup_bwd(d_out, dtype, d_out_stride, ids, itype, n, rows, dim,
+                                                             scale, d_table, d_table_stride, accumulate, workspace,
+                                                             ws_bytes, stream))
+
+
+def splat_group_norm_workspace_bytes(norm):
+    return lib().splat_group_norm_workspace_bytes(C.byref(norm))
+
+
+def splat_group_norm(norm, x, weight, bias, y, mean, rstd, workspace, ws_bytes, stream):
+    return _check("splat_group_norm", lib().splat_group_norm(C.byref(norm), x, weight, bias, y, mean, rstd, workspace,
+                                                             ws_bytes, stream))
+
+
+def splat_group_norm_bwd(norm, d_y, x, mean, rstd, weight, bias, d_x, d_weight, d_bias, workspace, ws_bytes, stream):
+    return _check("splat_group_norm_bwd", lib().splat_group_norm_bwd(C.byref(norm), d_y, x, mean, rstd, weight, bias,
+                                                                     d_x, d_weight, d_bias, workspace, ws_bytes,
+                                                                     stream))
+
+
+def splat_orthogonalize_workspace_bytes(batch, rows, cols):
+    return lib().splat_orthogonalize_workspace_bytes(batch, rows, cols)
+
+
+def splat_orthogonalize(g, dtype, batch, rows, cols, g_batch_stride, g_row_stride, steps, a, b, c, eps, scale, out,
+                        out_batch_stride, out_row_stride, workspace, ws_bytes, stream):
+    return _check("splat_orthogonalize", lib().splat_orthogonalize(g, dtype, batch, rows, cols, g_batch_stride,
+                                                                   g_row_stride, steps, a, b, c, eps, scale, out,
+                                                                   out_batch_stride, out_row_stride, workspace,
+                                                                   ws_bytes, stream))

@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplat.so")
-SOURCES = ["api.hip", "project.hip", "binsort.hip", "render_fwd.hip", "render_bwd.hip", "assemble.hip"]
+SOURCES = ["api.hip", "project.hip", "binsort.hip", "render_fwd.hip", "render_bwd.hip", "assemble.hip",
+           "lookup.hip", "group_norm.hip", "orthogonalize.hip"]
 # measurement kernels (sustained clock, copy and LDS bandwidth), a library of their own
 PEAKS_LIB = os.path.join(HERE, "libsplat_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]

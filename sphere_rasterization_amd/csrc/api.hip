@@ -28,6 +28,22 @@ int launch_assemble(const float *key_pos, const float *key_rot, int k, int k1, f
 int launch_assemble_bwd(const float *key_rot, int k, int k1, float w, long long n, const float *d_pos,
                         const float *d_rot, float *d_key_pos, float *d_key_rot, hipStream_t stream);
 
+int launch_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t ldt, const void *ids, int id_type,
+                  int64_t n, float scale, void *out, int64_t ldo, hipStream_t stream);
+size_t lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim);
+int launch_lookup_bwd(const void *d_out, int dtype, int64_t ldy, const void *ids, int id_type, int64_t n, int64_t rows,
+                      int dim, float scale, void *d_table, int64_t ldg, int accumulate, void *ws, hipStream_t stream);
+size_t group_norm_workspace_bytes(const splat_norm *d);
+int launch_group_norm(const splat_norm *d, const void *x, const void *w, const void *b, void *y, float *mean,
+                      float *rstd, void *ws, hipStream_t stream);
+int launch_group_norm_bwd(const splat_norm *d, const void *d_y, const void *x, const float *mean, const float *rstd,
+                          const void *w, const void *b, void *dx, void *dw, void *db, void *ws, hipStream_t stream);
+size_t orthogonalize_workspace_bytes(int64_t batch, int rows, int cols);
+int orthogonalize_bounds(int steps, float a, float b, float c);
+int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int cols, int64_t gb, int64_t gr,
+                         int steps, float ca, float cb, float cc, float eps, float scale, void *out, int64_t ob,
+                         int64_t orow, void *ws, hipStream_t stream);
+
 namespace {
 
 struct SideStream {
@@ -231,6 +247,47 @@ int key_bracket(const float *key_times, int n_keys, float t, int *k, int *k1, fl
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+
+constexpr int MAX_DIM = 65536;
+
+bool known_dtype(int t) { return t == SPLAT_F32 || t == SPLAT_F16 || t == SPLAT_BF16; }
+bool known_itype(int t) { return t == SPLAT_I32 || t == SPLAT_I64; }
+bool aligned_to(const void *p, int dtype) { return ((uintptr_t)p & (dtype == SPLAT_F32 ? 3u : 1u)) == 0; }
+bool aligned_ids(const void *p, int itype) { return ((uintptr_t)p & (itype == SPLAT_I64 ? 7u : 3u)) == 0; }
+// every offset of `count` rows a stride apart stays far inside 64 bits
+bool stride_fits(int64_t stride, int64_t count) {
+  return count <= 1 || (stride >= 0 && stride <= (int64_t)(1ll << 58) / count);
+}
+bool lookup_bwd_size(int64_t n, int64_t rows, int dim) {
+  return n >= 0 && n < (1ll << 31) && rows >= 0 && rows < (1ll << 31) - 1 && dim >= 0 && dim <= MAX_DIM;
+}
+bool ortho_size(int64_t batch, int rows, int cols) {
+  return batch >= 0 && batch <= 65535 && rows >= 0 && rows <= MAX_DIM && cols >= 0 && cols <= MAX_DIM;
+}
+
+// Shape, types and strides; `writes`: y (forward) or d_x (backward) is written.
+int check_norm(const splat_norm *m, bool bwd, bool writes) {
+  CHECK(m != nullptr, SPLAT_ERR_INVALID_ARG, "norm is NULL");
+  CHECK(known_dtype(m->dtype), SPLAT_ERR_INVALID_ARG, "dtype");
+  CHECK(m->param_dtype == SPLAT_F32 || m->param_dtype == m->dtype, SPLAT_ERR_INVALID_ARG, "parameter dtype");
+  CHECK(m->act >= SPLAT_ACT_NONE && m->act <= SPLAT_ACT_GELU, SPLAT_ERR_INVALID_ARG, "activation");
+  CHECK(m->channels >= 1 && m->channels <= MAX_DIM && m->groups >= 1 && m->channels % m->groups == 0,
+        SPLAT_ERR_INVALID_ARG, "channels must be a multiple of groups");
+  CHECK(isfinite(m->eps) && m->eps >= 0.0f, SPLAT_ERR_INVALID_ARG, "eps must be >= 0");
+  CHECK(m->images >= 0 && m->pixels >= 0 && m->images <= (1ll << 40) && m->pixels <= (1ll << 40) &&
+            (m->pixels == 0 || m->images <= (1ll << 40) / m->pixels),
+        SPLAT_ERR_INVALID_ARG, "image size");
+  const int64_t img[3] = {m->x_image_stride, m->y_image_stride, m->dx_image_stride};
+  const int64_t pix[3] = {m->x_pixel_stride, m->y_pixel_stride, m->dx_pixel_stride};
+  for (int k = 0; k < (bwd && writes ? 3 : 2); k++)
+    CHECK(stride_fits(img[k], m->images) && stride_fits(pix[k], m->pixels), SPLAT_ERR_INVALID_ARG, "stride");
+  // x and d_y may repeat pixels or images (stride 0); the image written may not
+  const int o = bwd ? 2 : 1;
+  if (writes)
+    CHECK((m->pixels <= 1 || pix[o] >= m->channels) && (m->images <= 1 || img[o] >= m->channels),
+          SPLAT_ERR_INVALID_ARG, "output pixels overlap");
+  return SPLAT_OK;
+}
 
 }  // namespace
 
@@ -475,6 +532,113 @@ int splat_interpolate_bwd(const float *key_times, int n_keys, float t, int n, co
   }
   return launch_assemble_bwd(key_rot, k, k1, w, n, do_pos ? d_pos : nullptr, do_rot ? d_rot : nullptr,
                              do_pos ? d_key_pos : nullptr, do_rot ? d_key_rot : nullptr, stream);
+}
+
+int splat_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t table_stride, const void *ids,
+                 int itype, int64_t n, float scale, void *out, int64_t out_stride, hipStream_t stream) {
+  CHECK(known_dtype(dtype), SPLAT_ERR_INVALID_ARG, "dtype");
+  CHECK(known_itype(itype), SPLAT_ERR_INVALID_ARG, "index type");
+  CHECK(rows >= 0 && n >= 0 && n < (1ll << 31) && dim >= 0 && dim <= MAX_DIM, SPLAT_ERR_INVALID_ARG, "lookup size");
+  CHECK(isfinite(scale), SPLAT_ERR_INVALID_ARG, "scale not finite");
+  if (n == 0 || dim == 0) return SPLAT_OK;
+  CHECK(out && ids && (table || rows == 0), SPLAT_ERR_INVALID_ARG, "NULL array");
+  CHECK((rows <= 1 || table_stride >= dim) && (n == 1 || out_stride >= dim), SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(stride_fits(table_stride, rows) && stride_fits(out_stride, n), SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(aligned_to(table, dtype) && aligned_to(out, dtype) && aligned_ids(ids, itype), SPLAT_ERR_INVALID_ARG,
+        "array not aligned to its element");
+  return launch_lookup(table, dtype, rows, dim, rows <= 1 ? dim : table_stride, ids, itype, n, scale, out,
+                       n == 1 ? dim : out_stride, stream);
+}
+
+size_t splat_lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim) {
+  if (!lookup_bwd_size(n, rows, dim)) return 0;
+  return lookup_bwd_workspace_bytes(n, rows, dim);
+}
+
+int splat_lookup_bwd(const void *d_out, int dtype, int64_t d_out_stride, const void *ids, int itype, int64_t n,
+                     int64_t rows, int dim, float scale, void *d_table, int64_t d_table_stride, int accumulate,
+                     void *workspace, size_t ws_bytes, hipStream_t stream) {
+  CHECK(known_dtype(dtype), SPLAT_ERR_INVALID_ARG, "dtype");
+  CHECK(known_itype(itype), SPLAT_ERR_INVALID_ARG, "index type");
+  CHECK(lookup_bwd_size(n, rows, dim), SPLAT_ERR_INVALID_ARG, "lookup size");
+  CHECK(isfinite(scale), SPLAT_ERR_INVALID_ARG, "scale not finite");
+  CHECK(accumulate == 0 || accumulate == 1, SPLAT_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+  if (rows == 0 || dim == 0) return SPLAT_OK;
+  CHECK(d_table && (n == 0 || (d_out && ids)), SPLAT_ERR_INVALID_ARG, "NULL array");
+  CHECK((n <= 1 || d_out_stride >= dim) && (rows == 1 || d_table_stride >= dim), SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(stride_fits(d_out_stride, n) && stride_fits(d_table_stride, rows), SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(aligned_to(d_out, dtype) && aligned_to(d_table, dtype) && aligned_ids(ids, itype), SPLAT_ERR_INVALID_ARG,
+        "array not aligned to its element");
+  if (n > 0) {
+    CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+    CHECK(ws_bytes >= lookup_bwd_workspace_bytes(n, rows, dim), SPLAT_ERR_CAPACITY, "lookup workspace too small");
+  }
+  return launch_lookup_bwd(d_out, dtype, n <= 1 ? dim : d_out_stride, ids, itype, n, rows, dim, scale, d_table,
+                           rows == 1 ? dim : d_table_stride, accumulate, workspace, stream);
+}
+
+size_t splat_group_norm_workspace_bytes(const splat_norm *norm) {
+  return check_norm(norm, false, false) == SPLAT_OK ? group_norm_workspace_bytes(norm) : 0;
+}
+
+int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, const void *bias, void *y,
+                     float *mean, float *rstd, void *workspace, size_t ws_bytes, hipStream_t stream) {
+  int st = check_norm(norm, false, true);
+  if (st) return st;
+  if (norm->images == 0 || norm->pixels == 0) return SPLAT_OK;
+  CHECK(x && y && mean && rstd, SPLAT_ERR_INVALID_ARG, "NULL array");
+  CHECK(aligned_to(x, norm->dtype) && aligned_to(y, norm->dtype) && aligned_to(weight, norm->param_dtype) &&
+            aligned_to(bias, norm->param_dtype) && aligned_to(mean, SPLAT_F32) && aligned_to(rstd, SPLAT_F32),
+        SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
+  CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+  CHECK(ws_bytes >= group_norm_workspace_bytes(norm), SPLAT_ERR_CAPACITY, "group norm workspace too small");
+  return launch_group_norm(norm, x, weight, bias, y, mean, rstd, workspace, stream);
+}
+
+int splat_group_norm_bwd(const splat_norm *norm, const void *d_y, const void *x, const float *mean,
+                         const float *rstd, const void *weight, const void *bias, void *d_x, void *d_weight,
+                         void *d_bias, void *workspace, size_t ws_bytes, hipStream_t stream) {
+  int st = check_norm(norm, true, d_x != nullptr);
+  if (st) return st;
+  if (norm->images > 0 && norm->pixels > 0) {
+    CHECK(x && d_y && mean && rstd, SPLAT_ERR_INVALID_ARG, "NULL array");
+    CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+    CHECK(ws_bytes >= group_norm_workspace_bytes(norm), SPLAT_ERR_CAPACITY, "group norm workspace too small");
+  }
+  CHECK(aligned_to(x, norm->dtype) && aligned_to(d_y, norm->dtype) && aligned_to(d_x, norm->dtype) &&
+            aligned_to(weight, norm->param_dtype) && aligned_to(bias, norm->param_dtype) &&
+            aligned_to(d_weight, norm->param_dtype) && aligned_to(d_bias, norm->param_dtype) &&
+            aligned_to(mean, SPLAT_F32) && aligned_to(rstd, SPLAT_F32),
+        SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
+  return launch_group_norm_bwd(norm, d_y, x, mean, rstd, weight, bias, d_x, d_weight, d_bias, workspace, stream);
+}
+
+size_t splat_orthogonalize_workspace_bytes(int64_t batch, int rows, int cols) {
+  return ortho_size(batch, rows, cols) ? orthogonalize_workspace_bytes(batch, rows, cols) : 0;
+}
+
+int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int cols, int64_t g_batch_stride,
+                        int64_t g_row_stride, int steps, float a, float b, float c, float eps, float scale,
+                        void *out, int64_t out_batch_stride, int64_t out_row_stride, void *workspace,
+                        size_t ws_bytes, hipStream_t stream) {
+  CHECK(known_dtype(dtype), SPLAT_ERR_INVALID_ARG, "dtype");
+  CHECK(ortho_size(batch, rows, cols), SPLAT_ERR_INVALID_ARG, "matrix size");
+  CHECK(steps >= 1 && steps <= 64, SPLAT_ERR_INVALID_ARG, "steps must be in 1..64");
+  CHECK(isfinite(a) && isfinite(b) && isfinite(c) && isfinite(scale), SPLAT_ERR_INVALID_ARG, "coefficients not finite");
+  CHECK(isfinite(eps) && eps >= 0.0f, SPLAT_ERR_INVALID_ARG, "eps must be >= 0");
+  int st = orthogonalize_bounds(steps, a, b, c);
+  if (st) return fail(st, "coefficients let singular values grow past 1e4");
+  if (batch == 0 || rows == 0 || cols == 0) return SPLAT_OK;
+  CHECK(g && out, SPLAT_ERR_INVALID_ARG, "NULL array");
+  CHECK((rows == 1 || g_row_stride >= cols) && (rows == 1 || out_row_stride >= cols), SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(stride_fits(g_row_stride, rows) && stride_fits(out_row_stride, rows) && stride_fits(g_batch_stride, batch) &&
+            stride_fits(out_batch_stride, batch) && g_batch_stride >= 0 && out_batch_stride >= 0,
+        SPLAT_ERR_INVALID_ARG, "stride");
+  CHECK(aligned_to(g, dtype) && aligned_to(out, dtype), SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
+  CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+  CHECK(ws_bytes >= orthogonalize_workspace_bytes(batch, rows, cols), SPLAT_ERR_CAPACITY, "workspace too small");
+  return launch_orthogonalize(g, dtype, batch, rows, cols, g_batch_stride, g_row_stride, steps, a, b, c, eps, scale,
+                              out, out_batch_stride, out_row_stride, workspace, stream);
 }
 
 const char *splat_status_string(int status) {

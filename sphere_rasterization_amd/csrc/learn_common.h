@@ -1,0 +1,86 @@
+// Helpers shared by the appearance operators (lookup, group norm, orthogonalisation):
+// element types, packed loads and stores, exact division by a launch constant.
+#pragma once
+#include "splat_internal.h"
+
+typedef _Float16 f16_t;
+typedef __bf16 bf16_t;
+
+// N consecutive elements, moved as one access when aligned to their size.
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+  T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ void load_f32(const T *p, float (&o)[N]) {
+  const Pack<T, N> x = *reinterpret_cast<const Pack<T, N> *>(p);
+#pragma unroll
+  for (int i = 0; i < N; i++) o[i] = (float)x.v[i];
+}
+
+// One rounding to the nearest value of the type.
+template <typename T, int N>
+__device__ __forceinline__ void store_f32(T *p, const float (&o)[N]) {
+  Pack<T, N> x;
+#pragma unroll
+  for (int i = 0; i < N; i++) x.v[i] = (T)o[i];
+  *reinterpret_cast<Pack<T, N> *>(p) = x;
+}
+
+// fp32 sums kept in the workspace: 16-byte accesses where N allows.
+template <int N>
+__device__ __forceinline__ void load_sums(const float *p, float (&o)[N]) {
+  if constexpr (N == 8) {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w; o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+  } else {
+    load_f32<float, N>(p, o);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_sums(float *p, const float (&o)[N]) {
+  if constexpr (N == 8) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(o[4], o[5], o[6], o[7]);
+  } else {
+    store_f32<float, N>(p, o);
+  }
+}
+
+// x / d for 0 <= x < 2^31 and a divisor known at launch, as one 64-bit product:
+// with l = ceil(log2 d) and m = floor(2^(31 + l) / d) + 1, m d - 2^(31 + l) lies in
+// (0, 2^l], so floor(x m / 2^(31 + l)) = floor(x / d) for every x < 2^31.
+struct FastDiv {
+  uint32_t d, m, s;
+};
+static inline FastDiv fast_div(uint32_t d) {
+  FastDiv f;
+  uint32_t l = 0;
+  while ((1ull << l) < d) l++;
+  f.d = d;
+  f.s = 31 + l;
+  f.m = (uint32_t)((1ull << f.s) / d + 1);
+  return f;
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t x, const FastDiv &f) {
+  return (uint32_t)(((uint64_t)x * f.m) >> f.s);
+}
+
+static inline int dtype_bytes(int dtype) { return dtype == SPLAT_F32 ? 4 : 2; }
+
+// The widest power-of-two number of elements, at most 16 bytes, by which a row can
+// be walked: it divides the row length, every stride and every pointer's alignment.
+static inline int vec_width(int bytes, int dim, const int64_t *strides, int n_strides, const void *const *ptrs,
+                            int n_ptrs) {
+  int v = 16 / bytes;
+  for (; v > 1; v >>= 1) {
+    bool ok = dim % v == 0;
+    for (int i = 0; ok && i < n_strides; i++) ok = strides[i] % v == 0;
+    for (int i = 0; ok && i < n_ptrs; i++) ok = ((uintptr_t)ptrs[i] % (uintptr_t)(v * bytes)) == 0;
+    if (ok) break;
+  }
+  return v;
+}
+
+static inline size_t ws_align(size_t x) { return (x + 255) & ~(size_t)255; }

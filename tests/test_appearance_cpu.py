@@ -1,0 +1,138 @@
+"""Host checks of the appearance operators (no GPU): size queries, refusals before any
+launch, sizes of zero."""
+import ctypes as C
+import os
+import re
+
+import pytest
+import torch
+
+from sphere_rasterization_amd import _lib as L
+
+P = C.c_void_p(256)          # an aligned address that no refused call may touch
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _norm(**kw):
+    d = L.splat_norm()
+    d.dtype, d.param_dtype, d.act, d.channels, d.groups, d.eps = 0, 0, 0, 8, 2, 1e-5
+    d.images, d.pixels = 2, 16
+    for k in ("x", "y", "dx"):
+        setattr(d, k + "_image_stride", 128)
+        setattr(d, k + "_pixel_stride", 8)
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def test_enums_match_the_header():
+    src = open(os.path.join(ROOT, "include", "splat.h")).read()
+    for name in ("SPLAT_F32", "SPLAT_F16", "SPLAT_BF16", "SPLAT_I32", "SPLAT_I64", "SPLAT_ACT_NONE", "SPLAT_ACT_RELU",
+                 "SPLAT_ACT_SILU", "SPLAT_ACT_GELU"):
+        assert int(re.search(name + r" = (\d+)", src).group(1)) == getattr(L, name)
+
+
+def test_size_queries():
+    n, rows, dim = 100_000, 5000, 32
+    need = L.splat_lookup_bwd_workspace_bytes(n, rows, dim)
+    assert need >= 16 * n + 8 * rows + 4 * dim * (n // 64)
+    assert L.splat_lookup_bwd_workspace_bytes(-1, rows, dim) == 0
+    assert L.splat_group_norm_workspace_bytes(_norm()) >= 2 * 2 * 8
+    assert L.splat_group_norm_workspace_bytes(_norm(groups=3)) == 0
+    assert L.splat_orthogonalize_workspace_bytes(2, 100, 300) >= 2 * 100 * 300 * 4 * 2
+    assert L.splat_orthogonalize_workspace_bytes(1, 100_000, 3) == 0
+
+
+@pytest.mark.parametrize("change", [
+    dict(dtype=7), dict(itype=2), dict(rows=-1), dict(n=-1), dict(n=1 << 31), dict(dim=70000), dict(scale=float("nan")),
+    dict(table=None), dict(ids=None), dict(out=None), dict(ldt=7), dict(ldo=7), dict(ldt=-8), dict(ldt=1 << 61),
+    dict(table=C.c_void_p(258)), dict(ids=C.c_void_p(260))])
+def test_lookup_refusals(change):
+    a = dict(table=P, dtype=0, rows=100, dim=8, ldt=8, ids=P, itype=1, n=10, scale=1.0, out=P, ldo=8)
+    a.update(change)
+    assert L.lib().splat_lookup(*a.values(), None) == L.SPLAT_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dtype=3), -1), (dict(itype=-1), -1), (dict(n=1 << 31), -1), (dict(rows=(1 << 31) - 1), -1),
+    (dict(scale=float("inf")), -1), (dict(accumulate=2), -1), (dict(d_out=None), -1), (dict(ids=None), -1),
+    (dict(d_table=None), -1), (dict(ldy=7), -1), (dict(ldg=7), -1), (dict(ws=None), -1), (dict(ws=C.c_void_p(264)), -1),
+    (dict(nbytes=100), -2)])
+def test_lookup_bwd_refusals(change, code):
+    a = dict(d_out=P, dtype=0, ldy=8, ids=P, itype=0, n=10, rows=100, dim=8, scale=1.0, d_table=P, ldg=8, accumulate=0,
+             ws=P, nbytes=1 << 30)
+    a.update(change)
+    assert L.lib().splat_lookup_bwd(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("change", [
+    dict(dtype=3), dict(param_dtype=1), dict(act=4), dict(channels=0), dict(groups=0), dict(groups=3), dict(eps=-1.0),
+    dict(eps=float("nan")), dict(images=-1), dict(pixels=-1), dict(images=1 << 30, pixels=1 << 30),
+    dict(x_pixel_stride=-8), dict(x_image_stride=1 << 60), dict(y_pixel_stride=7), dict(y_image_stride=0)])
+def test_group_norm_descriptor_refusals(change):
+    d = _norm(**change)
+    assert L.lib().splat_group_norm(C.byref(d), P, P, P, P, P, P, P, 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
+    if not any(k.startswith("y_") for k in change):
+        assert L.lib().splat_group_norm_bwd(C.byref(d), P, P, P, P, P, P, P, P, P, P, 1 << 30,
+                                            None) == L.SPLAT_ERR_INVALID_ARG
+
+
+def test_group_norm_pointer_refusals():
+    f, b, d = L.lib().splat_group_norm, L.lib().splat_group_norm_bwd, _norm()
+    bad = [P] * 7
+    for k in (0, 3, 4, 5, 6):                # x, y, mean, rstd, workspace
+        args = list(bad)
+        args[k] = None
+        assert f(C.byref(d), *args, 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
+    assert f(C.byref(d), *bad, 8, None) == L.SPLAT_ERR_CAPACITY
+    assert f(C.byref(d), C.c_void_p(258), *bad[1:], 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
+    for k in (0, 1, 2, 3, 9):                # d_y, x, mean, rstd, workspace
+        args = [P] * 10
+        args[k] = None
+        assert b(C.byref(d), *args, 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
+    assert b(C.byref(d), *[P] * 10, 8, None) == L.SPLAT_ERR_CAPACITY
+    overlap = _norm(dx_pixel_stride=4)
+    assert b(C.byref(overlap), *[P] * 10, 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
+    # nothing asked for: nothing done
+    assert b(C.byref(d), P, P, P, P, P, P, None, None, None, P, 1 << 30, None) == L.SPLAT_OK
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(dtype=3), -1), (dict(batch=-1), -1), (dict(batch=65536), -1), (dict(rows=70000), -1), (dict(cols=-1), -1),
+    (dict(steps=0), -1), (dict(steps=65), -1), (dict(a=float("nan")), -1), (dict(eps=-1e-7), -1),
+    (dict(scale=float("inf")), -1), (dict(a=20.0), -4), (dict(g=None), -1), (dict(out=None), -1), (dict(gr=9), -1),
+    (dict(orow=9), -1), (dict(gb=-1), -1), (dict(ws=None), -1), (dict(nbytes=64), -2)])
+def test_orthogonalize_refusals(change, code):
+    a = dict(g=P, dtype=0, batch=2, rows=8, cols=10, gb=80, gr=10, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7,
+             scale=1.0, out=P, ob=80, orow=10, ws=P, nbytes=1 << 30)
+    a.update(change)
+    assert L.lib().splat_orthogonalize(*a.values(), None) == code
+
+
+def test_sizes_of_zero_touch_nothing():
+    lib = L.lib()
+    assert lib.splat_lookup(None, 0, 0, 8, 8, None, 0, 0, 1.0, None, 8, None) == L.SPLAT_OK
+    assert lib.splat_lookup_bwd(None, 0, 8, None, 0, 0, 0, 8, 1.0, None, 8, 0, None, 0, None) == L.SPLAT_OK
+    assert lib.splat_lookup_bwd(P, 0, 8, P, 0, 0, 4, 8, 1.0, P, 8, 1, None, 0, None) == L.SPLAT_OK
+    d = _norm(images=0)
+    assert lib.splat_group_norm(C.byref(d), None, None, None, None, None, None, None, 0, None) == L.SPLAT_OK
+    assert lib.splat_orthogonalize(None, 0, 0, 8, 8, 64, 8, 5, 3.4445, -4.775, 2.0315, 1e-7, 1.0, None, 64, 8, None, 0,
+                                   None) == L.SPLAT_OK
+
+
+def test_python_refusals_without_a_gpu():
+    from sphere_rasterization_amd import appearance as A
+    t = torch.zeros(4, 8)
+    ids = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        A.lookup(t, ids)
+    with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
+        A.lookup(t.double(), ids)
+    with pytest.raises(ValueError, match="rows, dim"):
+        A.lookup(t[0], ids)
+    with pytest.raises(ValueError, match="act"):
+        A.group_norm(t, 2, act="tanh")
+    with pytest.raises(ValueError, match="images"):
+        A.group_norm(t[0], 2)
+    with pytest.raises(ValueError, match="rows, cols"):
+        A.orthogonalize(t[0])
