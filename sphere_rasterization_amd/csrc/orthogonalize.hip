@@ -18,10 +18,10 @@
 // 2^-23 of the product. Three fp16 products still run several times faster than one
 // in fp32, whose matrix rate on gfx950 is 1/16 of fp16's.
 //
-// Layout. A factor is stored by rows along the summed axis in blocks of 32 values:
-// 32 hi then 32 lo, 128 bytes, one cache line per row and block, so that a tile's
-// step is whole lines and the two parts travel together. X is kept both by rows and
-// transposed, because X X^T sums over columns and B X over rows.
+// Layout. A factor is stored in panels of 64 rows, a panel in blocks of 16 values of the
+// summed axis, and in a block each row's 16 hi then 16 lo parts: 64 bytes. So a block is
+// a contiguous 4 KB, loaded straight into LDS, and the two parts travel together. X is
+// kept both by rows and transposed, because X X^T sums over columns and B X over rows.
 #include <math.h>
 
 #include "learn_common.h"
@@ -32,11 +32,10 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
-constexpr int KB = 32;                 // values per block of the summed axis
-constexpr int PAD = 128;               // matrices are padded to multiples of the tile
-constexpr int TM = 128, TN = 128;      // tile of one workgroup: four waves of 64 x 64
+constexpr int KB = 16;                 // values per block of the summed axis
+constexpr int BLOCK = 64 * 2 * KB;     // halves per block of a panel
 constexpr int OR_THREADS = 256;
-constexpr int NORM_BLOCKS = 256;
+constexpr int NORM_BLOCKS = 1024;
 
 enum { EPI_GRAM, EPI_POLY, EPI_NEXT, EPI_LAST };
 
@@ -45,7 +44,9 @@ struct OrthoArgs {
   void *out;
   int64_t gb, gr, ob, orow;            // batch and row strides of the input and the output
   int dtype, rows, cols, tall;
-  int m, n, mp, np;                    // m <= n and their padded sizes
+  int m, n, mp, np;                    // m <= n, and padded to multiples of the tile
+  int tile;
+  float *part;                         // sums of shared-out products
   double *norms;                       // [batch][NORM_BLOCKS] partial sums of squares
   _Float16 *x, *y, *y2, *a, *b;        // packed factors: X, X^T (two), A, B; per matrix strides below
   int64_t sx, sa;                      // halves per matrix of x / y, and of a / b
@@ -56,7 +57,11 @@ struct GemmArgs {
   const _Float16 *p, *q;               // factors by rows [I][K], [J][K], packed
   int64_t pb, qb;                      // halves per matrix
   int K;                               // padded length of the summed axis
-  int ti, tj;                          // tiles per side
+  int ti;                              // tiles along I
+  int tiles;                           // tiles per matrix
+  // shared-out products: the sums of piece (run w, tile t) lie at part[w + t]
+  float *part;
+  int64_t units;                       // double steps of all tiles of all matrices
   float mul;                           // product of the stored sums to the stored result's scale
   // EPI_POLY: result = ca I + cb A + mul acc with A read from `a` (stored scale folded in)
   const _Float16 *a;
@@ -81,20 +86,31 @@ __device__ __forceinline__ void write_from_f32(void *p, int64_t i, int dtype, fl
   else ((bf16_t *)p)[i] = (bf16_t)v;
 }
 
-// Place of value k in a packed row: block k / 32, hi part first.
-__device__ __forceinline__ int packed(int k) { return (k >> 5) * (2 * KB) + (k & 31); }
+// Place of the hi part of value k of row r, for rows of K values; lo lies KB further.
+__device__ __forceinline__ int64_t packed(int r, int k, int K) {
+  return ((int64_t)(r >> 6) * (K / KB) + k / KB) * BLOCK + (r & 63) * (2 * KB) + k % KB;
+}
 
 // Sums of squares in fp64: no square over- or underflows and the norm is exact to fp32.
+// Rows in turn; a thread has 8 independent loads in flight.
 __global__ __launch_bounds__(OR_THREADS) void k_ortho_norm(OrthoArgs o) {
   __shared__ double s[OR_THREADS / WAVE];
   const int64_t mat = blockIdx.y;
   const char *g = (const char *)o.g + mat * o.gb * (o.dtype == SPLAT_F32 ? 4 : 2);
   double t = 0.0;
-  for (int r = blockIdx.x; r < o.rows; r += gridDim.x)
-    for (int c = threadIdx.x; c < o.cols; c += OR_THREADS) {
-      const double v = (double)read_as_f32(g, r * o.gr + c, o.dtype);
-      t = __builtin_fma(v, v, t);
+  const int64_t per = 8 * OR_THREADS;                     // values of a row per piece
+  const int64_t pieces = (o.cols + per - 1) / per;
+  for (int64_t i = blockIdx.x; i < pieces * o.rows; i += gridDim.x) {
+    const int64_t r = i / pieces, c0 = (i - r * pieces) * per + threadIdx.x;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const int64_t c = c0 + k * OR_THREADS;
+      v[k] = c < o.cols ? read_as_f32(g, r * o.gr + c, o.dtype) : 0.0f;
     }
+#pragma unroll
+    for (int k = 0; k < 8; k++) t = __builtin_fma((double)v[k], (double)v[k], t);
+  }
   t = wave_sum_f64(t);
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = t;
   __syncthreads();
@@ -108,7 +124,7 @@ __global__ __launch_bounds__(OR_THREADS) void k_ortho_pack(OrthoArgs o, int norm
   __shared__ double s[OR_THREADS / WAVE];
   const int64_t mat = blockIdx.z;
   double q = 0.0;
-  if ((int)threadIdx.x < norm_blocks) q = o.norms[mat * NORM_BLOCKS + threadIdx.x];
+  for (int k = threadIdx.x; k < norm_blocks; k += OR_THREADS) q += o.norms[mat * NORM_BLOCKS + k];
   q = wave_sum_f64(q);
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = q;
   __syncthreads();
@@ -124,7 +140,7 @@ __global__ __launch_bounds__(OR_THREADS) void k_ortho_pack(OrthoArgs o, int norm
     const float v = r < o.rows && c < o.cols ? read_as_f32(g, r * o.gr + c, o.dtype) * inv : 0.0f;
     t[ty + k][tx] = v;
     const _Float16 hi = (_Float16)v;
-    _Float16 *d = direct + (int64_t)r * 2 * dlen + packed(c);
+    _Float16 *d = direct + packed(r, c, dlen);
     d[0] = hi;
     d[KB] = (_Float16)(v - (float)hi);
   }
@@ -134,136 +150,326 @@ __global__ __launch_bounds__(OR_THREADS) void k_ortho_pack(OrthoArgs o, int norm
     const int r = r0 + tx, c = c0 + ty + k;
     const float v = t[tx][ty + k];
     const _Float16 hi = (_Float16)v;
-    _Float16 *d = cross + (int64_t)c * 2 * clen + packed(r);
+    _Float16 *d = cross + packed(c, r, clen);
     d[0] = hi;
     d[KB] = (_Float16)(v - (float)hi);
   }
 }
 
-// One 128 x 128 tile of D = P Q^T. A step of 32 along K brings 256 rows of 128 bytes
-// into LDS; the 16-byte chunk c of row r lies at c ^ (r & 7), so that the eight rows a
-// fragment read touches at a time fall on different banks.
-template <int EPI>
+// TL x TL tile (it, jt) of D = P Q^T, steps [k0, k1) of the summed axis, by four waves, a
+// quarter each. A stage holds SUB blocks of the tile's rows of P and Q; NST stages form a
+// ring in LDS, filled by loads that go straight there. In step k, after the wait for
+// stage k + 1 and a barrier, stage k (already in registers) is free for stage k + NST,
+// the fragments of stage k + 1 are read, and those of stage k are multiplied: loads have
+// NST - 1 steps to arrive, and fragment reads a step.
+//
+// In a block the 16-byte chunk c of row r lies at c ^ ((r >> 2) & 3): a fragment read
+// serves 16 rows in a cycle from 64 banks, four rows to a line of banks, and so meets no
+// bank twice (with an exchange by r & 3 the bank conflict counter shows twice the cycles).
+template <int TL, int SUB, int NST>
+struct Tile {
+  static constexpr int F = TL / 64;                  // 32 x 32 fragments per side of a wave's quarter, and panels
+  static constexpr int LOADS = SUB * 2 * F;          // loads per thread and stage, 16 bytes each
+  static constexpr int BLK = BLOCK / 8;              // 16-byte chunks per block
+  static constexpr int RING = NST * SUB * 2 * F * BLK;
+  static constexpr int PATCH = F * 2 * (32 * 40 + 16) / 8;   // 16-byte chunks of a wave's patch in the epilogue
+  static constexpr int LDS = RING > 4 * PATCH ? RING : 4 * PATCH;
+
+  static __device__ __forceinline__ void product(const _Float16 *p0, const _Float16 *q0, int K, int it, int jt,
+                                                 int k0, int k1, half8 *lds, float16v (&acc)[F][F]) {
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = (w & 1) * (TL / 2), wj = (w >> 1) * (TL / 2);
+    const int64_t panel = (int64_t)(K / KB) * BLOCK;
+    // chunk tid of a block, in the order in which LDS holds them
+    const int src = ((tid >> 2) * 4 + ((tid & 3) ^ ((tid >> 4) & 3))) * 8;
+    const _Float16 *p = p0 + (int64_t)it * F * panel + src, *q = q0 + (int64_t)jt * F * panel + src;
+    typedef const __attribute__((address_space(1))) void *gptr;
+    typedef __attribute__((address_space(3))) void *lptr;
+    // stages past the end load the last one again, so that the count of loads in flight
+    // stays a constant
+    auto fetch = [&](int k, int slot) {
+      const int64_t at = (int64_t)(k < k1 ? k : k1 - 1) * (SUB * BLOCK);
+#pragma unroll
+      for (int u = 0; u < SUB; u++)
+#pragma unroll
+        for (int f = 0; f < F; f++) {
+          half8 *d = &lds[(slot * SUB + u) * (2 * F * BLK) + f * BLK + w * 64];
+          __builtin_amdgcn_global_load_lds((gptr)(p + at + u * BLOCK + f * panel), (lptr)d, 16, 0, 0);
+          __builtin_amdgcn_global_load_lds((gptr)(q + at + u * BLOCK + f * panel), (lptr)(d + F * BLK), 16, 0, 0);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < F; i++)
+#pragma unroll
+      for (int j = 0; j < F; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+    const int fr = lane & 31, fk = lane >> 5;
+    // a fragment's chunk: row fr of its 32, hi chunk fk, lo chunk fk + 2
+    const int sw = (fr >> 2) & 3, hi_at = fr * 4 + (fk ^ sw), lo_at = fr * 4 + ((fk + 2) ^ sw);
+    half8 ph[2][SUB][F], pl[2][SUB][F], qh[2][SUB][F], ql[2][SUB][F];
+    auto read = [&](int slot, int set) {
+#pragma unroll
+      for (int u = 0; u < SUB; u++) {
+        const half8 *l = &lds[(slot * SUB + u) * (2 * F * BLK)];
+#pragma unroll
+        for (int i = 0; i < F; i++) {
+          const half8 *a = l + (wi + i * 32) * 4, *b = l + F * BLK + (wj + i * 32) * 4;
+          pl[set][u][i] = a[lo_at];
+          qh[set][u][i] = b[hi_at];
+          ph[set][u][i] = a[hi_at];
+          ql[set][u][i] = b[lo_at];
+        }
+      }
+    };
+    auto multiply = [&](int set) {
+#pragma unroll
+      for (int u = 0; u < SUB; u++) {
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+          for (int j = 0; j < F; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[set][u][i], qh[set][u][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+          for (int j = 0; j < F; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[set][u][i], ql[set][u][j], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+          for (int j = 0; j < F; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[set][u][i], qh[set][u][j], acc[i][j], 0, 0, 0);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < NST; k++) fetch(k0 + k, k);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NST - 1) * LOADS) : "memory");
+    read(0, 0);
+    int slot = 0;                                    // of stage k
+    auto step = [&](int k, int set) {
+      const int next = slot + 1 == NST ? 0 : slot + 1;
+      // the oldest stage in flight is in LDS for this wave and its own fragment reads
+      // are done (seen by the compiler's own count), then the same of the other waves
+      __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0)
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NST - 2) * LOADS) : "memory");
+      fetch(k + NST, slot);
+      read(next, set ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(set);
+      __builtin_amdgcn_sched_barrier(0);
+      slot = next;
+    };
+    for (int k = k0; k < k1; k += 2) {               // an even number of steps
+      step(k, 0);
+      step(k + 1, 1);
+    }
+    // nothing may land in LDS after this
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+
+  // Writes row i of fragments of a wave's quarter. A lane holds column fr and rows 8 (e / 4) + 4 fk +
+  // e % 4 of each fragment. Packed results go through LDS by patches of 32 rows of the
+  // wave's quarter, rows padded to 40 halves, so that memory sees whole 16-byte chunks of
+  // consecutive rows.
+  template <int EPI>
+  static __device__ __forceinline__ void finish(const GemmArgs &g, int64_t mat, int it, int jt, int w,
+                                                int i, _Float16 *patch, const float16v (&acc)[F]) {
+    const int lane = threadIdx.x & 63, fr = lane & 31, fk = lane >> 5;
+    const int wi = (w & 1) * (TL / 2), wj = (w >> 1) * (TL / 2);
+    const int I = it * TL + wi + i * 32, Jw = jt * TL + wj;
+    half4 hi[F][4], lo[F][4];
+#pragma unroll
+    for (int j = 0; j < F; j++) {
+      const int J = Jw + j * 32 + fr;
+#pragma unroll
+      for (int e4 = 0; e4 < 4; e4++) {
+        const int I0 = I + e4 * 8 + fk * 4;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          float v = acc[j][e4 * 4 + e] * g.mul;
+          if constexpr (EPI == EPI_POLY) {
+            const _Float16 *a = g.a + mat * g.db + packed(I0 + e, J, g.ld0);
+            v = __builtin_fmaf(g.cb, (float)a[0] + (float)a[KB], v);
+            if (I0 + e == J) v += g.ca;
+          }
+          if constexpr (EPI == EPI_LAST) {
+            if (I0 + e < g.m && J < g.n)
+              write_from_f32(g.out, mat * g.ob + (g.tall ? J * g.orow + I0 + e : (I0 + e) * g.orow + J), g.dtype, v);
+          } else {
+            hi[j][e4][e] = (_Float16)v;
+            lo[j][e4][e] = (_Float16)(v - (float)hi[j][e4][e]);
+          }
+        }
+      }
+    }
+    if constexpr (EPI != EPI_LAST) {
+      // by rows: 2 F blocks of 32 rows
+      constexpr int B0 = 32 * 40 + 16, B1 = F * 32 * 40 + 16;
+#pragma unroll
+      for (int j = 0; j < F; j++)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; e4++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            _Float16 *d = patch + (j * 2 + (fr >> 4)) * B0 + (e4 * 8 + fk * 4 + e) * 40 + (fr & 15);
+            d[0] = hi[j][e4][e];
+            d[KB] = lo[j][e4][e];
+          }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < F * 4; u++) {
+        const int c = u * 64 + lane, blk = c >> 7, r = (c >> 2) & 31, k = c & 3;
+        const half8 v = *reinterpret_cast<const half8 *>(patch + blk * B0 + r * 40 + k * 8);
+        *reinterpret_cast<half8 *>(g.d0 + mat * g.db + packed(I + r, Jw + blk * KB, g.ld0) + k * 8) = v;
+      }
+      // transposed (of a symmetric result: the tile above the diagonal): 2 blocks of 32 F rows
+      if (EPI == EPI_NEXT || it != jt) {
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int j = 0; j < F; j++)
+#pragma unroll
+          for (int e4 = 0; e4 < 4; e4++) {
+            _Float16 *d = patch + (e4 >> 1) * B1 + (j * 32 + fr) * 40 + (e4 & 1) * 8 + fk * 4;
+            *reinterpret_cast<half4 *>(d) = hi[j][e4];
+            *reinterpret_cast<half4 *>(d + KB) = lo[j][e4];
+          }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int u = 0; u < F * 4; u++) {
+          const int c = u * 64 + lane, blk = c / (F * 128), r = (c >> 2) % (F * 32), k = c & 3;
+          const half8 v = *reinterpret_cast<const half8 *>(patch + blk * B1 + r * 40 + k * 8);
+          *reinterpret_cast<half8 *>(g.d1 + mat * g.db + packed(Jw + r, I + blk * KB, g.ld1) + k * 8) = v;
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
+};
+
+// Tile t of the lower triangle, by rows.
+__device__ __forceinline__ void lower_tile(int t, int &it, int &jt) {
+  it = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+  while ((it + 1) * (it + 2) / 2 <= t) it++;
+  while (it * (it + 1) / 2 > t) it--;
+  jt = t - it * (it + 1) / 2;
+}
+
+// Workgroups go to the eight XCDs in turn. Work item of workgroup b out of n such that
+// each XCD takes a run of neighbouring items, whose panels its own L2 then holds.
+__device__ __forceinline__ int by_xcd(int b, int n) {
+  const int x = b & 7, each = n >> 3, more = n & 7;
+  return x * each + (x < more ? x : more) + (b >> 3);
+}
+
+// A whole tile per workgroup.
+template <int EPI, int TL, int SUB, int NST>
 __global__ __launch_bounds__(OR_THREADS, 2) void k_ortho_gemm(GemmArgs g) {
-  __shared__ half8 lds[2][(TM + TN) * 8];
+  typedef Tile<TL, SUB, NST> Tl;
+  __shared__ half8 lds[Tl::LDS];
   const int64_t mat = blockIdx.y;
   int it, jt;
   if constexpr (EPI == EPI_GRAM || EPI == EPI_POLY) {
-    // tile t of the lower triangle
-    const int t = blockIdx.x;
-    it = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-    while ((it + 1) * (it + 2) / 2 <= t) it++;
-    while (it * (it + 1) / 2 > t) it--;
-    jt = t - it * (it + 1) / 2;
+    lower_tile(blockIdx.x, it, jt);
   } else {
     it = blockIdx.x % g.ti;
     jt = blockIdx.x / g.ti;
   }
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int wi = (w & 1) * 64, wj = (w >> 1) * 64;
-  // this thread's chunks of a step: rows r0 + 32 k, chunk tid & 7
-  const int lr = tid >> 3, lc = tid & 7;
-  const int64_t row = 2 * (int64_t)g.K;
-  const _Float16 *p = g.p + mat * g.pb + ((int64_t)it * TM + lr) * row + lc * 8;
-  const _Float16 *q = g.q + mat * g.qb + ((int64_t)jt * TN + lr) * row + lc * 8;
-  half8 st[8];
-  auto fetch = [&](int k) {
+  float16v acc[Tl::F][Tl::F];
+  Tl::product(g.p + mat * g.pb, g.q + mat * g.qb, g.K, it, jt, 0, g.K / (KB * SUB), lds, acc);
+  const int w = threadIdx.x >> 6;
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-      st[u] = *reinterpret_cast<const half8 *>(p + (int64_t)u * 32 * row + k * (2 * KB));
-      st[4 + u] = *reinterpret_cast<const half8 *>(q + (int64_t)u * 32 * row + k * (2 * KB));
-    }
-  };
-  auto stage = [&](int buf) {
+  for (int i = 0; i < Tl::F; i++)
+    Tl::template finish<EPI>(g, mat, it, jt, w, i, reinterpret_cast<_Float16 *>(lds + w * Tl::PATCH), acc[i]);
+}
+
+// Symmetric products with too few tiles to fill the chip evenly: the steps of all tiles,
+// laid end to end, are cut into equal runs, one per workgroup, and a second kernel adds
+// the pieces of each tile in order.
+template <int TL, int SUB, int NST>
+__global__ __launch_bounds__(OR_THREADS, 2) void k_ortho_pieces(GemmArgs g) {
+  typedef Tile<TL, SUB, NST> Tl;
+  __shared__ half8 lds[Tl::LDS];
+  const int per = g.K / (KB * SUB) / 2;              // double steps per tile
+  const int run = by_xcd(blockIdx.x, gridDim.x);
+  int64_t u = g.units * run / gridDim.x;
+  const int64_t end = g.units * (run + 1) / gridDim.x;
+  while (u < end) {
+    const int t = (int)(u / per), from = (int)(u - (int64_t)t * per);
+    const int to = end - u < per - from ? from + (int)(end - u) : per;
+    const int64_t mat = t / g.tiles;
+    int it, jt;
+    lower_tile((int)(t - mat * g.tiles), it, jt);
+    float16v acc[Tl::F][Tl::F];
+    Tl::product(g.p + mat * g.pb, g.q + mat * g.qb, g.K, it, jt, 2 * from, 2 * to, lds, acc);
+    float4 *o = reinterpret_cast<float4 *>(g.part + ((int64_t)run + t) * TL * TL) + threadIdx.x;
 #pragma unroll
-    for (int u = 0; u < 8; u++) {
-      const int r = lr + u * 32;
-      lds[buf][r * 8 + (lc ^ (r & 7))] = st[u];
-    }
-  };
-  float16v acc[2][2];
+    for (int i = 0; i < Tl::F; i++)
 #pragma unroll
-  for (int i = 0; i < 2; i++)
+      for (int j = 0; j < Tl::F; j++)
 #pragma unroll
-    for (int j = 0; j < 2; j++)
-#pragma unroll
-      for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
-  const int steps = g.K / KB;
-  const int fr = lane & 31, fk = lane >> 5;
-  fetch(0);
-  stage(0);
-  __syncthreads();
-  for (int k = 0; k < steps; k++) {
-    if (k + 1 < steps) fetch(k + 1);
-    const half8 *l = lds[k & 1];
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      half8 ph[2], pl[2], qh[2], ql[2];
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int r = wi + i * 32 + fr, c = h * 2 + fk;
-        ph[i] = l[r * 8 + (c ^ (r & 7))];
-        pl[i] = l[r * 8 + ((c + 4) ^ (r & 7))];
-        const int s = TM + wj + i * 32 + fr;
-        qh[i] = l[s * 8 + (c ^ (s & 7))];
-        ql[i] = l[s * 8 + ((c + 4) ^ (s & 7))];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[i], qh[j], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], ql[j], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[i], qh[j], acc[i][j], 0, 0, 0);
-        }
-    }
-    if (k + 1 < steps) stage((k + 1) & 1);
-    __syncthreads();
+        for (int e = 0; e < 4; e++)
+          o[((i * Tl::F + j) * 4 + e) * OR_THREADS] =
+              make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
+    u += to - from;
   }
-  // a lane holds column fr and rows 8 (e / 4) + 4 (lane / 32) + e % 4 of each 32 x 32
+}
+
+// A workgroup per row of fragments of a tile's quarter: each wave adds every fourth piece,
+// first to last, and the first wave adds the four sums and writes the result.
+template <int EPI, int TL, int SUB, int NST>
+__global__ __launch_bounds__(OR_THREADS) void k_ortho_join(GemmArgs g, int groups) {
+  typedef Tile<TL, SUB, NST> Tl;
+  constexpr int F = Tl::F;
+  __shared__ float4 sums[3][F * 4][WAVE];
+  __shared__ half8 lds[Tl::PATCH];
+  const int per = g.K / (KB * SUB) / 2;
+  const int i = blockIdx.x % F, w = blockIdx.x / F & 3, t = blockIdx.x / (F * 4);
+  const int64_t mat = t / g.tiles;
+  int it, jt;
+  lower_tile((int)(t - mat * g.tiles), it, jt);
+  // the first and the last run [units r / groups, units (r + 1) / groups) that meets the
+  // tile's [t per, (t + 1) per)
+  const int64_t lo = (int64_t)t * per, hi = lo + per;
+  int first = (int)(lo * groups / g.units), last = (int)((hi - 1) * groups / g.units);
+  while (g.units * (first + 1) / groups <= lo) first++;
+  while (g.units * (last + 1) / groups < hi) last++;
+  const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;
+  float4 a[F * 4];
 #pragma unroll
-  for (int i = 0; i < 2; i++)
+  for (int e = 0; e < F * 4; e++) a[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int r = first + part; r <= last; r += 4) {
+    const float4 *o = reinterpret_cast<const float4 *>(g.part + ((int64_t)r + t) * TL * TL) +
+                      i * F * 4 * OR_THREADS + w * WAVE + lane;
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-      const int J = jt * TN + wj + j * 32 + fr;
-#pragma unroll
-      for (int e4 = 0; e4 < 4; e4++) {
-        const int I0 = it * TM + wi + i * 32 + e4 * 8 + fk * 4;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) v[e] = acc[i][j][e4 * 4 + e] * g.mul;
-        if constexpr (EPI == EPI_POLY) {
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const _Float16 *a = g.a + mat * g.db + (int64_t)(I0 + e) * 2 * g.ld0 + packed(J);
-            v[e] = __builtin_fmaf(g.cb, (float)a[0] + (float)a[KB], v[e]);
-            if (I0 + e == J) v[e] += g.ca;
-          }
-        }
-        if constexpr (EPI == EPI_LAST) {
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            if (I0 + e < g.m && J < g.n)
-              write_from_f32(g.out, mat * g.ob + (g.tall ? J * g.orow + I0 + e : (I0 + e) * g.orow + J), g.dtype, v[e]);
-        } else {
-          half4 hi, lo;
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            hi[e] = (_Float16)v[e];
-            lo[e] = (_Float16)(v[e] - (float)hi[e]);
-            _Float16 *d = g.d0 + mat * g.db + (int64_t)(I0 + e) * 2 * g.ld0 + packed(J);
-            d[0] = hi[e];
-            d[KB] = lo[e];
-          }
-          // the transposed image (of a symmetric result: the tile above the diagonal)
-          if (EPI == EPI_NEXT || it != jt) {
-            _Float16 *d = g.d1 + mat * g.db + (int64_t)J * 2 * g.ld1 + packed(I0);
-            *reinterpret_cast<half4 *>(d) = hi;
-            *reinterpret_cast<half4 *>(d + KB) = lo;
-          }
-        }
-      }
+    for (int e = 0; e < F * 4; e++) {
+      const float4 x = o[e * OR_THREADS];
+      a[e].x += x.x; a[e].y += x.y; a[e].z += x.z; a[e].w += x.w;
     }
+  }
+  if (part > 0) {
+#pragma unroll
+    for (int e = 0; e < F * 4; e++) sums[part - 1][e][lane] = a[e];
+  }
+  __syncthreads();
+  if (part > 0) return;
+  float16v acc[F];
+#pragma unroll
+  for (int j = 0; j < F; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      float4 x = a[j * 4 + e];
+#pragma unroll
+      for (int k = 0; k < 3; k++) {
+        const float4 y = sums[k][j * 4 + e][lane];
+        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+      }
+      acc[j][4 * e] = x.x;
+      acc[j][4 * e + 1] = x.y;
+      acc[j][4 * e + 2] = x.z;
+      acc[j][4 * e + 3] = x.w;
+    }
+  Tl::template finish<EPI>(g, mat, it, jt, w, i, reinterpret_cast<_Float16 *>(lds), acc);
 }
 
 // ---- host -----------------------------------------------------------------------------
@@ -304,6 +510,13 @@ int scale_exp(double bound) {
 
 int round_up(int x, int k) { return (x + k - 1) / k * k; }
 
+constexpr int GROUPS = 512;               // workgroups that the chip holds at once, two per CU
+
+int64_t lower_tiles(int len, int tl) { return (int64_t)(len / tl) * (len / tl + 1) / 2; }
+
+// Whether a symmetric product's tiles are shared out over all workgroups.
+bool share_out(int64_t tiles, int tl, int K) { return tiles < GROUPS && K >= (tl == 128 ? 512 : 2048); }
+
 OrthoArgs ortho_layout(void *base, int64_t batch, int rows, int cols, size_t *bytes) {
   OrthoArgs o = {};
   o.rows = rows;
@@ -311,8 +524,11 @@ OrthoArgs ortho_layout(void *base, int64_t batch, int rows, int cols, size_t *by
   o.tall = rows > cols;
   o.m = o.tall ? cols : rows;
   o.n = o.tall ? rows : cols;
-  o.mp = round_up(o.m, PAD);
-  o.np = round_up(o.n, PAD);
+  // 128 x 128 tiles move half the bytes per product of 64 x 64 ones, which serve where
+  // they would leave CUs without work
+  o.tile = (int64_t)(round_up(o.m, 128) / 128) * (round_up(o.n, 128) / 128) * batch >= GROUPS ? 128 : 64;
+  o.mp = round_up(o.m, o.tile);
+  o.np = round_up(o.n, o.tile);
   o.sx = 2 * (int64_t)o.mp * o.np;
   o.sa = 2 * (int64_t)o.mp * o.mp;
   char *p = (char *)base;
@@ -327,8 +543,42 @@ OrthoArgs ortho_layout(void *base, int64_t batch, int rows, int cols, size_t *by
   o.y2 = (_Float16 *)take(2 * (size_t)o.sx * batch);
   o.a = (_Float16 *)take(2 * (size_t)o.sa * batch);
   o.b = (_Float16 *)take(2 * (size_t)o.sa * batch);
+  const int64_t lower = lower_tiles(o.mp, o.tile) * batch;
+  const size_t pieces = share_out(lower, o.tile, o.np) || share_out(lower, o.tile, o.mp) ? (size_t)(lower + GROUPS) : 0;
+  o.part = (float *)take(sizeof(float) * o.tile * o.tile * pieces);
   *bytes = (size_t)(p - (char *)base);
   return o;
+}
+
+// One product over the padded sizes I x J.
+template <int EPI, int TL, int SUB, int NST>
+int run_tiles(GemmArgs q, int I, int J, int64_t batch, hipStream_t stream) {
+  constexpr bool sym = EPI == EPI_GRAM || EPI == EPI_POLY;
+  q.ti = I / TL;
+  const int64_t tiles = sym ? lower_tiles(I, TL) : (int64_t)(I / TL) * (J / TL);
+  if constexpr (sym) {
+    if (share_out(tiles * batch, TL, q.K)) {
+      q.tiles = (int)tiles;
+      q.units = tiles * batch * (q.K / (KB * SUB) / 2);
+      const int64_t most = q.units / 4;              // at least eight steps each
+      const int groups = (int)(most < GROUPS ? most : GROUPS);
+      hipLaunchKernelGGL((k_ortho_pieces<TL, SUB, NST>), dim3(groups), dim3(OR_THREADS), 0, stream, q);
+      SPLAT_LAUNCH_CHECK();
+      hipLaunchKernelGGL((k_ortho_join<EPI, TL, SUB, NST>), dim3((unsigned)(tiles * batch * 4 * (TL / 64))),
+                         dim3(OR_THREADS), 0, stream, q, groups);
+      SPLAT_LAUNCH_CHECK();
+      return SPLAT_OK;
+    }
+  }
+  hipLaunchKernelGGL((k_ortho_gemm<EPI, TL, SUB, NST>), dim3((unsigned)tiles, (unsigned)batch), dim3(OR_THREADS), 0,
+                     stream, q);
+  SPLAT_LAUNCH_CHECK();
+  return SPLAT_OK;
+}
+
+template <int EPI>
+int run_gemm(const GemmArgs &q, int tile, int I, int J, int64_t batch, hipStream_t stream) {
+  return tile == 128 ? run_tiles<EPI, 128, 1, 5>(q, I, J, batch, stream) : run_tiles<EPI, 64, 2, 4>(q, I, J, batch, stream);
 }
 
 }  // namespace
@@ -364,29 +614,29 @@ int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int 
   double u = 1.0;
   int ex = scale_exp(u);
   o.s0 = ldexpf(1.0f, ex);
-  const int nb = rows < NORM_BLOCKS ? rows : NORM_BLOCKS;
+  const int64_t pieces = (int64_t)rows * ((cols + 8 * OR_THREADS - 1) / (8 * OR_THREADS));
+  const int nb = pieces < NORM_BLOCKS ? (int)pieces : NORM_BLOCKS;
   hipLaunchKernelGGL(k_ortho_norm, dim3(nb, (unsigned)batch), dim3(OR_THREADS), 0, stream, o);
   SPLAT_LAUNCH_CHECK();
   const int pr = o.tall ? o.np : o.mp, pc = o.tall ? o.mp : o.np;
   hipLaunchKernelGGL(k_ortho_pack, dim3(pc / 32, pr / 32, (unsigned)batch), dim3(OR_THREADS), 0, stream, o, nb);
   SPLAT_LAUNCH_CHECK();
-  const int tm = o.mp / TM, tn = o.np / TN;
   for (int k = 0; k < steps; k++) {
     const int ea = scale_exp(u * u), eb = scale_exp(sup_quadratic(ca, cb, cc, u * u));
     const double un = sup_quintic(ca, cb, cc, u);
     const int en = scale_exp(un);
     const bool last = k + 1 == steps;
     GemmArgs q = {};
+    q.part = o.part;
     q.p = q.q = o.x;
     q.pb = q.qb = o.sx;
     q.K = o.np;
-    q.ti = q.tj = tm;
     q.mul = ldexpf(1.0f, ea - 2 * ex);
     q.d0 = q.d1 = o.a;
     q.db = o.sa;
     q.ld0 = q.ld1 = o.mp;
-    hipLaunchKernelGGL(k_ortho_gemm<EPI_GRAM>, dim3(tm * (tm + 1) / 2, (unsigned)batch), dim3(OR_THREADS), 0, stream, q);
-    SPLAT_LAUNCH_CHECK();
+    int st = run_gemm<EPI_GRAM>(q, o.tile, o.mp, o.mp, batch, stream);
+    if (st) return st;
     q.p = q.q = o.a;
     q.pb = q.qb = o.sa;
     q.K = o.mp;
@@ -395,13 +645,11 @@ int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int 
     q.ca = ldexpf(ca, eb);
     q.cb = ldexpf(cb, eb - ea);
     q.d0 = q.d1 = o.b;
-    hipLaunchKernelGGL(k_ortho_gemm<EPI_POLY>, dim3(tm * (tm + 1) / 2, (unsigned)batch), dim3(OR_THREADS), 0, stream, q);
-    SPLAT_LAUNCH_CHECK();
+    if ((st = run_gemm<EPI_POLY>(q, o.tile, o.mp, o.mp, batch, stream))) return st;
     q.p = o.b;
     q.q = o.y;
     q.pb = o.sa;
     q.qb = o.sx;
-    q.tj = tn;
     q.mul = last ? ldexpf(scale, -(eb + ex)) : ldexpf(1.0f, en - eb - ex);
     q.d0 = o.x;
     q.d1 = o.y2;
@@ -415,11 +663,8 @@ int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int 
     q.tall = o.tall;
     q.m = o.m;
     q.n = o.n;
-    if (last)
-      hipLaunchKernelGGL(k_ortho_gemm<EPI_LAST>, dim3(tm * tn, (unsigned)batch), dim3(OR_THREADS), 0, stream, q);
-    else
-      hipLaunchKernelGGL(k_ortho_gemm<EPI_NEXT>, dim3(tm * tn, (unsigned)batch), dim3(OR_THREADS), 0, stream, q);
-    SPLAT_LAUNCH_CHECK();
+    st = last ? run_gemm<EPI_LAST>(q, o.tile, o.mp, o.np, batch, stream) : run_gemm<EPI_NEXT>(q, o.tile, o.mp, o.np, batch, stream);
+    if (st) return st;
     _Float16 *t = o.y;
     o.y = o.y2;
     o.y2 = t;

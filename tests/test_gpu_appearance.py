@@ -344,6 +344,17 @@ def test_orthogonalize_batches_strides_and_scale(dev):
         assert np.linalg.norm(_np(A.orthogonalize(g, steps, coeffs)) - ref) <= _ortho_tol(ref, "f32", steps, max(1.0, coeffs[0]))
 
 
+@pytest.mark.parametrize("shape", [(130, 2500), (300, 4100), (3, 70, 2049), (513, 16400), (130, 200, 250), (2300, 60)])
+def test_orthogonalize_tiles(dev, shape):
+    """Long summed axes (a product's steps shared out over all workgroups) and many tiles."""
+    from sphere_rasterization_amd import appearance as A
+    g = _put(np.random.default_rng(33).standard_normal(shape), "f32", dev)
+    got, ref = A.orthogonalize(g), O.orthogonalize(_np(g))
+    for p, q in zip(_np(got).reshape((-1,) + shape[-2:]), ref.reshape((-1,) + shape[-2:])):
+        assert np.linalg.norm(p - q) <= _ortho_tol(q, "f32")
+    assert torch.equal(got, A.orthogonalize(g)), "not the same bits twice"
+
+
 def test_orthogonalize_zero_tiny_huge_and_low_rank(dev):
     from sphere_rasterization_amd import appearance as A
     assert (A.orthogonalize(torch.zeros(2, 40, 30, device=dev)) == 0).all()
