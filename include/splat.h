@@ -366,7 +366,8 @@ int splat_group_norm_bwd(const splat_norm *norm, const void *d_y, const void *x,
  * Products keep 22 bits of each factor and fp32 sums. 1 <= steps <= 64; rows, cols <=
  * 65536; batch <= 65535; eps >= 0. Coefficients under which singular values could grow
  * past 1e4 return SPLAT_ERR_UNSUPPORTED. out may not overlap g.
- * workspace: [splat_orthogonalize_workspace_bytes] device bytes. */
+ * workspace: [splat_orthogonalize_workspace_bytes] device bytes (none for matrices that
+ * one workgroup's LDS holds). */
 size_t splat_orthogonalize_workspace_bytes(int64_t batch, int rows, int cols);
 int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int cols, int64_t g_batch_stride,
                         int64_t g_row_stride, int steps, float a, float b, float c, float eps, float scale,

@@ -635,8 +635,10 @@ int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int c
             stride_fits(out_batch_stride, batch) && g_batch_stride >= 0 && out_batch_stride >= 0,
         SPLAT_ERR_INVALID_ARG, "stride");
   CHECK(aligned_to(g, dtype) && aligned_to(out, dtype), SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
-  CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
-  CHECK(ws_bytes >= orthogonalize_workspace_bytes(batch, rows, cols), SPLAT_ERR_CAPACITY, "workspace too small");
+  if (const size_t need = orthogonalize_workspace_bytes(batch, rows, cols)) {
+    CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+    CHECK(ws_bytes >= need, SPLAT_ERR_CAPACITY, "workspace too small");
+  }
   return launch_orthogonalize(g, dtype, batch, rows, cols, g_batch_stride, g_row_stride, steps, a, b, c, eps, scale,
                               out, out_batch_stride, out_row_stride, workspace, stream);
 }

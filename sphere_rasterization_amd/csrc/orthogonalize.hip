@@ -472,6 +472,170 @@ __global__ __launch_bounds__(OR_THREADS) void k_ortho_join(GemmArgs g, int group
   Tl::template finish<EPI>(g, mat, it, jt, w, i, reinterpret_cast<_Float16 *>(lds), acc);
 }
 
+// ---- small matrices ---------------------------------------------------------------------
+// All steps of one matrix by one workgroup, X, X^T, A and B in LDS, padded to multiples
+// of 32: a step is three short products and as many barriers instead of three launches.
+// What bounds it is the length of one wave's instruction stream per product (a 32 x 32
+// tile's 16 values per lane to split and store took 0.8 us), so tiles are 16 x 16 and 16
+// waves share them. Symmetric results are written transposed only, four values to a
+// store. A block of a factor holds 32 values of the summed axis: 32 hi, then 32 lo, 128
+// bytes a row; 16-byte chunk c of row r lies at c ^ ((r >> 1) & 7), which meets no bank
+// twice in a fragment read.
+constexpr int SM_THREADS = 1024, SM_WAVES = SM_THREADS / WAVE;
+constexpr int SM_TILES = 6;                        // 16 x 16 tiles of X per wave, at most
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+struct SmallArgs {
+  const void *g;
+  void *out;
+  int64_t gb, gr, ob, orow;
+  int dtype, rows, cols, tall, m, n, mp, np, steps;
+  float eps, s0;
+  struct {
+    float mul_a, mul_p, ca, cb, mul_x, pad[3];     // scales of A, B and X, folded in
+  } step[64];
+};
+
+// Chunk `c` (hi 0 .. 3, lo 4 .. 7) of row r in block b of a factor of R rows, in halves.
+__device__ __forceinline__ int small_at(int R, int b, int r, int c) { return (b * R + r) * 64 + ((c ^ ((r >> 1) & 7)) << 3); }
+
+// 16 x 16 tile (it, jt) of P Q^T, factors of RP and RQ rows, summed over kb blocks.
+__device__ __forceinline__ float4v small_product(const _Float16 *p, int RP, int it, const _Float16 *q, int RQ, int jt,
+                                                 int kb, int lane) {
+  const int fr = lane & 15, fk = lane >> 4, ri = it * 16 + fr, rj = jt * 16 + fr;
+  float4v acc = {0.0f, 0.0f, 0.0f, 0.0f}, cross = acc;
+#pragma unroll 1
+  for (int b = 0; b < kb; b++) {
+    const half8 pl = *reinterpret_cast<const half8 *>(p + small_at(RP, b, ri, fk + 4));
+    const half8 qh = *reinterpret_cast<const half8 *>(q + small_at(RQ, b, rj, fk));
+    const half8 ph = *reinterpret_cast<const half8 *>(p + small_at(RP, b, ri, fk));
+    const half8 ql = *reinterpret_cast<const half8 *>(q + small_at(RQ, b, rj, fk + 4));
+    cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh, cross, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh, acc, 0, 0, 0);
+    cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql, cross, 0, 0, 0);
+  }
+  return acc + cross;
+}
+
+// Writes v as element k of row r of a factor of R rows.
+__device__ __forceinline__ void small_put(_Float16 *d, int R, int r, int k, float v) {
+  const int at = k & 7, c = (k >> 3) & 3;
+  const _Float16 hi = (_Float16)v;
+  d[small_at(R, k >> 5, r, c) + at] = hi;
+  d[small_at(R, k >> 5, r, c + 4) + at] = (_Float16)(v - (float)hi);
+}
+// Four consecutive elements from k, a multiple of four.
+__device__ __forceinline__ void small_put4(_Float16 *d, int R, int r, int k, float4v v) {
+  const int at = k & 7, c = (k >> 3) & 3;
+  half4 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    hi[e] = (_Float16)v[e];
+    lo[e] = (_Float16)(v[e] - (float)hi[e]);
+  }
+  *reinterpret_cast<half4 *>(d + small_at(R, k >> 5, r, c) + at) = hi;
+  *reinterpret_cast<half4 *>(d + small_at(R, k >> 5, r, c + 4) + at) = lo;
+}
+
+template <int LDS_BYTES>
+__global__ __launch_bounds__(SM_THREADS) void k_ortho_small(SmallArgs o) {
+  constexpr int SUMS = SM_WAVES * sizeof(double);
+  __shared__ __align__(16) char lds[LDS_BYTES];
+  double *sums = reinterpret_cast<double *>(lds);
+  float *result = reinterpret_cast<float *>(lds + SUMS);   // in X's and X^T's place at the end, rows padded by one
+  _Float16 *x = reinterpret_cast<_Float16 *>(lds + SUMS), *y = x + 2 * o.mp * o.np, *a = y + 2 * o.mp * o.np,
+           *b = a + 2 * o.mp * o.mp;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int lane = tid & 63;
+  const int64_t mat = blockIdx.x;
+  const char *g = (const char *)o.g + mat * o.gb * (o.dtype == SPLAT_F32 ? 4 : 2);
+  const int count = o.rows * o.cols;
+  double t = 0.0;
+  for (int i = tid; i < count; i += SM_THREADS) {
+    const int r = i / o.cols, c = i - r * o.cols;
+    const double v = (double)read_as_f32(g, r * o.gr + c, o.dtype);
+    t = __builtin_fma(v, v, t);
+  }
+  t = wave_sum_f64(t);
+  if (lane == 0) sums[w] = t;
+  __syncthreads();
+  double all = 0.0;
+#pragma unroll
+  for (int k = 0; k < SM_WAVES; k++) all += sums[k];
+  const float inv = (float)((double)o.s0 / (sqrt(all) + (double)o.eps));
+  for (int i = tid; i < o.mp * o.np; i += SM_THREADS) {
+    const int r = i / o.np, c = i - r * o.np;     // of X
+    float v = 0.0f;
+    if (r < o.m && c < o.n) v = read_as_f32(g, o.tall ? c * o.gr + r : r * o.gr + c, o.dtype) * inv;
+    small_put(x, o.mp, r, c, v);
+    small_put(y, o.np, c, r, v);
+  }
+  __syncthreads();
+  const int tm = o.mp / 16, tn = o.np / 16;
+  // k / tm for k below 6 x 16 tiles, exactly: tm is at most 9
+  const int recip = (65536 + tm - 1) / tm;
+  auto div_tm = [&](int k) { return (k * recip) >> 16; };
+  for (int s = 0; s < o.steps; s++) {
+    const auto st = o.step[s];
+    // the lane as a new value in each step: addresses made from it are formed where they
+    // are used, not kept (and spilled) across steps
+    asm volatile("" : "+v"(lane));
+    const int fr = lane & 15, fk = lane >> 4;
+#pragma unroll 1
+    for (int k = w; k < tm * tm; k += SM_WAVES) {  // A
+      const int it = div_tm(k), jt = k - it * tm;
+      const float4v v = small_product(x, o.mp, it, x, o.mp, jt, o.np / 32, lane);
+      small_put4(a, o.mp, jt * 16 + fr, it * 16 + fk * 4, v * st.mul_a);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = w; k < tm * tm; k += SM_WAVES) {  // B = a I + b A + c A A
+      const int it = div_tm(k), jt = k - it * tm, J = jt * 16 + fr, I0 = it * 16 + fk * 4;
+      const int at = I0 & 7, c = (I0 >> 3) & 3;
+      const half4 hi = *reinterpret_cast<const half4 *>(a + small_at(o.mp, I0 >> 5, J, c) + at);
+      const half4 lo = *reinterpret_cast<const half4 *>(a + small_at(o.mp, I0 >> 5, J, c + 4) + at);
+      float4v v = small_product(a, o.mp, it, a, o.mp, jt, o.mp / 32, lane);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        v[e] = __builtin_fmaf(st.cb, (float)hi[e] + (float)lo[e], v[e] * st.mul_p);
+        if (I0 + e == J) v[e] += st.ca;
+      }
+      small_put4(b, o.mp, J, I0, v);
+    }
+    __syncthreads();
+    // X <- B X: X^T is read by every wave, so the results wait in registers
+    float4v acc[SM_TILES];
+#pragma unroll
+    for (int u = 0; u < SM_TILES; u++) {
+      const int k = w + u * SM_WAVES;
+      if (k < tm * tn) acc[u] = small_product(b, o.mp, k - div_tm(k) * tm, y, o.np, div_tm(k), o.mp / 32, lane);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < SM_TILES; u++) {
+      const int k = w + u * SM_WAVES;
+      if (k < tm * tn) {
+        const int jt = div_tm(k), I0 = (k - jt * tm) * 16 + fk * 4, J = jt * 16 + fr;
+        const float4v v = acc[u] * st.mul_x;
+        if (s + 1 < o.steps) {
+          small_put4(y, o.np, J, I0, v);
+#pragma unroll
+          for (int e = 0; e < 4; e++) small_put(x, o.mp, I0 + e, J, v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e++) result[o.tall ? J * (o.mp + 1) + I0 + e : (I0 + e) * (o.np + 1) + J] = v[e];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int ld = (o.tall ? o.mp : o.np) + 1;
+  for (int i = tid; i < count; i += SM_THREADS) {
+    const int r = i / o.cols, c = i - r * o.cols;
+    write_from_f32(o.out, mat * o.ob + r * o.orow + c, o.dtype, result[r * ld + c]);
+  }
+}
+
 // ---- host -----------------------------------------------------------------------------
 // Largest |a x + b x^3 + c x^5| for 0 <= x <= u.
 double sup_quintic(double a, double b, double c, double u) {
@@ -508,11 +672,19 @@ int scale_exp(double bound) {
   return e - 1;
 }
 
-int round_up(int x, int k) { return (x + k - 1) / k * k; }
-
 constexpr int GROUPS = 512;               // workgroups that the chip holds at once, two per CU
 
 int64_t lower_tiles(int len, int tl) { return (int64_t)(len / tl) * (len / tl + 1) / 2; }
+
+int round_up(int x, int k) { return (x + k - 1) / k * k; }
+
+// LDS bytes of the one-workgroup form; 0 if the matrix is too large for it.
+constexpr int SMALL_LDS = 64 << 10, LARGE_LDS = 160 << 10;
+int small_lds(int rows, int cols) {
+  const int64_t m = round_up(rows < cols ? rows : cols, 32), n = round_up(rows < cols ? cols : rows, 32);
+  const int64_t bytes = 8 * SM_WAVES + 4 * (2 * m * n + 2 * m * m);
+  return (m / 16) * (n / 16) <= SM_TILES * SM_WAVES && bytes <= LARGE_LDS ? (int)bytes : 0;
+}
 
 // Whether a symmetric product's tiles are shared out over all workgroups.
 bool share_out(int64_t tiles, int tl, int K) { return tiles < GROUPS && K >= (tl == 128 ? 512 : 2048); }
@@ -584,6 +756,7 @@ int run_gemm(const GemmArgs &q, int tile, int I, int J, int64_t batch, hipStream
 }  // namespace
 
 size_t orthogonalize_workspace_bytes(int64_t batch, int rows, int cols) {
+  if (small_lds(rows, cols)) return 0;
   size_t bytes = 0;
   ortho_layout(nullptr, batch, rows, cols, &bytes);
   return bytes;
@@ -604,6 +777,45 @@ int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int 
                          int steps, float ca, float cb, float cc, float eps, float scale, void *out, int64_t ob,
                          int64_t orow, void *ws, hipStream_t stream) {
   if (batch == 0 || rows == 0 || cols == 0) return SPLAT_OK;
+  if (const int lds = small_lds(rows, cols)) {
+    SmallArgs o = {};
+    o.g = g;
+    o.out = out;
+    o.gb = gb;
+    o.gr = gr;
+    o.ob = ob;
+    o.orow = orow;
+    o.dtype = dtype;
+    o.rows = rows;
+    o.cols = cols;
+    o.tall = rows > cols;
+    o.m = o.tall ? cols : rows;
+    o.n = o.tall ? rows : cols;
+    o.mp = round_up(o.m, 32);
+    o.np = round_up(o.n, 32);
+    o.steps = steps;
+    o.eps = eps;
+    double u = 1.0;
+    int ex = scale_exp(u);
+    o.s0 = ldexpf(1.0f, ex);
+    for (int k = 0; k < steps; k++) {
+      const int ea = scale_exp(u * u), eb = scale_exp(sup_quadratic(ca, cb, cc, u * u));
+      u = sup_quintic(ca, cb, cc, u);
+      const int en = scale_exp(u);
+      o.step[k].mul_a = ldexpf(1.0f, ea - 2 * ex);
+      o.step[k].mul_p = ldexpf(cc, eb - 2 * ea);
+      o.step[k].ca = ldexpf(ca, eb);
+      o.step[k].cb = ldexpf(cb, eb - ea);
+      o.step[k].mul_x = k + 1 == steps ? ldexpf(scale, -(eb + ex)) : ldexpf(1.0f, en - eb - ex);
+      ex = en;
+    }
+    if (lds <= SMALL_LDS)
+      hipLaunchKernelGGL(k_ortho_small<SMALL_LDS>, dim3((unsigned)batch), dim3(SM_THREADS), 0, stream, o);
+    else
+      hipLaunchKernelGGL(k_ortho_small<LARGE_LDS>, dim3((unsigned)batch), dim3(SM_THREADS), 0, stream, o);
+    SPLAT_LAUNCH_CHECK();
+    return SPLAT_OK;
+  }
   size_t bytes;
   OrthoArgs o = ortho_layout(ws, batch, rows, cols, &bytes);
   o.g = g;

@@ -39,8 +39,9 @@ def test_size_queries():
     assert L.splat_lookup_bwd_workspace_bytes(-1, rows, dim) == 0
     assert L.splat_group_norm_workspace_bytes(_norm()) >= 2 * 2 * 8
     assert L.splat_group_norm_workspace_bytes(_norm(groups=3)) == 0
-    assert L.splat_orthogonalize_workspace_bytes(2, 100, 300) >= 2 * 100 * 300 * 4 * 2
+    assert L.splat_orthogonalize_workspace_bytes(2, 200, 300) >= 2 * 200 * 300 * 4 * 2
     assert L.splat_orthogonalize_workspace_bytes(1, 100_000, 3) == 0
+    assert L.splat_orthogonalize_workspace_bytes(100, 64, 96) == 0        # held in LDS
 
 
 @pytest.mark.parametrize("change", [
@@ -103,8 +104,8 @@ def test_group_norm_pointer_refusals():
     (dict(scale=float("inf")), -1), (dict(a=20.0), -4), (dict(g=None), -1), (dict(out=None), -1), (dict(gr=9), -1),
     (dict(orow=9), -1), (dict(gb=-1), -1), (dict(ws=None), -1), (dict(nbytes=64), -2)])
 def test_orthogonalize_refusals(change, code):
-    a = dict(g=P, dtype=0, batch=2, rows=8, cols=10, gb=80, gr=10, steps=5, a=3.4445, b=-4.775, c=2.0315, eps=1e-7,
-             scale=1.0, out=P, ob=80, orow=10, ws=P, nbytes=1 << 30)
+    a = dict(g=P, dtype=0, batch=2, rows=300, cols=400, gb=120000, gr=400, steps=5, a=3.4445, b=-4.775, c=2.0315,
+             eps=1e-7, scale=1.0, out=P, ob=120000, orow=400, ws=P, nbytes=1 << 30)
     a.update(change)
     assert L.lib().splat_orthogonalize(*a.values(), None) == code
 
