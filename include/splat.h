@@ -344,8 +344,9 @@ typedef struct {
   int64_t dx_image_stride, dx_pixel_stride;
 } splat_norm;
 
-/* Workspace bytes of either direction. */
-size_t splat_group_norm_workspace_bytes(const splat_norm *norm);
+/* Workspace bytes of splat_group_norm (backward = 0) or splat_group_norm_bwd (1); 0 where
+ * none is needed (few, small groups). The strides do not matter here. */
+size_t splat_group_norm_workspace_bytes(const splat_norm *norm, int backward);
 
 /* y = act(weight (x - mean) rstd + bias), rstd = 1 / sqrt(var + eps). weight and bias
  * [channels] may be NULL (1 and 0). mean, rstd [images][groups] fp32 receive the

@@ -120,7 +120,7 @@ def lib():
         L.splat_lookup_bwd.restype = i32
         L.splat_lookup_bwd.argtypes = [vp, i32, i64, vp, i32, i64, i64, i32, f32, vp, i64, i32, vp, sz, vp]
         L.splat_group_norm_workspace_bytes.restype = sz
-        L.splat_group_norm_workspace_bytes.argtypes = [norm_p]
+        L.splat_group_norm_workspace_bytes.argtypes = [norm_p, i32]
         L.splat_group_norm.restype = i32
         L.splat_group_norm.argtypes = [norm_p, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.splat_group_norm_bwd.restype = i32
@@ -231,8 +231,8 @@ def splat_lookup_bwd(d_out, dtype, d_out_stride, ids, itype, n, rows, dim, scale
                                                              ws_bytes, stream))
 
 
-def splat_group_norm_workspace_bytes(norm):
-    return lib().splat_group_norm_workspace_bytes(C.byref(norm))
+def splat_group_norm_workspace_bytes(norm, backward):
+    return lib().splat_group_norm_workspace_bytes(C.byref(norm), 1 if backward else 0)
 
 
 def splat_group_norm(norm, x, weight, bias, y, mean, rstd, workspace, ws_bytes, stream):

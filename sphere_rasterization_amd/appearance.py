@@ -53,15 +53,19 @@ class _Launch:
     def __enter__(self):
         if self.dev != self.prev:
             torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.dev)
 
     def __exit__(self, *exc):
         if self.dev != self.prev:
             torch.cuda.set_device(self.prev)
 
 
-def _workspace(nbytes: int, ref: torch.Tensor) -> torch.Tensor:
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=ref.device)
+def _workspace(nbytes: int, ref: torch.Tensor) -> Tuple[Optional[torch.Tensor], Optional[int], int]:
+    """(memory to keep until the call returns, its address, its bytes)."""
+    if nbytes == 0:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=ref.device)
+    return ws, ws.data_ptr(), nbytes
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -113,11 +117,10 @@ def lookup_backward(d_out: torch.Tensor, ids: torch.Tensor, rows: int, scale: fl
             raise ValueError("out: rows must be contiguous and must not overlap")
     n = ids.numel()
     dy, flat = _rows(d_out.reshape(n, dim)), ids.contiguous()
-    nbytes = L.splat_lookup_bwd_workspace_bytes(n, rows, dim)
-    ws = _workspace(nbytes, d_out)
+    _keep, ws, nbytes = _workspace(L.splat_lookup_bwd_workspace_bytes(n, rows, dim), d_out)
     with _Launch(d_out) as stream:
         L.splat_lookup_bwd(dy.data_ptr(), dt, dy.stride(0), flat.data_ptr(), it, n, rows, dim, scale, out.data_ptr(),
-                           out.stride(0), 1 if accumulate else 0, ws.data_ptr(), ws.numel(), stream)
+                           out.stride(0), 1 if accumulate else 0, ws, nbytes, stream)
     return out
 
 
@@ -189,20 +192,31 @@ def _flat(t: Optional[torch.Tensor]):
     return None if t is None else t.contiguous()
 
 
-def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
-                       bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none"):
-    """(y, mean, rstd) of `group_norm`: mean and rstd [images, groups] are what the
-    backward needs besides x."""
+def _group_norm(x, groups, weight, bias, eps, act, keep: bool):
+    """y and, if kept, the statistics [2, images, groups] (mean, rstd)."""
     d = _norm_desc(x, weight, bias, groups, act, eps)
     x, d.x_image_stride, d.x_pixel_stride = _pixels(x)
     weight, bias = _flat(weight), _flat(bias)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, d.images, d.groups), dtype=torch.float32, device=x.device)
     d.y_image_stride, d.y_pixel_stride = d.pixels * d.channels, d.channels
-    ws = _workspace(L.splat_group_norm_workspace_bytes(d), x)
+    one, nbytes = 4 * d.images * d.groups, L.splat_group_norm_workspace_bytes(d, False)
+    if keep:
+        stats = torch.empty((2, d.images, d.groups), dtype=torch.float32, device=x.device)
+        mean = stats.data_ptr()
+        _ws, ws, nbytes = _workspace(nbytes, x)
+    else:                                    # one allocation: the workspace, then the statistics
+        stats, ws, _n = _workspace(nbytes + 2 * one, x)
+        mean = (ws or 0) + nbytes
     with _Launch(x) as stream:
-        L.splat_group_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), stats[0].data_ptr(),
-                           stats[1].data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        L.splat_group_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean, mean + one, ws, nbytes, stream)
+    return y, stats
+
+
+def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = None,
+                       bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none"):
+    """(y, mean, rstd) of `group_norm`: mean and rstd [images, groups] are what the
+    backward needs besides x."""
+    y, stats = _group_norm(x, groups, weight, bias, eps, act, True)
     return y, stats[0], stats[1]
 
 
@@ -226,10 +240,10 @@ def group_norm_backward(d_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, 
     dw = torch.empty(d.channels, dtype=kind, device=x.device) if "weight" in want else None
     db = torch.empty(d.channels, dtype=kind, device=x.device) if "bias" in want else None
     d.dx_image_stride, d.dx_pixel_stride = d.pixels * d.channels, d.channels
-    ws = _workspace(L.splat_group_norm_workspace_bytes(d), x)
+    _keep, ws, nbytes = _workspace(L.splat_group_norm_workspace_bytes(d, True), x)
     with _Launch(x) as stream:
         L.splat_group_norm_bwd(d, d_y.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
-                               _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db), ws.data_ptr(), ws.numel(), stream)
+                               _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db), ws, nbytes, stream)
     return dx, dw, db
 
 
@@ -260,7 +274,7 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     channels_last memory format is read in place as x.permute(0, 2, 3, 1)."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
         return _GroupNorm.apply(x, groups, weight, bias, eps, act)
-    return group_norm_forward(x, groups, weight, bias, eps, act)[0]
+    return _group_norm(x, groups, weight, bias, eps, act, False)[0]
 
 
 # ---- orthogonalised updates ----------------------------------------------------------
@@ -282,10 +296,8 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = (3.
     if (cols > 1 and m.stride(2) != 1) or (rows > 1 and m.stride(1) < cols):
         m = m.contiguous()
     batch = m.shape[0]
-    nbytes = L.splat_orthogonalize_workspace_bytes(batch, rows, cols)
-    ws = _workspace(nbytes, g)
+    _keep, ws, nbytes = _workspace(L.splat_orthogonalize_workspace_bytes(batch, rows, cols), g)
     with _Launch(g) as stream:
         L.splat_orthogonalize(m.data_ptr(), dt, batch, rows, cols, m.stride(0), m.stride(1), steps, *map(float, coeffs),
-                              float(eps), float(scale), out.data_ptr(), rows * cols, cols, ws.data_ptr(), ws.numel(),
-                              stream)
+                              float(eps), float(scale), out.data_ptr(), rows * cols, cols, ws, nbytes, stream)
     return out

@@ -33,7 +33,7 @@ int launch_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t l
 size_t lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim);
 int launch_lookup_bwd(const void *d_out, int dtype, int64_t ldy, const void *ids, int id_type, int64_t n, int64_t rows,
                       int dim, float scale, void *d_table, int64_t ldg, int accumulate, void *ws, hipStream_t stream);
-size_t group_norm_workspace_bytes(const splat_norm *d);
+size_t group_norm_workspace_bytes(const splat_norm *d, bool bwd);
 int launch_group_norm(const splat_norm *d, const void *x, const void *w, const void *b, void *y, float *mean,
                       float *rstd, void *ws, hipStream_t stream);
 int launch_group_norm_bwd(const splat_norm *d, const void *d_y, const void *x, const float *mean, const float *rstd,
@@ -577,8 +577,8 @@ int splat_lookup_bwd(const void *d_out, int dtype, int64_t d_out_stride, const v
                            rows == 1 ? dim : d_table_stride, accumulate, workspace, stream);
 }
 
-size_t splat_group_norm_workspace_bytes(const splat_norm *norm) {
-  return check_norm(norm, false, false) == SPLAT_OK ? group_norm_workspace_bytes(norm) : 0;
+size_t splat_group_norm_workspace_bytes(const splat_norm *norm, int backward) {
+  return check_norm(norm, false, false) == SPLAT_OK ? group_norm_workspace_bytes(norm, backward != 0) : 0;
 }
 
 int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, const void *bias, void *y,
@@ -590,8 +590,10 @@ int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, 
   CHECK(aligned_to(x, norm->dtype) && aligned_to(y, norm->dtype) && aligned_to(weight, norm->param_dtype) &&
             aligned_to(bias, norm->param_dtype) && aligned_to(mean, SPLAT_F32) && aligned_to(rstd, SPLAT_F32),
         SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
-  CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
-  CHECK(ws_bytes >= group_norm_workspace_bytes(norm), SPLAT_ERR_CAPACITY, "group norm workspace too small");
+  if (const size_t need = group_norm_workspace_bytes(norm, false)) {
+    CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+    CHECK(ws_bytes >= need, SPLAT_ERR_CAPACITY, "group norm workspace too small");
+  }
   return launch_group_norm(norm, x, weight, bias, y, mean, rstd, workspace, stream);
 }
 
@@ -602,8 +604,10 @@ int splat_group_norm_bwd(const splat_norm *norm, const void *d_y, const void *x,
   if (st) return st;
   if (norm->images > 0 && norm->pixels > 0) {
     CHECK(x && d_y && mean && rstd, SPLAT_ERR_INVALID_ARG, "NULL array");
-    CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
-    CHECK(ws_bytes >= group_norm_workspace_bytes(norm), SPLAT_ERR_CAPACITY, "group norm workspace too small");
+    if (const size_t need = group_norm_workspace_bytes(norm, true)) {
+      CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+      CHECK(ws_bytes >= need, SPLAT_ERR_CAPACITY, "group norm workspace too small");
+    }
   }
   CHECK(aligned_to(x, norm->dtype) && aligned_to(d_y, norm->dtype) && aligned_to(d_x, norm->dtype) &&
             aligned_to(weight, norm->param_dtype) && aligned_to(bias, norm->param_dtype) &&

@@ -28,6 +28,21 @@ __device__ __forceinline__ void store_f32(T *p, const float (&o)[N]) {
   *reinterpret_cast<Pack<T, N> *>(p) = x;
 }
 
+// The same for results that this call does not read again: they pass by the caches that
+// hold its inputs.
+template <typename T, int N>
+__device__ __forceinline__ void stream_f32(T *p, const float (&o)[N]) {
+  if constexpr (sizeof(T) * N == 16) {
+    typedef unsigned chunk __attribute__((ext_vector_type(4)));
+    Pack<T, N> x;
+#pragma unroll
+    for (int i = 0; i < N; i++) x.v[i] = (T)o[i];
+    __builtin_nontemporal_store(__builtin_bit_cast(chunk, x), reinterpret_cast<chunk *>(p));
+  } else {
+    store_f32<T, N>(p, o);
+  }
+}
+
 // fp32 sums kept in the workspace: 16-byte accesses where N allows.
 template <int N>
 __device__ __forceinline__ void load_sums(const float *p, float (&o)[N]) {

@@ -37,8 +37,9 @@ def test_size_queries():
     need = L.splat_lookup_bwd_workspace_bytes(n, rows, dim)
     assert need >= 16 * n + 8 * rows + 4 * dim * (n // 64)
     assert L.splat_lookup_bwd_workspace_bytes(-1, rows, dim) == 0
-    assert L.splat_group_norm_workspace_bytes(_norm()) >= 2 * 2 * 8
-    assert L.splat_group_norm_workspace_bytes(_norm(groups=3)) == 0
+    assert L.splat_group_norm_workspace_bytes(_norm(pixels=1 << 20), False) >= 2 * 2 * 8
+    assert L.splat_group_norm_workspace_bytes(_norm(pixels=1 << 20), True) >= 2 * 8 * 8
+    assert L.splat_group_norm_workspace_bytes(_norm(groups=3, pixels=1 << 20), False) == 0
     assert L.splat_orthogonalize_workspace_bytes(2, 200, 300) >= 2 * 200 * 300 * 4 * 2
     assert L.splat_orthogonalize_workspace_bytes(1, 100_000, 3) == 0
     assert L.splat_orthogonalize_workspace_bytes(100, 64, 96) == 0        # held in LDS
@@ -79,7 +80,7 @@ def test_group_norm_descriptor_refusals(change):
 
 
 def test_group_norm_pointer_refusals():
-    f, b, d = L.lib().splat_group_norm, L.lib().splat_group_norm_bwd, _norm()
+    f, b, d = L.lib().splat_group_norm, L.lib().splat_group_norm_bwd, _norm(pixels=1 << 20)
     bad = [P] * 7
     for k in (0, 3, 4, 5, 6):                # x, y, mean, rstd, workspace
         args = list(bad)
@@ -92,7 +93,7 @@ def test_group_norm_pointer_refusals():
         args[k] = None
         assert b(C.byref(d), *args, 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
     assert b(C.byref(d), *[P] * 10, 8, None) == L.SPLAT_ERR_CAPACITY
-    overlap = _norm(dx_pixel_stride=4)
+    overlap = _norm(pixels=1 << 20, dx_pixel_stride=4)
     assert b(C.byref(overlap), *[P] * 10, 1 << 30, None) == L.SPLAT_ERR_INVALID_ARG
     # nothing asked for: nothing done
     assert b(C.byref(d), P, P, P, P, P, P, None, None, None, P, 1 << 30, None) == L.SPLAT_OK
