@@ -311,17 +311,23 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_apply(NormArgs a) {
     T *y = (T *)a.y + q.n * a.yi + (int64_t)unit * VEC;
     constexpr int U = 4;
     for (int64_t p = q.p0 + pl; p < q.p1; p += (int64_t)U * a.TP) {
-      float v[U][VEC];
+      Raw<T, VEC> t[U];
 #pragma unroll
-      for (int k = 0; k < U; k++)
-        if (p + (int64_t)k * a.TP < q.p1) load_f32<T, VEC>(x + (p + (int64_t)k * a.TP) * a.xp, v[k]);
+      for (int k = 0; k < U; k++) {
+        const int64_t pk = p + (int64_t)k * a.TP;
+        t[k] = load_if<T, VEC>(pk < q.p1, x + pk * a.xp);
+      }
 #pragma unroll
-      for (int k = 0; k < U; k++)
-        if (p + (int64_t)k * a.TP < q.p1) {
+      for (int k = 0; k < U; k++) {
+        const int64_t pk = p + (int64_t)k * a.TP;
+        if (pk < q.p1) {
+          float v[VEC];
+          to_f32<T, VEC>(t[k], v);
 #pragma unroll
-          for (int j = 0; j < VEC; j++) v[k][j] = act_of<ACT>(__builtin_fmaf(v[k][j] - mu[j], s[j], b[j]));
-          stream_f32<T, VEC>(y + (p + (int64_t)k * a.TP) * a.yp, v[k]);
+          for (int j = 0; j < VEC; j++) v[j] = act_of<ACT>(__builtin_fmaf(v[j] - mu[j], s[j], b[j]));
+          stream_f32<T, VEC>(y + pk * a.yp, v);
         }
+      }
     }
   }
 }
@@ -356,16 +362,18 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_bwd_sums(NormArgs a) {
       const T *dy = (const T *)a.dy + q.n * a.yi + (int64_t)unit * VEC;
       constexpr int U = 4;
       for (int64_t p = q.p0 + pl; p < q.p1; p += (int64_t)U * a.TP) {
-        float v[U][VEC], d[U][VEC];
+        Raw<T, VEC> xv[U], dv[U];
 #pragma unroll
         for (int k = 0; k < U; k++) {
           const int64_t pk = p + (int64_t)k * a.TP;
+          xv[k] = load_if<T, VEC>(pk < q.p1, x + pk * a.xp);
+          dv[k] = load_if<T, VEC>(pk < q.p1, dy + pk * a.yp);   // past the end dz = 0
+        }
+        float v[U][VEC], d[U][VEC];
 #pragma unroll
-          for (int j = 0; j < VEC; j++) d[k][j] = 0.0f, v[k][j] = mu[j];
-          if (pk < q.p1) {
-            load_f32<T, VEC>(x + pk * a.xp, v[k]);
-            load_f32<T, VEC>(dy + pk * a.yp, d[k]);
-          }
+        for (int k = 0; k < U; k++) {
+          to_f32<T, VEC>(xv[k], v[k]);
+          to_f32<T, VEC>(dv[k], d[k]);
         }
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
@@ -516,26 +524,27 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_bwd_apply(NormArgs a, int m
       T *dx = (T *)a.dx + q.n * a.di + (int64_t)unit * VEC;
       constexpr int U = 2;
       for (int64_t p = q.p0 + pl; p < q.p1; p += (int64_t)U * a.TP) {
-        float v[U][VEC], d[U][VEC];
+        Raw<T, VEC> xv[U], dv[U];
 #pragma unroll
         for (int k = 0; k < U; k++) {
           const int64_t pk = p + (int64_t)k * a.TP;
-          if (pk < q.p1) {
-            load_f32<T, VEC>(x + pk * a.xp, v[k]);
-            load_f32<T, VEC>(dy + pk * a.yp, d[k]);
-          }
+          xv[k] = load_if<T, VEC>(pk < q.p1, x + pk * a.xp);
+          dv[k] = load_if<T, VEC>(pk < q.p1, dy + pk * a.yp);
         }
 #pragma unroll
         for (int k = 0; k < U; k++) {
           const int64_t pk = p + (int64_t)k * a.TP;
           if (pk < q.p1) {
+            float v[VEC], d[VEC];
+            to_f32<T, VEC>(xv[k], v);
+            to_f32<T, VEC>(dv[k], d);
 #pragma unroll
             for (int j = 0; j < VEC; j++) {
-              const float xc = v[k][j] - mu[j];
-              const float dz = d[k][j] * act_slope<ACT>(__builtin_fmaf(xc, rw[j], b[j]));
-              v[k][j] = __builtin_fmaf(dz, rw[j], __builtin_fmaf(xc, t2[j], t1[j]));
+              const float xc = v[j] - mu[j];
+              const float dz = d[j] * act_slope<ACT>(__builtin_fmaf(xc, rw[j], b[j]));
+              v[j] = __builtin_fmaf(dz, rw[j], __builtin_fmaf(xc, t2[j], t1[j]));
             }
-            stream_f32<T, VEC>(dx + pk * a.dp, v[k]);
+            stream_f32<T, VEC>(dx + pk * a.dp, v);
           }
         }
       }
@@ -580,20 +589,21 @@ __global__ __launch_bounds__(GS_THREADS) void k_norm_small(NormArgs a) {
     const int g = (int)(i - n * a.G), c0 = g * a.cg + ul * VEC;
     const T *x = (const T *)a.x + n * a.xi + c0;
     T *y = (T *)a.y + n * a.yi + c0;
+    Raw<T, VEC> t[GS_FWD];
     float v[GS_FWD][VEC], sum = 0.0f, m2 = 0.0f, w[VEC], bias[VEC];
 #pragma unroll
     for (int k = 0; k < GS_FWD; k++) {
       const int64_t p = pl + (int64_t)k * a.TP;
-#pragma unroll
-      for (int j = 0; j < VEC; j++) v[k][j] = 0.0f;
-      if (on && p < a.P) load_f32<T, VEC>(x + p * a.xp, v[k]);
+      t[k] = load_if<T, VEC>(on && p < a.P, x + p * a.xp);
     }
     params_at<T, VEC>(a.w, on ? c0 : 0, a.pf32, 1.0f, w);
     params_at<T, VEC>(a.b, on ? c0 : 0, a.pf32, 0.0f, bias);
 #pragma unroll
-    for (int k = 0; k < GS_FWD; k++)
+    for (int k = 0; k < GS_FWD; k++) {
+      to_f32<T, VEC>(t[k], v[k]);
 #pragma unroll
       for (int j = 0; j < VEC; j++) sum += v[k][j];
+    }
     const float mean = block_sum8(sum, s) * im;
 #pragma unroll
     for (int k = 0; k < GS_FWD; k++)
@@ -632,16 +642,13 @@ __global__ __launch_bounds__(GS_THREADS) void k_norm_bwd_small(NormArgs a) {
     const int g = (int)(i - n * a.G), c0 = g * a.cg + ul * VEC;
     const T *x = (const T *)a.x + n * a.xi + c0, *dy = (const T *)a.dy + n * a.yi + c0;
     const float mean = a.mean[i], rstd = a.rstd[i];
+    Raw<T, VEC> xv[GS_BWD], dv[GS_BWD];
     float v[GS_BWD][VEC], d[GS_BWD][VEC], rw[VEC], b[VEC], A[VEC], B[VEC];
 #pragma unroll
     for (int k = 0; k < GS_BWD; k++) {
       const int64_t p = pl + (int64_t)k * a.TP;
-#pragma unroll
-      for (int j = 0; j < VEC; j++) v[k][j] = mean, d[k][j] = 0.0f;
-      if (on && p < a.P) {
-        load_f32<T, VEC>(x + p * a.xp, v[k]);
-        load_f32<T, VEC>(dy + p * a.yp, d[k]);
-      }
+      xv[k] = load_if<T, VEC>(on && p < a.P, x + p * a.xp);
+      dv[k] = load_if<T, VEC>(on && p < a.P, dy + p * a.yp);
     }
     params_at<T, VEC>(a.w, on ? c0 : 0, a.pf32, 1.0f, rw);
     params_at<T, VEC>(a.b, on ? c0 : 0, a.pf32, 0.0f, b);
@@ -651,7 +658,9 @@ __global__ __launch_bounds__(GS_THREADS) void k_norm_bwd_small(NormArgs a) {
       A[j] = B[j] = 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < GS_BWD; k++)
+    for (int k = 0; k < GS_BWD; k++) {
+      to_f32<T, VEC>(xv[k], v[k]);
+      to_f32<T, VEC>(dv[k], d[k]);
 #pragma unroll
       for (int j = 0; j < VEC; j++) {
         v[k][j] -= mean;
@@ -659,6 +668,7 @@ __global__ __launch_bounds__(GS_THREADS) void k_norm_bwd_small(NormArgs a) {
         A[j] += d[k][j];
         B[j] = __builtin_fmaf(d[k][j], v[k][j], B[j]);
       }
+    }
     if (on) {
 #pragma unroll
       for (int j = 0; j < VEC; j++) s_ab[threadIdx.x * VEC + j] = make_float2(A[j], B[j] * rstd);

@@ -12,11 +12,40 @@ struct alignas(sizeof(T) * N) Pack {
   T v[N];
 };
 
+// The bits of a pack as whole words: what the compiler keeps in registers unsplit.
+template <int BYTES>
+struct RawBits;
+template <>
+struct RawBits<16> { typedef uint32_t type __attribute__((ext_vector_type(4))); };
+template <>
+struct RawBits<8> { typedef uint32_t type __attribute__((ext_vector_type(2))); };
+template <>
+struct RawBits<4> { typedef uint32_t type; };
+template <>
+struct RawBits<2> { typedef uint16_t type; };
 template <typename T, int N>
-__device__ __forceinline__ void load_f32(const T *p, float (&o)[N]) {
-  const Pack<T, N> x = *reinterpret_cast<const Pack<T, N> *>(p);
+using Raw = typename RawBits<sizeof(T) * N>::type;
+
+template <typename T, int N>
+__device__ __forceinline__ void to_f32(const Raw<T, N> &r, float (&o)[N]) {
+  const Pack<T, N> x = __builtin_bit_cast(Pack<T, N>, r);
 #pragma unroll
   for (int i = 0; i < N; i++) o[i] = (float)x.v[i];
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void load_f32(const T *p, float (&o)[N]) {
+  to_f32<T, N>(*reinterpret_cast<const Raw<T, N> *>(p), o);
+}
+
+// The pack at p, or zeros. Several of these are in flight together when they are
+// converted only after the last one: a conversion next to its load, under the load's
+// condition, waits for that load alone.
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> load_if(bool ok, const T *p) {
+  Raw<T, N> x = {};
+  if (ok) x = *reinterpret_cast<const Raw<T, N> *>(p);
+  return x;
 }
 
 // One rounding to the nearest value of the type.
@@ -33,11 +62,10 @@ __device__ __forceinline__ void store_f32(T *p, const float (&o)[N]) {
 template <typename T, int N>
 __device__ __forceinline__ void stream_f32(T *p, const float (&o)[N]) {
   if constexpr (sizeof(T) * N == 16) {
-    typedef unsigned chunk __attribute__((ext_vector_type(4)));
     Pack<T, N> x;
 #pragma unroll
     for (int i = 0; i < N; i++) x.v[i] = (T)o[i];
-    __builtin_nontemporal_store(__builtin_bit_cast(chunk, x), reinterpret_cast<chunk *>(p));
+    __builtin_nontemporal_store(__builtin_bit_cast(Raw<T, N>, x), reinterpret_cast<Raw<T, N> *>(p));
   } else {
     store_f32<T, N>(p, o);
   }

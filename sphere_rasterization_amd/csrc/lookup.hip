@@ -9,22 +9,25 @@
 // tokens are sorted by id (stable, so each row's tokens keep their order) and each
 // row is summed in a fixed order:
 //   1. counting sort by digits of up to 9 bits, least significant first: counts per
-//      tile of 4096 tokens, a scan per digit, a scatter that ranks equal digits
+//      tile of 1024 or 4096 tokens, a scan per digit, a scatter that ranks equal digits
 //      within a wave by ballots. Up to 4096 tokens: one workgroup, all in LDS;
 //   2. the sorted list is cut into chunks of 64; a chunk that lies within one row's
 //      segment is summed to one fp32 row, and 64 such sums to one of the next level;
-//   3. each row adds its loose tokens and its whole chunks and writes its gradient.
-// So a row that holds all n tokens costs no thread more than 4 x 64 + n / 4096 adds.
+//   3. each row is written by adding its tokens, or its loose tokens and whole chunks.
+// So a row that holds all n tokens costs no lane more than 4 x 64 + n / 4096 adds.
 #include "learn_common.h"
 
 namespace {
 
 constexpr int LK_THREADS = 256;
 constexpr int LK_ITEMS = 4;
-constexpr int ST_THREADS = 256, ST_ITEMS = 16, ST_TILE = ST_THREADS * ST_ITEMS;
+constexpr int ST_THREADS = 256;              // sort tiles: 4 or 16 tokens a thread
 constexpr int ST_WAVES = ST_THREADS / WAVE;
 constexpr int RADIX_BITS = 9, RADIX = 1 << RADIX_BITS;
 constexpr int CHUNK = 64;
+// Tokens up to which tiles are small: more workgroups for the same chain of rankings.
+constexpr int64_t SMALL_TILES = 256 << 10;
+constexpr int tile_items(int64_t n) { return n <= SMALL_TILES ? 4 : 16; }
 
 // ---------------------------------------------------------------------------
 // forward
@@ -34,28 +37,28 @@ __global__ __launch_bounds__(LK_THREADS) void k_lookup(const T *__restrict__ tab
                                                        const ID *__restrict__ ids, uint32_t total, FastDiv units,
                                                        float scale, T *__restrict__ out, int64_t ldo) {
   const uint32_t base = blockIdx.x * (LK_THREADS * LK_ITEMS) + threadIdx.x;
-  float v[LK_ITEMS][VEC];
+  uint32_t row[LK_ITEMS], col[LK_ITEMS];
+  int64_t id[LK_ITEMS];
+  Raw<T, VEC> x[LK_ITEMS];
 #pragma unroll
   for (int k = 0; k < LK_ITEMS; k++) {
     const uint32_t u = base + k * LK_THREADS;
-#pragma unroll
-    for (int j = 0; j < VEC; j++) v[k][j] = 0.0f;
-    if (u < total) {
-      const uint32_t i = div_by(u, units), c = (u - i * units.d) * VEC;
-      const int64_t id = (int64_t)ids[i];
-      if (id >= 0 && id < rows) load_f32<T, VEC>(table + id * ldt + c, v[k]);
-    }
+    row[k] = div_by(u, units);
+    col[k] = (u - row[k] * units.d) * VEC;
+    id[k] = u < total ? (int64_t)ids[row[k]] : -1;
   }
 #pragma unroll
-  for (int k = 0; k < LK_ITEMS; k++) {
-    const uint32_t u = base + k * LK_THREADS;
-    if (u < total) {
-      const uint32_t i = div_by(u, units), c = (u - i * units.d) * VEC;
+  for (int k = 0; k < LK_ITEMS; k++)
+    x[k] = load_if<T, VEC>(id[k] >= 0 && id[k] < rows, table + id[k] * ldt + col[k]);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) v[k][j] *= scale;
-      store_f32<T, VEC>(out + (int64_t)i * ldo + c, v[k]);
+  for (int k = 0; k < LK_ITEMS; k++)
+    if (base + k * LK_THREADS < total) {
+      float v[VEC];
+      to_f32<T, VEC>(x[k], v);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[j] *= scale;
+      stream_f32<T, VEC>(out + (int64_t)row[k] * ldo + col[k], v);
     }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -68,28 +71,28 @@ __device__ __forceinline__ uint32_t key_of(const ID *ids, uint32_t i, uint32_t r
   return id >= 0 && id < (int64_t)rows ? (uint32_t)id : rows;
 }
 
-// Where pass p reads its keys: the caller's ids in the first pass, the workspace after.
+// Where a pass reads its (key, token) pairs: the caller's ids in the first pass, the
+// workspace after.
 template <typename ID>
 struct KeySource {
   const ID *ids;
-  const uint32_t *keys;   // NULL in the first pass
-  const uint32_t *perm;
+  const uint2 *pairs;     // NULL in the first pass
   uint32_t n, rows;
-  __device__ uint32_t key(uint32_t i) const { return keys ? keys[i] : key_of(ids, i, rows); }
-  __device__ uint32_t token(uint32_t i) const { return keys ? perm[i] : i; }
+  __device__ uint32_t key(uint32_t i) const { return pairs ? pairs[i].x : key_of(ids, i, rows); }
+  __device__ uint2 pair(uint32_t i) const { return pairs ? pairs[i] : make_uint2(key_of(ids, i, rows), i); }
 };
 
 // counts[digit][tile]; also clears the rows' segment bounds (each thread a share).
-template <typename ID>
+template <typename ID, int ITEMS>
 __global__ __launch_bounds__(ST_THREADS) void k_sort_count(KeySource<ID> src, int shift, int bits, uint32_t tiles,
                                                            uint32_t *__restrict__ counts, int2 *bounds,
                                                            uint32_t nbounds) {
   __shared__ uint32_t h[RADIX];
   for (int d = threadIdx.x; d < RADIX; d += ST_THREADS) h[d] = 0;
   __syncthreads();
-  const uint32_t mask = (1u << bits) - 1u, t0 = blockIdx.x * (uint32_t)ST_TILE;
+  const uint32_t mask = (1u << bits) - 1u, t0 = blockIdx.x * (uint32_t)(ST_THREADS * ITEMS);
 #pragma unroll
-  for (int j = 0; j < ST_ITEMS; j++) {
+  for (int j = 0; j < ITEMS; j++) {
     const uint32_t i = t0 + j * ST_THREADS + threadIdx.x;
     if (i < src.n) atomicAdd(&h[(src.key(i) >> shift) & mask], 1u);
   }
@@ -143,7 +146,8 @@ __global__ __launch_bounds__(ST_THREADS) void k_sort_scan(uint32_t *__restrict__
 // Rank of this lane's digit among the wave's items so far, adding the wave's items to
 // hist (this wave's counters). Lanes with equal digits find each other by one ballot
 // per bit; the lowest of them updates the counter. Inactive lanes pass ok = false.
-__device__ __forceinline__ uint32_t wave_rank(uint32_t digit, int bits, bool ok, volatile uint32_t *hist) {
+typedef volatile __attribute__((address_space(3))) uint32_t *LdsCounters;
+__device__ __forceinline__ uint32_t wave_rank(uint32_t digit, int bits, bool ok, LdsCounters hist) {
   uint64_t peers = ballot64(ok);
 #pragma unroll
   for (int b = 0; b < RADIX_BITS; b++) {
@@ -162,71 +166,86 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, int bits, bool ok,
   return old + (uint32_t)__popcll(below);
 }
 
-template <typename ID>
+// The tile's pairs are put in digit order in LDS first, so that a wave's store covers a
+// few runs of consecutive pairs instead of 64 places.
+template <typename ID, int ITEMS>
 __global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID> src, int shift, int bits, uint32_t tiles,
                                                              const uint32_t *__restrict__ counts,
                                                              const uint32_t *__restrict__ totals,
-                                                             uint32_t *__restrict__ keys_out,
-                                                             uint32_t *__restrict__ perm_out) {
-  __shared__ uint32_t hist[ST_WAVES][RADIX];
+                                                             uint2 *__restrict__ out) {
+  constexpr int ST_TILE = ST_THREADS * ITEMS;
+  __shared__ uint32_t hist[ST_WAVES][RADIX];   // a wave's counts, then its first place in the tile, per digit
+  __shared__ uint32_t away[RADIX];             // a digit's first place in the output less that in the tile
+  __shared__ uint2 tile[ST_TILE];
   __shared__ uint32_t s[ST_WAVES];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int d = threadIdx.x; d < ST_WAVES * RADIX; d += ST_THREADS) (&hist[0][0])[d] = 0;
-  const uint32_t mask = (1u << bits) - 1u;
-  const uint32_t i0 = blockIdx.x * (uint32_t)ST_TILE + w * (ST_TILE / ST_WAVES) + lane;
-  uint32_t key[ST_ITEMS], tok[ST_ITEMS], rank[ST_ITEMS];
+  const uint32_t mask = (1u << bits) - 1u, t0 = blockIdx.x * (uint32_t)ST_TILE;
+  const uint32_t i0 = t0 + w * (ST_TILE / ST_WAVES) + lane;
+  uint2 pair[ITEMS];
+  uint32_t rank[ITEMS];
 #pragma unroll
-  for (int j = 0; j < ST_ITEMS; j++) {
+  for (int j = 0; j < ITEMS; j++) {
     const uint32_t i = i0 + j * WAVE;
-    key[j] = i < src.n ? src.key(i) : 0u;
-    tok[j] = i < src.n ? src.token(i) : 0u;
+    pair[j] = i < src.n ? src.pair(i) : make_uint2(0u, 0u);
   }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < ST_ITEMS; j++)
-    rank[j] = wave_rank((key[j] >> shift) & mask, bits, i0 + j * WAVE < src.n, hist[w]);
-  // each digit's first slot for each wave: the digits before it in all tiles, its
-  // own items in earlier tiles, its items in earlier waves of this tile
   constexpr int DPT = RADIX / ST_THREADS;
-  uint32_t tot[DPT], sum = 0, all;
+  uint32_t tot[DPT], cnt[DPT], sum = 0, all;
 #pragma unroll
   for (int k = 0; k < DPT; k++) {
     const uint32_t d = threadIdx.x * DPT + k;
     tot[k] = d <= mask ? totals[d] : 0u;
+    cnt[k] = d <= mask ? counts[(size_t)d * tiles + blockIdx.x] : 0u;
     sum += tot[k];
-  }
-  uint32_t at = block_scan<ST_WAVES>(sum, s, &all) - sum;   // its barriers also end the ranking
-#pragma unroll
-  for (int k = 0; k < DPT; k++) {
-    const uint32_t d = threadIdx.x * DPT + k;
-    if (d <= mask) {
-      uint32_t run = at + counts[(size_t)d * tiles + blockIdx.x];
-#pragma unroll
-      for (int v = 0; v < ST_WAVES; v++) {
-        const uint32_t c = hist[v][d];
-        hist[v][d] = run;
-        run += c;
-      }
-    }
-    at += tot[k];
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < ST_ITEMS; j++) {
-    if (i0 + j * WAVE < src.n) {
-      const uint32_t p = hist[w][(key[j] >> shift) & mask] + rank[j];
-      keys_out[p] = key[j];
-      perm_out[p] = tok[j];
+  for (int j = 0; j < ITEMS; j++)
+    rank[j] = wave_rank((pair[j].x >> shift) & mask, bits, i0 + j * WAVE < src.n, (LdsCounters)hist[w]);
+  // first places: in the output, after the smaller digits of all tiles and the digit's
+  // earlier tiles; in the tile, after its smaller digits and the digit's earlier waves
+  uint32_t at = block_scan<ST_WAVES>(sum, s, &all) - sum;   // its barriers also end the ranking
+  uint32_t mine = 0;
+#pragma unroll
+  for (int k = 0; k < DPT; k++)
+#pragma unroll
+    for (int v = 0; v < ST_WAVES; v++) mine += hist[v][threadIdx.x * DPT + k];
+  uint32_t in_tile = block_scan<ST_WAVES>(mine, s, &all) - mine;
+#pragma unroll
+  for (int k = 0; k < DPT; k++) {
+    const uint32_t d = threadIdx.x * DPT + k;
+    away[d] = at + cnt[k] - in_tile;
+    at += tot[k];
+#pragma unroll
+    for (int v = 0; v < ST_WAVES; v++) {
+      const uint32_t c = hist[v][d];
+      hist[v][d] = in_tile;
+      in_tile += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++)
+    if (i0 + j * WAVE < src.n) tile[hist[w][(pair[j].x >> shift) & mask] + rank[j]] = pair[j];
+  __syncthreads();
+  const uint32_t m = src.n - t0 < ST_TILE ? src.n - t0 : ST_TILE;
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++) {
+    const uint32_t i = j * ST_THREADS + threadIdx.x;
+    if (i < m) {
+      const uint2 v = tile[i];
+      out[away[(v.x >> shift) & mask] + i] = v;
     }
   }
 }
 
-// Up to ST_TILE tokens: workgroup 0 sorts them in LDS, the others clear the bounds.
-constexpr int SM_THREADS = 1024, SM_WAVES = SM_THREADS / WAVE, SM_ITEMS = ST_TILE / SM_THREADS;
+// Up to 4096 tokens: workgroup 0 sorts them in LDS, the others clear the bounds. (With 16
+// tokens a thread its registers spill: 72 us for 16383 tokens, against 50 us of launches.)
+constexpr int SM_THREADS = 1024, SM_WAVES = SM_THREADS / WAVE, SM_ITEMS = 4;
 template <typename ID>
 __global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict__ ids, uint32_t n, uint32_t rows,
-                                                           int bits, int passes, uint32_t *__restrict__ keys_out,
-                                                           uint32_t *__restrict__ perm_out, int2 *bounds) {
+                                                           int bits, int passes, uint2 *__restrict__ out,
+                                                           int2 *bounds) {
   if (blockIdx.x > 0) {
     for (uint32_t r = (blockIdx.x - 1) * SM_THREADS + threadIdx.x; r < rows; r += (gridDim.x - 1) * SM_THREADS)
       bounds[r] = make_int2(0, 0);
@@ -234,9 +253,10 @@ __global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict_
   }
   __shared__ uint32_t hist[SM_WAVES][RADIX];
   __shared__ uint32_t s[SM_WAVES];
-  __shared__ uint32_t sk[ST_TILE], sp[ST_TILE];
+  __shared__ uint32_t sk[SM_THREADS * SM_ITEMS];
+  __shared__ uint16_t sp[SM_THREADS * SM_ITEMS];
   const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const uint32_t i0 = w * (ST_TILE / SM_WAVES) + lane;
+  const uint32_t i0 = w * (WAVE * SM_ITEMS) + lane;
   uint32_t key[SM_ITEMS], tok[SM_ITEMS], rank[SM_ITEMS];
 #pragma unroll
   for (int j = 0; j < SM_ITEMS; j++) {
@@ -252,7 +272,7 @@ __global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict_
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < SM_ITEMS; j++)
-      rank[j] = wave_rank((key[j] >> shift) & mask, dbits, i0 + j * WAVE < n, hist[w]);
+      rank[j] = wave_rank((key[j] >> shift) & mask, dbits, i0 + j * WAVE < n, (LdsCounters)hist[w]);
     __syncthreads();
     const uint32_t d = threadIdx.x;   // SM_THREADS >= RADIX
     uint32_t sum = 0, all;
@@ -271,7 +291,7 @@ __global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict_
       if (i0 + j * WAVE < n) {
         const uint32_t at = hist[w][(key[j] >> shift) & mask] + rank[j];
         sk[at] = key[j];
-        sp[at] = tok[j];
+        sp[at] = (uint16_t)tok[j];
       }
     __syncthreads();
 #pragma unroll
@@ -287,10 +307,7 @@ __global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict_
 #pragma unroll
   for (int j = 0; j < SM_ITEMS; j++) {
     const uint32_t i = i0 + j * WAVE;
-    if (i < n) {
-      keys_out[i] = key[j];
-      perm_out[i] = tok[j];
-    }
+    if (i < n) out[i] = make_uint2(key[j], tok[j]);
   }
 }
 
@@ -298,47 +315,83 @@ __global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict_
 // sums
 // ---------------------------------------------------------------------------
 // How a wave covers a row of `units` packs: 2^lg lanes per row (64 if the row has 64
-// packs or more, then one slice of 64 packs per wave), so 64 >> lg rows at once.
+// packs or more, then one slice of 64 packs per wave), so G = 64 >> lg rows at once.
 struct SumArgs {
   const void *dy;
   int64_t ldy;
-  const uint32_t *perm, *keys;
-  int2 *bounds;
+  const uint2 *sorted;      // (row, token) by row, then token
+  int2 *bounds;             // [rows] segment of each row in `sorted`, (0, 0) without tokens
   float *part1, *part2;     // sums of whole chunks of 64 and of 64 x 64 tokens [.][dim]
   void *grad;
   int64_t ldg;
-  uint32_t n, rows;
+  uint32_t n, rows, chunks;
   int dim, units, lg, slices, two_levels, accumulate;
   float scale;
 };
 
-// Adds rows [p0, p1) of a list to acc, the wave's 64 >> lg row lanes in turn: row lane
-// g takes p0 + g, p0 + g + G, ...; U loads in flight each. Rows are tokens of dy, found
-// through perm (src = T), or chunk sums (src = float, perm NULL).
-template <typename T, int VEC, int U>
-__device__ __forceinline__ void add_rows(const T *src, int64_t ld, const uint32_t *perm, uint32_t p0, uint32_t p1,
-                                         uint32_t g, uint32_t G, int col, bool on, float (&acc)[VEC]) {
-  for (uint32_t p = p0 + g; p < p1; p += U * G) {
+// This lane's place in a wave's share of the work.
+struct Place {
+  uint32_t lane, g, G;      // row lane and row lanes per wave
+  int col;
+  bool on;
+};
+template <int VEC>
+__device__ __forceinline__ Place place_of(const SumArgs &a, uint32_t slice) {
+  Place q;
+  q.lane = threadIdx.x & 63;
+  q.G = 64u >> a.lg;
+  q.g = q.lane >> a.lg;
+  const int unit = (int)(slice << 6) + (int)(q.lane & ((1u << a.lg) - 1u));
+  q.on = unit < a.units;
+  q.col = unit * VEC;
+  return q;
+}
+
+// Adds rows p0 .. p1 of `src` to acc, the wave's G row lanes in turn, U loads in flight
+// each; the rows are those of chunk sums, in order.
+template <int VEC, int U>
+__device__ __forceinline__ void add_sums(const float *src, int64_t ld, uint32_t p0, uint32_t p1, const Place &q,
+                                         float (&acc)[VEC]) {
+  for (uint32_t p = p0 + q.g; p < p1; p += U * q.G) {
     float v[U][VEC];
-    uint32_t at[U];
-#pragma unroll
-    for (int k = 0; k < U; k++) {
-      const uint32_t q = p + k * G;
-      at[k] = q < p1 ? (perm ? perm[q] : q) : 0u;
-    }
 #pragma unroll
     for (int k = 0; k < U; k++) {
 #pragma unroll
       for (int j = 0; j < VEC; j++) v[k][j] = 0.0f;
-      if (on && p + k * G < p1) {
-        if constexpr (sizeof(T) == 4 && VEC == 8) load_sums<VEC>((const float *)src + (int64_t)at[k] * ld + col, v[k]);
-        else load_f32<T, VEC>(src + (int64_t)at[k] * ld + col, v[k]);
-      }
+      if (q.on && p + k * q.G < p1) load_sums<VEC>(src + (int64_t)(p + k * q.G) * ld + q.col, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < U; k++)
 #pragma unroll
       for (int j = 0; j < VEC; j++) acc[j] += v[k][j];
+  }
+}
+
+// Adds the rows of dy of sorted tokens [p0, p1) to acc, the wave's G row lanes in turn.
+// The lanes fetch 64 token numbers at once and pass them round, so that only the rows
+// themselves are waited for. Every lane of the wave calls it.
+template <typename T, int VEC, int U>
+__device__ __forceinline__ void add_tokens(const SumArgs &a, uint32_t p0, uint32_t p1, const Place &q, float (&acc)[VEC]) {
+  const T *dy = (const T *)a.dy + q.col;
+  for (uint32_t b = p0; b < p1; b += 64) {
+    const uint32_t m = p1 - b < 64u ? p1 - b : 64u;
+    const uint32_t tok = q.lane < m ? a.sorted[b + q.lane].y : 0u;
+    for (uint32_t k0 = 0; k0 < m; k0 += U * q.G) {
+      Raw<T, VEC> x[U];
+#pragma unroll
+      for (int k = 0; k < U; k++) {
+        const uint32_t t = k0 + k * q.G + q.g;
+        const uint32_t at = __shfl(tok, (int)(t & 63u));
+        x[k] = load_if<T, VEC>(q.on && t < m, dy + (int64_t)at * a.ldy);
+      }
+#pragma unroll
+      for (int k = 0; k < U; k++) {
+        float v[VEC];
+        to_f32<T, VEC>(x[k], v);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) acc[j] += v[j];
+      }
+    }
   }
 }
 
@@ -350,58 +403,56 @@ __device__ __forceinline__ void join_row_lanes(float (&acc)[VEC], int lg) {
     for (int j = 0; j < VEC; j++) acc[j] += __shfl_xor(acc[j], o);
 }
 
+// Row loads in flight per lane (16: 30 -> 35 us for the chunk sums of 2M x 32 fp32).
+constexpr int DEEP = 8;
+
 // One wave per (chunk, slice): the bounds of the segments that begin or end in the
 // chunk, and the chunk's sum if one row holds all of it.
 template <typename T, int VEC>
-__device__ __forceinline__ void chunk_sum(const SumArgs &a, uint32_t c, uint32_t slice, uint32_t lane) {
-  const uint32_t p = c * CHUNK + lane;
-  const uint32_t key = p < a.n ? a.keys[p] : a.rows;
+__device__ __forceinline__ void chunk_sum(const SumArgs &a, uint32_t c, uint32_t slice) {
+  const Place q = place_of<VEC>(a, slice);
+  const uint32_t p = c * CHUNK + q.lane;
+  const uint32_t key = p < a.n ? a.sorted[p].x : a.rows;
   const uint32_t first = __shfl(key, 0), last = __shfl(key, 63);
   if (slice == 0 && key < a.rows) {
-    if (p == 0 || a.keys[p - 1] != key) a.bounds[key].x = (int)p;
-    if (p + 1 == a.n || a.keys[p + 1] != key) a.bounds[key].y = (int)p + 1;
+    if (p == 0 || a.sorted[p - 1].x != key) a.bounds[key].x = (int)p;
+    if (p + 1 == a.n || a.sorted[p + 1].x != key) a.bounds[key].y = (int)p + 1;
   }
   if (first != last || first >= a.rows) return;
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
-  const uint32_t G = 64u >> a.lg, g = lane >> a.lg;
-  const int unit = (int)(slice << 6) + (int)(lane & ((1u << a.lg) - 1u));
-  const bool on = unit < a.units;
-  add_rows<T, VEC, 8>((const T *)a.dy, a.ldy, a.perm, c * CHUNK, c * CHUNK + CHUNK, g, G, unit * VEC, on, acc);
+  add_tokens<T, VEC, DEEP>(a, c * CHUNK, c * CHUNK + CHUNK, q, acc);
   join_row_lanes<VEC>(acc, a.lg);
-  if (g == 0 && on) store_sums<VEC>(a.part1 + (size_t)c * a.dim + unit * VEC, acc);
+  if (q.g == 0 && q.on) store_sums<VEC>(a.part1 + (size_t)c * a.dim + q.col, acc);
 }
 
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void k_chunk_sums(SumArgs a) {
-  const uint32_t lane = threadIdx.x & 63;
-  const uint64_t waves = (uint64_t)((a.n + CHUNK - 1) / CHUNK) * a.slices;
+  const uint64_t waves = (uint64_t)a.chunks * a.slices;
   for (uint64_t wv = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); wv < waves; wv += (uint64_t)gridDim.x * 4)
-    chunk_sum<T, VEC>(a, (uint32_t)(wv / (uint32_t)a.slices), (uint32_t)(wv % (uint32_t)a.slices), lane);
+    chunk_sum<T, VEC>(a, (uint32_t)(wv / (uint32_t)a.slices), (uint32_t)(wv % (uint32_t)a.slices));
 }
+
 // The next level: one wave per (64 chunks, slice) that one row holds wholly.
 template <int VEC>
-__device__ __forceinline__ void chunk_sum2(const SumArgs &a, uint32_t c, uint32_t slice, uint32_t lane) {
-  const uint32_t first = a.keys[c * (CHUNK * CHUNK)], last = a.keys[c * (CHUNK * CHUNK) + CHUNK * CHUNK - 1];
+__device__ __forceinline__ void chunk_sum2(const SumArgs &a, uint32_t c, uint32_t slice) {
+  const Place q = place_of<VEC>(a, slice);
+  const uint32_t first = a.sorted[c * (CHUNK * CHUNK)].x, last = a.sorted[c * (CHUNK * CHUNK) + CHUNK * CHUNK - 1].x;
   if (first != last || first >= a.rows) return;
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
-  const uint32_t G = 64u >> a.lg, g = lane >> a.lg;
-  const int unit = (int)(slice << 6) + (int)(lane & ((1u << a.lg) - 1u));
-  const bool on = unit < a.units;
-  add_rows<float, VEC, 4>(a.part1, a.dim, nullptr, c * CHUNK, c * CHUNK + CHUNK, g, G, unit * VEC, on, acc);
+  add_sums<VEC, DEEP>(a.part1, a.dim, c * CHUNK, c * CHUNK + CHUNK, q, acc);
   join_row_lanes<VEC>(acc, a.lg);
-  if (g == 0 && on) store_sums<VEC>(a.part2 + (size_t)c * a.dim + unit * VEC, acc);
+  if (q.g == 0 && q.on) store_sums<VEC>(a.part2 + (size_t)c * a.dim + q.col, acc);
 }
 
 template <int VEC>
 __global__ __launch_bounds__(256) void k_chunk_sums2(SumArgs a) {
-  const uint32_t lane = threadIdx.x & 63;
   const uint64_t waves = (uint64_t)(a.n / (CHUNK * CHUNK)) * a.slices;
   for (uint64_t wv = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); wv < waves; wv += (uint64_t)gridDim.x * 4)
-    chunk_sum2<VEC>(a, (uint32_t)(wv / (uint32_t)a.slices), (uint32_t)(wv % (uint32_t)a.slices), lane);
+    chunk_sum2<VEC>(a, (uint32_t)(wv / (uint32_t)a.slices), (uint32_t)(wv % (uint32_t)a.slices));
 }
 
 template <typename T, int VEC>
@@ -415,60 +466,93 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t row, int co
 #pragma unroll
     for (int j = 0; j < VEC; j++) acc[j] += old[j];
   }
-  store_f32<T, VEC>(o, acc);
+  stream_f32<T, VEC>(o, acc);
 }
 
-// Every row of the gradient. A wave holds 64 >> lg rows, one per row lane; a row of at
-// most 64 tokens is summed by its own lanes, a longer one by the whole wave.
+// A row of more than 64 tokens, by a wave: its segment holds a multiple of 64, and the
+// first one's chunk stands for the row. Loose tokens at both ends, whole chunks between.
 template <typename T, int VEC>
-__device__ __forceinline__ void row_grads(const SumArgs &a, uint32_t row0, uint32_t slice, uint32_t lane) {
-  const uint32_t G = 64u >> a.lg, g = lane >> a.lg, row = row0 + g;
-  const int unit = (int)(slice << 6) + (int)(lane & ((1u << a.lg) - 1u));
-  const bool on = unit < a.units;
-  const int col = unit * VEC;
-  const int2 b = row < a.rows ? a.bounds[row] : make_int2(0, 0);
-  const T *dy = (const T *)a.dy;
-  const bool heavy = b.y - b.x > CHUNK;
+__device__ __forceinline__ void heavy_row(const SumArgs &a, uint32_t c, uint32_t slice) {
+  const uint32_t row = a.sorted[c * CHUNK].x;
+  if (row >= a.rows) return;
+  const int2 b = a.bounds[row];
+  const uint32_t s = (uint32_t)b.x, e = (uint32_t)b.y;
+  if (e - s <= CHUNK || (s + CHUNK - 1) / CHUNK != c) return;
+  const Place q = place_of<VEC>(a, slice);
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
-  if (!heavy) {
-    add_rows<T, VEC, 4>(dy, a.ldy, a.perm, (uint32_t)b.x, (uint32_t)b.y, 0, 1, col, on, acc);
-    if (row < a.rows && on && (b.y > b.x || !a.accumulate)) write_row<T, VEC>(a, row, col, acc);
+  const uint32_t c1 = e / CHUNK;
+  add_tokens<T, VEC, DEEP>(a, s, c * CHUNK, q, acc);
+  const uint32_t d0 = (c + CHUNK - 1) / CHUNK, d1 = c1 / CHUNK;
+  if (!a.two_levels || d0 >= d1) {
+    add_sums<VEC, DEEP>(a.part1, a.dim, c, c1, q, acc);
+  } else {
+    add_sums<VEC, DEEP>(a.part1, a.dim, c, d0 * CHUNK, q, acc);
+    add_sums<VEC, DEEP>(a.part2, a.dim, d0, d1, q, acc);
+    add_sums<VEC, DEEP>(a.part1, a.dim, d1 * CHUNK, c1, q, acc);
   }
-  uint64_t todo = ballot64(heavy);
-  while (todo) {
-    const uint32_t h = (uint32_t)__builtin_ctzll(todo) >> a.lg;
-    todo &= a.lg == 6 ? 0ull : ~(((1ull << (1u << a.lg)) - 1ull) << (h << a.lg));
-    const uint32_t s = (uint32_t)__shfl(b.x, (int)(h << a.lg)), e = (uint32_t)__shfl(b.y, (int)(h << a.lg));
+  add_tokens<T, VEC, DEEP>(a, c1 * CHUNK, e, q, acc);
+  join_row_lanes<VEC>(acc, a.lg);
+  if (q.g == 0 && q.on) write_row<T, VEC>(a, row, q.col, acc);
+}
+
+// Rows of at most 64 tokens, SETS sets of G in a wave: a set at a time, each row by its
+// own lanes. The bounds of all sets are fetched at once, so that rows without tokens wait
+// for nothing else. A wave's sets lie far apart, because neighbouring ids are often
+// alike: frequent ones come first in many tables.
+template <typename T, int VEC, int SETS>
+__device__ __forceinline__ void light_rows(const SumArgs &a, uint32_t set, uint32_t stride, uint32_t slice) {
+  const Place q = place_of<VEC>(a, slice);
+  int2 b[SETS];
+#pragma unroll
+  for (int u = 0; u < SETS; u++) {
+    const uint64_t row = ((uint64_t)set + (uint64_t)u * stride) * q.G + q.g;
+    b[u] = row < a.rows ? a.bounds[row] : make_int2(0, CHUNK + 1);
+  }
+#pragma unroll
+  for (int u = 0; u < SETS; u++) {
+    const uint32_t s = (uint32_t)b[u].x, e = (uint32_t)b[u].y;
+    if (e - s > CHUNK) continue;                   // another wave's, or past the end
+    float acc[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
-    uint32_t c0 = (s + CHUNK - 1) / CHUNK, c1 = e / CHUNK;
-    if (c0 >= c1) {
-      add_rows<T, VEC, 4>(dy, a.ldy, a.perm, s, e, g, G, col, on, acc);
-    } else {
-      add_rows<T, VEC, 4>(dy, a.ldy, a.perm, s, c0 * CHUNK, g, G, col, on, acc);
-      const uint32_t d0 = (c0 + CHUNK - 1) / CHUNK, d1 = c1 / CHUNK;
-      if (!a.two_levels || d0 >= d1) {
-        add_rows<float, VEC, 4>(a.part1, a.dim, nullptr, c0, c1, g, G, col, on, acc);
-      } else {
-        add_rows<float, VEC, 4>(a.part1, a.dim, nullptr, c0, d0 * CHUNK, g, G, col, on, acc);
-        add_rows<float, VEC, 4>(a.part2, a.dim, nullptr, d0, d1, g, G, col, on, acc);
-        add_rows<float, VEC, 4>(a.part1, a.dim, nullptr, d1 * CHUNK, c1, g, G, col, on, acc);
+    constexpr int U = 8;
+    for (uint32_t p = s; p < e; p += U) {
+      Raw<T, VEC> x[U];
+      uint32_t at[U];
+#pragma unroll
+      for (int k = 0; k < U; k++) at[k] = p + k < e ? a.sorted[p + k].y : 0u;
+#pragma unroll
+      for (int k = 0; k < U; k++)
+        x[k] = load_if<T, VEC>(q.on && p + k < e, (const T *)a.dy + (int64_t)at[k] * a.ldy + q.col);
+#pragma unroll
+      for (int k = 0; k < U; k++) {
+        float v[VEC];
+        to_f32<T, VEC>(x[k], v);
+#pragma unroll
+        for (int j = 0; j < VEC; j++) acc[j] += v[j];
       }
-      add_rows<T, VEC, 4>(dy, a.ldy, a.perm, c1 * CHUNK, e, g, G, col, on, acc);
     }
-    join_row_lanes<VEC>(acc, a.lg);
-    if (g == 0 && on) write_row<T, VEC>(a, row0 + h, col, acc);
+    if (q.on && (e > s || !a.accumulate)) write_row<T, VEC>(a, (set + u * stride) * q.G + q.g, q.col, acc);
   }
 }
 
-template <typename T, int VEC>
+// Every row of the gradient: first the waves that look for heavy rows, one per chunk and
+// slice, then those of the light rows.
+template <typename T, int VEC, int SETS>
 __global__ __launch_bounds__(256) void k_row_grads(SumArgs a) {
-  const uint32_t lane = threadIdx.x & 63, G = 64u >> a.lg;
-  const uint64_t waves = (uint64_t)((a.rows + G - 1) / G) * a.slices;
-  for (uint64_t wv = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); wv < waves; wv += (uint64_t)gridDim.x * 4)
-    row_grads<T, VEC>(a, (uint32_t)(wv / (uint32_t)a.slices) * G, (uint32_t)(wv % (uint32_t)a.slices), lane);
+  const uint32_t G = 64u >> a.lg, sets = (a.rows + G - 1) / G, stride = (sets + SETS - 1) / SETS;
+  const uint64_t heavy = a.n > CHUNK ? (uint64_t)a.chunks * a.slices : 0;
+  const uint64_t waves = heavy + (uint64_t)stride * a.slices;
+  for (uint64_t wv = (uint64_t)blockIdx.x * 4 + (threadIdx.x >> 6); wv < waves; wv += (uint64_t)gridDim.x * 4) {
+    if (wv < heavy) {
+      heavy_row<T, VEC>(a, (uint32_t)(wv / (uint32_t)a.slices), (uint32_t)(wv % (uint32_t)a.slices));
+    } else {
+      const uint64_t v = wv - heavy;
+      light_rows<T, VEC, SETS>(a, (uint32_t)(v / (uint32_t)a.slices), stride, (uint32_t)(v % (uint32_t)a.slices));
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -493,7 +577,8 @@ int run_lookup(const void *table, int64_t ldt, int64_t rows, int dim, const void
 }
 
 struct BwdLayout {
-  uint32_t *keys[2], *perm[2], *counts, *totals;
+  uint2 *pairs[2];
+  uint32_t *counts, *totals;
   int2 *bounds;
   float *part1, *part2;
   size_t bytes;
@@ -507,11 +592,9 @@ BwdLayout bwd_layout(void *base, int64_t n, int64_t rows, int dim) {
     p += ws_align(b);
     return (void *)q;
   };
-  const size_t tiles = (size_t)((n + ST_TILE - 1) / ST_TILE);
-  for (int k = 0; k < 2; k++) {
-    L.keys[k] = (uint32_t *)take(4 * (size_t)n);
-    L.perm[k] = (uint32_t *)take(4 * (size_t)n);
-  }
+  const int tile = ST_THREADS * tile_items(n);
+  const size_t tiles = (size_t)((n + tile - 1) / tile);
+  for (int k = 0; k < 2; k++) L.pairs[k] = (uint2 *)take(8 * (size_t)n);
   L.counts = (uint32_t *)take(4 * RADIX * tiles);
   L.totals = (uint32_t *)take(4 * RADIX);
   L.bounds = (int2 *)take(8 * (size_t)rows);
@@ -527,42 +610,49 @@ unsigned wave_grid(uint64_t waves) {
   return (unsigned)(b < (1u << 22) ? b : (1u << 22));
 }
 
-// Sorts the tokens by id: keys and tokens end in the returned half of the workspace.
+template <typename ID, int ITEMS>
+int sort_passes(const ID *ids, uint32_t n, uint32_t rows, int bits, int passes, const BwdLayout &L, int *half,
+                hipStream_t stream) {
+  constexpr uint32_t TOKENS = ST_THREADS * ITEMS;
+  const uint32_t tiles = (n + TOKENS - 1) / TOKENS;
+  const int dbits = (bits + passes - 1) / passes;
+  for (int p = 0; p < passes; p++) {
+    KeySource<ID> src;
+    src.ids = ids;
+    src.pairs = p ? L.pairs[(p - 1) & 1] : nullptr;
+    src.n = n;
+    src.rows = rows;
+    const int shift = p * dbits, b = bits - shift < dbits ? bits - shift : dbits;
+    hipLaunchKernelGGL((k_sort_count<ID, ITEMS>), dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, tiles, L.counts,
+                       p ? (int2 *)nullptr : L.bounds, rows);
+    SPLAT_LAUNCH_CHECK();
+    hipLaunchKernelGGL(k_sort_scan, dim3(1u << b), dim3(ST_THREADS), 0, stream, L.counts, tiles, L.totals);
+    SPLAT_LAUNCH_CHECK();
+    hipLaunchKernelGGL((k_sort_scatter<ID, ITEMS>), dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, tiles, L.counts,
+                       L.totals, L.pairs[p & 1]);
+    SPLAT_LAUNCH_CHECK();
+  }
+  *half = (passes - 1) & 1;
+  return SPLAT_OK;
+}
+
+// Sorts the tokens by id into pairs[*half].
 template <typename ID>
 int sort_tokens(const void *ids, uint32_t n, uint32_t rows, const BwdLayout &L, int *half, hipStream_t stream) {
   int bits = 1;
   while (bits < 32 && (rows >> bits)) bits++;        // keys 0 .. rows
   const int passes = (bits + RADIX_BITS - 1) / RADIX_BITS;
-  if (n <= ST_TILE) {
+  if (n <= 4 * SM_THREADS) {
     unsigned clear = (rows + 4 * SM_THREADS - 1) / (4 * SM_THREADS);
     clear = clear > 1024 ? 1024 : clear;
     hipLaunchKernelGGL((k_sort_small<ID>), dim3(1 + clear), dim3(SM_THREADS), 0, stream, (const ID *)ids, n, rows,
-                       bits, passes, L.keys[0], L.perm[0], L.bounds);
+                       bits, passes, L.pairs[0], L.bounds);
     SPLAT_LAUNCH_CHECK();
     *half = 0;
     return SPLAT_OK;
   }
-  const uint32_t tiles = (n + ST_TILE - 1) / ST_TILE;
-  const int dbits = (bits + passes - 1) / passes;
-  for (int p = 0; p < passes; p++) {
-    KeySource<ID> src;
-    src.ids = (const ID *)ids;
-    src.keys = p ? L.keys[(p - 1) & 1] : nullptr;
-    src.perm = p ? L.perm[(p - 1) & 1] : nullptr;
-    src.n = n;
-    src.rows = rows;
-    const int shift = p * dbits, b = bits - shift < dbits ? bits - shift : dbits;
-    hipLaunchKernelGGL((k_sort_count<ID>), dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, tiles, L.counts,
-                       p ? (int2 *)nullptr : L.bounds, rows);
-    SPLAT_LAUNCH_CHECK();
-    hipLaunchKernelGGL(k_sort_scan, dim3(1u << b), dim3(ST_THREADS), 0, stream, L.counts, tiles, L.totals);
-    SPLAT_LAUNCH_CHECK();
-    hipLaunchKernelGGL((k_sort_scatter<ID>), dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, tiles, L.counts,
-                       L.totals, L.keys[p & 1], L.perm[p & 1]);
-    SPLAT_LAUNCH_CHECK();
-  }
-  *half = (passes - 1) & 1;
-  return SPLAT_OK;
+  return tile_items(n) == 4 ? sort_passes<ID, 4>((const ID *)ids, n, rows, bits, passes, L, half, stream)
+                            : sort_passes<ID, 16>((const ID *)ids, n, rows, bits, passes, L, half, stream);
 }
 
 // Every row zero: no token to add.
@@ -592,15 +682,15 @@ int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_
   const int st = id_type == SPLAT_I64 ? sort_tokens<int64_t>(ids, a.n, a.rows, L, &half, stream)
                                       : sort_tokens<int32_t>(ids, a.n, a.rows, L, &half, stream);
   if (st) return st;
-  a.keys = L.keys[half];
-  a.perm = L.perm[half];
+  a.sorted = L.pairs[half];
+  a.chunks = (a.n + CHUNK - 1) / CHUNK;
   a.bounds = L.bounds;
   a.part1 = L.part1;
   a.part2 = L.part2;
   a.lg = 0;
   while (a.lg < 6 && (1 << a.lg) < a.units) a.lg++;
   a.slices = (a.units + 63) / 64;
-  const uint64_t w1 = (uint64_t)((a.n + CHUNK - 1) / CHUNK) * a.slices;
+  const uint64_t w1 = (uint64_t)a.chunks * a.slices;
   hipLaunchKernelGGL((k_chunk_sums<T, VEC>), dim3(wave_grid(w1)), dim3(256), 0, stream, a);
   SPLAT_LAUNCH_CHECK();
   // below two whole second-level chunks a row has at most 128 first-level sums: not worth a launch
@@ -610,9 +700,13 @@ int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_
     hipLaunchKernelGGL((k_chunk_sums2<VEC>), dim3(wave_grid(w2)), dim3(256), 0, stream, a);
     SPLAT_LAUNCH_CHECK();
   }
-  const uint32_t G = 64u >> a.lg;
-  const uint64_t wr = (uint64_t)((a.rows + G - 1) / G) * a.slices;
-  hipLaunchKernelGGL((k_row_grads<T, VEC>), dim3(wave_grid(wr)), dim3(256), 0, stream, a);
+  const uint32_t G = 64u >> a.lg, sets = (a.rows + G - 1) / G;
+  const uint64_t heavy = a.n > CHUNK ? a.chunks : 0;
+  if (a.n < a.rows) {      // most rows empty
+    hipLaunchKernelGGL((k_row_grads<T, VEC, 8>), dim3(wave_grid((heavy + (sets + 7) / 8) * a.slices)), dim3(256), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((k_row_grads<T, VEC, 1>), dim3(wave_grid((heavy + sets) * a.slices)), dim3(256), 0, stream, a);
+  }
   SPLAT_LAUNCH_CHECK();
   return SPLAT_OK;
 }
