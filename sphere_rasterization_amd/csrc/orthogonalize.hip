@@ -14,9 +14,9 @@
 // one 11-bit operand per factor is not enough. Every operand is kept as two fp16
 // parts, v S = hi + lo (22 bits and more; S a power of two from a bound on the
 // singular values, so that neither part leaves fp16's range), and a product is
-// hi hi + hi lo + lo hi on the matrix cores with fp32 sums: the dropped lo lo is below
-// 2^-23 of the product. Three fp16 products still run several times faster than one
-// in fp32, whose matrix rate on gfx950 is 1/16 of fp16's.
+// hi hi + hi lo + lo hi on the matrix cores with fp32 sums (with few rows also lo lo, which is
+// below 2^-22 of the product). Three fp16 products still run several times faster
+// than one in fp32, whose matrix rate on gfx950 is 1/16 of fp16's.
 //
 // Layout. A factor is stored in panels of 64 rows, a panel in blocks of 16 values of the
 // summed axis, and in a block each row's 16 hi then 16 lo parts: 64 bytes. So a block is
@@ -176,7 +176,8 @@ struct Tile {
   static constexpr int LDS = RING > 4 * PATCH ? RING : 4 * PATCH;
 
   static __device__ __forceinline__ void product(const _Float16 *p0, const _Float16 *q0, int K, int it, int jt,
-                                                 int k0, int k1, half8 *lds, float16v (&acc)[F][F]) {
+                                                 int k0, int k1, bool one_tile, half8 *lds,
+                                                 float16v (&acc)[F][F]) {
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = (w & 1) * (TL / 2), wj = (w >> 1) * (TL / 2);
     const int64_t panel = (int64_t)(K / KB) * BLOCK;
@@ -222,9 +223,27 @@ struct Tile {
         }
       }
     };
+    // 64 x 64 tiles wait for memory rather than for the matrix cores and can afford sums of
+    // their own for the small products. Where one tile holds all rows, lo lo is among them:
+    // with few rows and long sums it is a good part of the error (8 x 2048 fp32: 1.9 times
+    // that of fp32 products without, 1.2 with; all tiles with it: 1000 x 777 bf16 from 165
+    // to 177 us).
+    float16v small[F][F];
+#pragma unroll
+    for (int i = 0; i < F; i++)
+#pragma unroll
+      for (int j = 0; j < F; j++) small[i][j] = acc[i][j];
     auto multiply = [&](int set) {
 #pragma unroll
       for (int u = 0; u < SUB; u++) {
+        if constexpr (F == 1) {
+          if (one_tile)
+            small[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[set][u][0], ql[set][u][0], small[0][0], 0, 0, 0);
+          acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[set][u][0], qh[set][u][0], acc[0][0], 0, 0, 0);
+          small[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl[set][u][0], qh[set][u][0], small[0][0], 0, 0, 0);
+          small[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph[set][u][0], ql[set][u][0], small[0][0], 0, 0, 0);
+          continue;
+        }
 #pragma unroll
         for (int i = 0; i < F; i++)
 #pragma unroll
@@ -260,10 +279,33 @@ struct Tile {
       __builtin_amdgcn_sched_barrier(0);
       slot = next;
     };
+    // The matrix cores' running sums lose bits as they grow: every 256 values they are
+    // added to the total and start again.
+    float16v total[F][F];
+#pragma unroll
+    for (int i = 0; i < F; i++)
+#pragma unroll
+      for (int j = 0; j < F; j++) total[i][j] = acc[i][j];
+    constexpr int FLUSH = 256 / (KB * SUB);
     for (int k = k0; k < k1; k += 2) {               // an even number of steps
       step(k, 0);
       step(k + 1, 1);
+      if ((k - k0) % FLUSH == FLUSH - 2) {
+#pragma unroll
+        for (int i = 0; i < F; i++)
+#pragma unroll
+          for (int j = 0; j < F; j++)
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              total[i][j][e] += acc[i][j][e];
+              acc[i][j][e] = 0.0f;
+            }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < F; i++)
+#pragma unroll
+      for (int j = 0; j < F; j++) acc[i][j] += total[i][j] + small[i][j];
     // nothing may land in LDS after this
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
@@ -285,12 +327,17 @@ struct Tile {
 #pragma unroll
       for (int e4 = 0; e4 < 4; e4++) {
         const int I0 = I + e4 * 8 + fk * 4;
+        half4 ah, al;                                  // A (symmetric) at row J, values I0 .. I0 + 3
+        if constexpr (EPI == EPI_POLY) {
+          const _Float16 *a = g.a + mat * g.db + packed(J, I0, g.ld0);
+          ah = *reinterpret_cast<const half4 *>(a);
+          al = *reinterpret_cast<const half4 *>(a + KB);
+        }
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           float v = acc[j][e4 * 4 + e] * g.mul;
           if constexpr (EPI == EPI_POLY) {
-            const _Float16 *a = g.a + mat * g.db + packed(I0 + e, J, g.ld0);
-            v = __builtin_fmaf(g.cb, (float)a[0] + (float)a[KB], v);
+            v = __builtin_fmaf(g.cb, (float)ah[e] + (float)al[e], v);
             if (I0 + e == J) v += g.ca;
           }
           if constexpr (EPI == EPI_LAST) {
@@ -376,7 +423,7 @@ __global__ __launch_bounds__(OR_THREADS, 2) void k_ortho_gemm(GemmArgs g) {
     jt = blockIdx.x / g.ti;
   }
   float16v acc[Tl::F][Tl::F];
-  Tl::product(g.p + mat * g.pb, g.q + mat * g.qb, g.K, it, jt, 0, g.K / (KB * SUB), lds, acc);
+  Tl::product(g.p + mat * g.pb, g.q + mat * g.qb, g.K, it, jt, 0, g.K / (KB * SUB), g.ti == 1, lds, acc);
   const int w = threadIdx.x >> 6;
 #pragma unroll
   for (int i = 0; i < Tl::F; i++)
@@ -401,7 +448,7 @@ __global__ __launch_bounds__(OR_THREADS, 2) void k_ortho_pieces(GemmArgs g) {
     int it, jt;
     lower_tile((int)(t - mat * g.tiles), it, jt);
     float16v acc[Tl::F][Tl::F];
-    Tl::product(g.p + mat * g.pb, g.q + mat * g.qb, g.K, it, jt, 2 * from, 2 * to, lds, acc);
+    Tl::product(g.p + mat * g.pb, g.q + mat * g.qb, g.K, it, jt, 2 * from, 2 * to, g.ti == 1, lds, acc);
     float4 *o = reinterpret_cast<float4 *>(g.part + ((int64_t)run + t) * TL * TL) + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < Tl::F; i++)
@@ -510,6 +557,7 @@ __device__ __forceinline__ float4v small_product(const _Float16 *p, int RP, int 
     const half8 qh = *reinterpret_cast<const half8 *>(q + small_at(RQ, b, rj, fk));
     const half8 ph = *reinterpret_cast<const half8 *>(p + small_at(RP, b, ri, fk));
     const half8 ql = *reinterpret_cast<const half8 *>(q + small_at(RQ, b, rj, fk + 4));
+    cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, ql, cross, 0, 0, 0);
     cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(pl, qh, cross, 0, 0, 0);
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, qh, acc, 0, 0, 0);
     cross = __builtin_amdgcn_mfma_f32_16x16x32_f16(ph, ql, cross, 0, 0, 0);
