@@ -324,7 +324,7 @@ int splat_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t ta
  * every row written (accumulate = 0) or added to (accumulate = 1). d_out [n][dim] and
  * d_table [rows][dim] are of one dtype; sums are fp32. The tokens are sorted by id
  * inside the call. n < 2^31, rows < 2^31 - 1, dim <= 65536.
- * workspace: [splat_lookup_bwd_workspace_bytes] device bytes. */
+ * workspace: [splat_lookup_bwd_workspace_bytes] device bytes (none for few tokens). */
 size_t splat_lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim);
 int splat_lookup_bwd(const void *d_out, int dtype, int64_t d_out_stride, const void *ids, int itype, int64_t n,
                      int64_t rows, int dim, float scale, void *d_table, int64_t d_table_stride, int accumulate,

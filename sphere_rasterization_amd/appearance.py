@@ -43,21 +43,13 @@ def _like(name: str, t: torch.Tensor, ref: torch.Tensor, shape, dtypes):
                          f"got {tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
-class _Launch:
-    """The current stream of a tensor's GPU, with that GPU current for the launches."""
-
-    def __init__(self, t: torch.Tensor):
-        self.dev = t.device.index
-        self.prev = torch.cuda.current_device()
-
-    def __enter__(self):
-        if self.dev != self.prev:
-            torch.cuda.set_device(self.dev)
-        return torch._C._cuda_getCurrentRawStream(self.dev)
-
-    def __exit__(self, *exc):
-        if self.dev != self.prev:
-            torch.cuda.set_device(self.prev)
+def _launch(t: torch.Tensor, fn, *args):
+    """fn(*args, stream) on the current stream of t's GPU, with that GPU current."""
+    dev = t.get_device()
+    if dev == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _workspace(nbytes: int, ref: torch.Tensor) -> Tuple[Optional[torch.Tensor], Optional[int], int]:
@@ -91,9 +83,8 @@ def _lookup(table: torch.Tensor, ids: torch.Tensor, scale: float) -> torch.Tenso
     table, flat = _rows(table), ids.contiguous()
     rows, dim = table.shape
     out = torch.empty(tuple(ids.shape) + (dim,), dtype=table.dtype, device=table.device)
-    with _Launch(table) as stream:
-        L.splat_lookup(table.data_ptr(), dt, rows, dim, table.stride(0), flat.data_ptr(), it, flat.numel(), scale,
-                       out.data_ptr(), dim, stream)
+    _launch(table, L.splat_lookup, table.data_ptr(), dt, rows, dim, table.stride(0), flat.data_ptr(), it, flat.numel(),
+            scale, out.data_ptr(), dim)
     return out
 
 
@@ -118,9 +109,8 @@ def lookup_backward(d_out: torch.Tensor, ids: torch.Tensor, rows: int, scale: fl
     n = ids.numel()
     dy, flat = _rows(d_out.reshape(n, dim)), ids.contiguous()
     _keep, ws, nbytes = _workspace(L.splat_lookup_bwd_workspace_bytes(n, rows, dim), d_out)
-    with _Launch(d_out) as stream:
-        L.splat_lookup_bwd(dy.data_ptr(), dt, dy.stride(0), flat.data_ptr(), it, n, rows, dim, scale, out.data_ptr(),
-                           out.stride(0), 1 if accumulate else 0, ws, nbytes, stream)
+    _launch(d_out, L.splat_lookup_bwd, dy.data_ptr(), dt, dy.stride(0), flat.data_ptr(), it, n, rows, dim, scale,
+            out.data_ptr(), out.stride(0), 1 if accumulate else 0, ws, nbytes)
     return out
 
 
@@ -207,8 +197,7 @@ def _group_norm(x, groups, weight, bias, eps, act, keep: bool):
     else:                                    # one allocation: the workspace, then the statistics
         stats, ws, _n = _workspace(nbytes + 2 * one, x)
         mean = (ws or 0) + nbytes
-    with _Launch(x) as stream:
-        L.splat_group_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean, mean + one, ws, nbytes, stream)
+    _launch(x, L.splat_group_norm, d, x.data_ptr(), _ptr(weight), _ptr(bias), y.data_ptr(), mean, mean + one, ws, nbytes)
     return y, stats
 
 
@@ -241,9 +230,8 @@ def group_norm_backward(d_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, 
     db = torch.empty(d.channels, dtype=kind, device=x.device) if "bias" in want else None
     d.dx_image_stride, d.dx_pixel_stride = d.pixels * d.channels, d.channels
     _keep, ws, nbytes = _workspace(L.splat_group_norm_workspace_bytes(d, True), x)
-    with _Launch(x) as stream:
-        L.splat_group_norm_bwd(d, d_y.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
-                               _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db), ws, nbytes, stream)
+    _launch(x, L.splat_group_norm_bwd, d, d_y.data_ptr(), x.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(weight),
+            _ptr(bias), _ptr(dx), _ptr(dw), _ptr(db), ws, nbytes)
     return dx, dw, db
 
 
@@ -297,7 +285,6 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = (3.
         m = m.contiguous()
     batch = m.shape[0]
     _keep, ws, nbytes = _workspace(L.splat_orthogonalize_workspace_bytes(batch, rows, cols), g)
-    with _Launch(g) as stream:
-        L.splat_orthogonalize(m.data_ptr(), dt, batch, rows, cols, m.stride(0), m.stride(1), steps, *map(float, coeffs),
-                              float(eps), float(scale), out.data_ptr(), rows * cols, cols, ws, nbytes, stream)
+    _launch(g, L.splat_orthogonalize, m.data_ptr(), dt, batch, rows, cols, m.stride(0), m.stride(1), steps,
+            *map(float, coeffs), float(eps), float(scale), out.data_ptr(), rows * cols, cols, ws, nbytes)
     return out

@@ -569,9 +569,9 @@ int splat_lookup_bwd(const void *d_out, int dtype, int64_t d_out_stride, const v
   CHECK(stride_fits(d_out_stride, n) && stride_fits(d_table_stride, rows), SPLAT_ERR_INVALID_ARG, "row stride");
   CHECK(aligned_to(d_out, dtype) && aligned_to(d_table, dtype) && aligned_ids(ids, itype), SPLAT_ERR_INVALID_ARG,
         "array not aligned to its element");
-  if (n > 0) {
+  if (const size_t need = lookup_bwd_workspace_bytes(n, rows, dim)) {
     CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
-    CHECK(ws_bytes >= lookup_bwd_workspace_bytes(n, rows, dim), SPLAT_ERR_CAPACITY, "lookup workspace too small");
+    CHECK(ws_bytes >= need, SPLAT_ERR_CAPACITY, "lookup workspace too small");
   }
   return launch_lookup_bwd(d_out, dtype, n <= 1 ? dim : d_out_stride, ids, itype, n, rows, dim, scale, d_table,
                            rows == 1 ? dim : d_table_stride, accumulate, workspace, stream);

@@ -10,7 +10,7 @@
 // row is summed in a fixed order:
 //   1. counting sort by digits of up to 9 bits, least significant first: counts per
 //      tile of 1024 or 4096 tokens, a scan per digit, a scatter that ranks equal digits
-//      within a wave by ballots. Up to 4096 tokens: one workgroup, all in LDS;
+//      within a wave by ballots;
 //   2. the sorted list is cut into chunks of 64; a chunk that lies within one row's
 //      segment is summed to one fp32 row, and 64 such sums to one of the next level;
 //   3. each row is written by adding its tokens, or its loose tokens and whole chunks.
@@ -236,78 +236,6 @@ __global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID> src, 
       const uint2 v = tile[i];
       out[away[(v.x >> shift) & mask] + i] = v;
     }
-  }
-}
-
-// Up to 4096 tokens: workgroup 0 sorts them in LDS, the others clear the bounds. (With 16
-// tokens a thread its registers spill: 72 us for 16383 tokens, against 50 us of launches.)
-constexpr int SM_THREADS = 1024, SM_WAVES = SM_THREADS / WAVE, SM_ITEMS = 4;
-template <typename ID>
-__global__ __launch_bounds__(SM_THREADS) void k_sort_small(const ID *__restrict__ ids, uint32_t n, uint32_t rows,
-                                                           int bits, int passes, uint2 *__restrict__ out,
-                                                           int2 *bounds) {
-  if (blockIdx.x > 0) {
-    for (uint32_t r = (blockIdx.x - 1) * SM_THREADS + threadIdx.x; r < rows; r += (gridDim.x - 1) * SM_THREADS)
-      bounds[r] = make_int2(0, 0);
-    return;
-  }
-  __shared__ uint32_t hist[SM_WAVES][RADIX];
-  __shared__ uint32_t s[SM_WAVES];
-  __shared__ uint32_t sk[SM_THREADS * SM_ITEMS];
-  __shared__ uint16_t sp[SM_THREADS * SM_ITEMS];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const uint32_t i0 = w * (WAVE * SM_ITEMS) + lane;
-  uint32_t key[SM_ITEMS], tok[SM_ITEMS], rank[SM_ITEMS];
-#pragma unroll
-  for (int j = 0; j < SM_ITEMS; j++) {
-    const uint32_t i = i0 + j * WAVE;
-    key[j] = i < n ? key_of(ids, i, rows) : 0u;
-    tok[j] = i;
-  }
-  const int dbits = (bits + passes - 1) / passes;
-  for (int p = 0; p < passes; p++) {
-    const int shift = p * dbits;
-    const uint32_t mask = (1u << dbits) - 1u;
-    for (int d = threadIdx.x; d < SM_WAVES * RADIX; d += SM_THREADS) (&hist[0][0])[d] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < SM_ITEMS; j++)
-      rank[j] = wave_rank((key[j] >> shift) & mask, dbits, i0 + j * WAVE < n, (LdsCounters)hist[w]);
-    __syncthreads();
-    const uint32_t d = threadIdx.x;   // SM_THREADS >= RADIX
-    uint32_t sum = 0, all;
-    if (d < RADIX)
-      for (int v = 0; v < SM_WAVES; v++) sum += hist[v][d];
-    uint32_t run = block_scan<SM_WAVES>(sum, s, &all) - sum;
-    if (d < RADIX)
-      for (int v = 0; v < SM_WAVES; v++) {
-        const uint32_t c = hist[v][d];
-        hist[v][d] = run;
-        run += c;
-      }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < SM_ITEMS; j++)
-      if (i0 + j * WAVE < n) {
-        const uint32_t at = hist[w][(key[j] >> shift) & mask] + rank[j];
-        sk[at] = key[j];
-        sp[at] = (uint16_t)tok[j];
-      }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < SM_ITEMS; j++) {
-      const uint32_t i = i0 + j * WAVE;
-      if (i < n) {
-        key[j] = sk[i];
-        tok[j] = sp[i];
-      }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int j = 0; j < SM_ITEMS; j++) {
-    const uint32_t i = i0 + j * WAVE;
-    if (i < n) out[i] = make_uint2(key[j], tok[j]);
   }
 }
 
@@ -556,6 +484,131 @@ __global__ __launch_bounds__(256) void k_row_grads(SumArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+// The whole gradient in one launch for up to FEW tokens: a workgroup owns a run of rows
+// (and a slice of 64 packs), keeps the tokens whose ids fall in it, in order, in LDS, and
+// sums row by row. Short lists go a row to a wave; long ones (many tokens in few rows) a
+// row to the whole workgroup, each wave taking every eighth part of 64 entries. Nothing is
+// sorted, and no workspace is needed. What bounds it is its chain of waits: ids, rows,
+// stores.
+constexpr int FW_THREADS = 512, FW_WAVES = FW_THREADS / WAVE, FW_ITEMS = 8;
+constexpr int FEW = FW_THREADS * FW_ITEMS;
+constexpr int FW_LONG = 256;               // entries from which the workgroup works together
+constexpr uint32_t FW_RUNS = 1024;         // runs of rows, at most
+
+// Adds the rows of the tokens buf[0 .. m), m <= 64, to acc, the wave's row lanes in turn.
+template <typename T, int VEC>
+__device__ __forceinline__ void add_few(const SumArgs &a, const uint16_t *buf, uint32_t m, const Place &q, float (&acc)[VEC]) {
+  const T *dy = (const T *)a.dy + q.col;
+  for (uint32_t k0 = 0; k0 < m; k0 += DEEP * q.G) {
+    Raw<T, VEC> x[DEEP];
+#pragma unroll
+    for (int k = 0; k < DEEP; k++) {
+      const uint32_t t = k0 + k * q.G + q.g;
+      x[k] = load_if<T, VEC>(q.on && t < m, dy + (int64_t)(t < m ? buf[t] : 0) * a.ldy);
+    }
+#pragma unroll
+    for (int k = 0; k < DEEP; k++) {
+      float v[VEC];
+      to_f32<T, VEC>(x[k], v);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) acc[j] += v[j];
+    }
+  }
+}
+
+template <typename T, int VEC, typename ID>
+__global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *__restrict__ ids, uint32_t run) {
+  __shared__ uint32_t s_row[FEW];            // row within the run, then token, of each entry
+  __shared__ uint16_t s_tok[FEW];
+  __shared__ uint16_t s_buf[FW_WAVES][128];
+  __shared__ uint32_t s_cnt[FW_WAVES];
+  __shared__ float s_sum[FW_WAVES][WAVE * VEC];
+  const uint32_t r0 = blockIdx.x * run, rows = a.rows - r0 < run ? a.rows - r0 : run;
+  const Place q = place_of<VEC>(a, blockIdx.y);
+  const uint32_t w = threadIdx.x >> 6, i0 = w * (WAVE * FW_ITEMS) + q.lane;
+  uint32_t row[FW_ITEMS], rank[FW_ITEMS], mine = 0;
+#pragma unroll
+  for (int j = 0; j < FW_ITEMS; j++) {
+    const uint32_t i = i0 + j * WAVE;
+    row[j] = i < a.n ? key_of(ids, i, a.rows) - r0 : ~0u;   // ids outside lie past every run
+  }
+#pragma unroll
+  for (int j = 0; j < FW_ITEMS; j++) {
+    const uint64_t m = ballot64(row[j] < rows);
+    rank[j] = mine + (uint32_t)__popcll(m & ((1ull << q.lane) - 1ull));
+    mine += (uint32_t)__popcll(m);
+  }
+  if (q.lane == 0) s_cnt[w] = mine;
+  __syncthreads();
+  uint32_t base = 0, len = 0;
+#pragma unroll
+  for (uint32_t k = 0; k < FW_WAVES; k++) {
+    if (k < w) base += s_cnt[k];
+    len += s_cnt[k];
+  }
+#pragma unroll
+  for (int j = 0; j < FW_ITEMS; j++)
+    if (row[j] < rows) {
+      s_row[base + rank[j]] = row[j];
+      s_tok[base + rank[j]] = (uint16_t)(i0 + j * WAVE);
+    }
+  __syncthreads();
+  if (len == 0) {                              // no token here: G rows to a store
+    if (a.accumulate || !q.on) return;
+    for (uint32_t r = w * q.G + q.g; r < rows; r += FW_WAVES * q.G) {
+      float zero[VEC] = {};
+      stream_f32<T, VEC>((T *)a.grad + (int64_t)(r0 + r) * a.ldg + q.col, zero);
+    }
+    return;
+  }
+  const bool together = len > FW_LONG;
+  uint16_t *buf = s_buf[w];
+  for (uint32_t r = together ? 0 : w; r < rows; r += together ? 1 : FW_WAVES) {
+    float acc[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
+    uint32_t held = 0, seen = 0;               // tokens waiting in buf, and found in all
+    for (uint32_t p = together ? w * 64 : 0; p < len; p += together ? FW_WAVES * 64 : 64) {
+      const bool hit = p + q.lane < len && s_row[p + q.lane] == r;
+      const uint64_t m = ballot64(hit);
+      if (hit) buf[held + (uint32_t)__popcll(m & ((1ull << q.lane) - 1ull))] = s_tok[p + q.lane];
+      held += (uint32_t)__popcll(m);
+      seen += (uint32_t)__popcll(m);
+      __builtin_amdgcn_wave_barrier();
+      if (held >= 64) {
+        add_few<T, VEC>(a, buf, 64, q, acc);
+        const uint16_t rest = buf[64 + q.lane];
+        __builtin_amdgcn_wave_barrier();
+        held -= 64;
+        if (q.lane < held) buf[q.lane] = rest;
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+    if (held) add_few<T, VEC>(a, buf, held, q, acc);
+    __builtin_amdgcn_wave_barrier();
+    if (seen) join_row_lanes<VEC>(acc, a.lg);
+    if (together) {
+      __syncthreads();                         // the last row's sums have been read
+#pragma unroll
+      for (int j = 0; j < VEC; j++) s_sum[w][q.lane * VEC + j] = acc[j];
+      if (q.lane == 0) s_cnt[w] = seen;
+      __syncthreads();
+      if (w > 0) continue;
+      seen = 0;
+#pragma unroll
+      for (uint32_t k = 0; k < FW_WAVES; k++) seen += s_cnt[k];
+#pragma unroll
+      for (uint32_t k = 1; k < FW_WAVES; k++)
+#pragma unroll
+        for (int j = 0; j < VEC; j++) acc[j] += s_sum[k][q.lane * VEC + j];
+    }
+    if (q.g == 0 && q.on && (seen || !a.accumulate)) write_row<T, VEC>(a, r0 + r, q.col, acc);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, typename ID>
@@ -642,15 +695,6 @@ int sort_tokens(const void *ids, uint32_t n, uint32_t rows, const BwdLayout &L, 
   int bits = 1;
   while (bits < 32 && (rows >> bits)) bits++;        // keys 0 .. rows
   const int passes = (bits + RADIX_BITS - 1) / RADIX_BITS;
-  if (n <= 4 * SM_THREADS) {
-    unsigned clear = (rows + 4 * SM_THREADS - 1) / (4 * SM_THREADS);
-    clear = clear > 1024 ? 1024 : clear;
-    hipLaunchKernelGGL((k_sort_small<ID>), dim3(1 + clear), dim3(SM_THREADS), 0, stream, (const ID *)ids, n, rows,
-                       bits, passes, L.pairs[0], L.bounds);
-    SPLAT_LAUNCH_CHECK();
-    *half = 0;
-    return SPLAT_OK;
-  }
   return tile_items(n) == 4 ? sort_passes<ID, 4>((const ID *)ids, n, rows, bits, passes, L, half, stream)
                             : sort_passes<ID, 16>((const ID *)ids, n, rows, bits, passes, L, half, stream);
 }
@@ -677,6 +721,19 @@ int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_
     SPLAT_LAUNCH_CHECK();
     return SPLAT_OK;
   }
+  a.lg = 0;
+  while (a.lg < 6 && (1 << a.lg) < a.units) a.lg++;
+  a.slices = (a.units + 63) / 64;
+  if (a.n <= FEW) {
+    const uint32_t run = (a.rows + FW_RUNS - 1) / FW_RUNS;
+    const dim3 grid((a.rows + run - 1) / run, (unsigned)a.slices);
+    if (id_type == SPLAT_I64)
+      hipLaunchKernelGGL((k_few_grads<T, VEC, int64_t>), grid, dim3(FW_THREADS), 0, stream, a, (const int64_t *)ids, run);
+    else
+      hipLaunchKernelGGL((k_few_grads<T, VEC, int32_t>), grid, dim3(FW_THREADS), 0, stream, a, (const int32_t *)ids, run);
+    SPLAT_LAUNCH_CHECK();
+    return SPLAT_OK;
+  }
   const BwdLayout L = bwd_layout(ws, a.n, a.rows, a.dim);
   int half = 0;
   const int st = id_type == SPLAT_I64 ? sort_tokens<int64_t>(ids, a.n, a.rows, L, &half, stream)
@@ -687,9 +744,6 @@ int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_
   a.bounds = L.bounds;
   a.part1 = L.part1;
   a.part2 = L.part2;
-  a.lg = 0;
-  while (a.lg < 6 && (1 << a.lg) < a.units) a.lg++;
-  a.slices = (a.units + 63) / 64;
   const uint64_t w1 = (uint64_t)a.chunks * a.slices;
   hipLaunchKernelGGL((k_chunk_sums<T, VEC>), dim3(wave_grid(w1)), dim3(256), 0, stream, a);
   SPLAT_LAUNCH_CHECK();
@@ -739,7 +793,9 @@ int launch_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t l
 #undef GO
 }
 
-size_t lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim) { return bwd_layout(nullptr, n, rows, dim).bytes; }
+size_t lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim) {
+  return n <= FEW ? 0 : bwd_layout(nullptr, n, rows, dim).bytes;
+}
 
 int launch_lookup_bwd(const void *d_out, int dtype, int64_t ldy, const void *ids, int id_type, int64_t n, int64_t rows,
                       int dim, float scale, void *d_table, int64_t ldg, int accumulate, void *ws, hipStream_t stream) {

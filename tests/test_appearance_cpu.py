@@ -37,6 +37,7 @@ def test_size_queries():
     need = L.splat_lookup_bwd_workspace_bytes(n, rows, dim)
     assert need >= 16 * n + 8 * rows + 4 * dim * (n // 64)
     assert L.splat_lookup_bwd_workspace_bytes(-1, rows, dim) == 0
+    assert L.splat_lookup_bwd_workspace_bytes(1000, rows, dim) == 0       # one launch, no workspace
     assert L.splat_group_norm_workspace_bytes(_norm(pixels=1 << 20), False) >= 2 * 2 * 8
     assert L.splat_group_norm_workspace_bytes(_norm(pixels=1 << 20), True) >= 2 * 8 * 8
     assert L.splat_group_norm_workspace_bytes(_norm(groups=3, pixels=1 << 20), False) == 0
@@ -61,7 +62,7 @@ def test_lookup_refusals(change):
     (dict(d_table=None), -1), (dict(ldy=7), -1), (dict(ldg=7), -1), (dict(ws=None), -1), (dict(ws=C.c_void_p(264)), -1),
     (dict(nbytes=100), -2)])
 def test_lookup_bwd_refusals(change, code):
-    a = dict(d_out=P, dtype=0, ldy=8, ids=P, itype=0, n=10, rows=100, dim=8, scale=1.0, d_table=P, ldg=8, accumulate=0,
+    a = dict(d_out=P, dtype=0, ldy=8, ids=P, itype=0, n=10_000, rows=100, dim=8, scale=1.0, d_table=P, ldg=8, accumulate=0,
              ws=P, nbytes=1 << 30)
     a.update(change)
     assert L.lib().splat_lookup_bwd(*a.values(), None) == code

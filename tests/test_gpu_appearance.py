@@ -112,6 +112,24 @@ def test_lookup_large_and_skewed(dev):
     _check(got, ref, (8 + 256 + n / 4096) * U * mag + U * np.abs(ref), "table gradient")
 
 
+def test_lookup_few_tokens_in_one_row(dev):
+    """The one-launch form with most of its tokens in one row, at the ends of its range."""
+    from sphere_rasterization_amd import appearance as A
+    rng = np.random.default_rng(13)
+    for n, rows, dim in ((4096, 5, 3), (4096, 3000, 70), (4095, 100_000, 1), (300, 1, 600), (257, 2, 33), (4097, 9, 20)):
+        ids = np.where(rng.random(n) < 0.9, rows // 2, rng.integers(0, rows, n)).astype(np.int32)
+        dy = _put(rng.standard_normal((n, dim)), "f32", dev)
+        t = torch.from_numpy(ids).to(dev)
+        got = A.lookup_backward(dy, t, rows)
+        ref, mag = O.lookup_backward(_np(dy), ids, rows), O.lookup_backward(np.abs(_np(dy)), ids, rows)
+        # depth: eight waves' chains of at most 512 / 1 adds, eight in flight, then joins
+        _check(got, ref, (520 + 16) * U * mag + U * np.abs(ref), "table gradient")
+        acc = got.clone()
+        A.lookup_backward(dy, t, rows, out=acc, accumulate=True)
+        _check(acc, 2 * ref, (520 + 16) * 3 * U * mag + 4 * U * np.abs(ref), "accumulated gradient")
+        assert torch.equal(got, A.lookup_backward(dy, t, rows)), "not the same bits twice"
+
+
 def test_lookup_no_valid_ids_nan_and_strides(dev):
     from sphere_rasterization_amd import appearance as A
     rng = np.random.default_rng(12)
