@@ -143,8 +143,8 @@ def _pixels(t: torch.Tensor) -> Tuple[torch.Tensor, int, int]:
     """(tensor, image stride, pixel stride) of [N, ..., C] read as [N][pixels][C]; a copy
     where the pixels are not evenly spaced."""
     if t.is_contiguous():
-        c = t.shape[-1]
-        return t, t[0].numel() if t.shape[0] else 0, c
+        n, c = t.shape[0], t.shape[-1]
+        return t, t.numel() // n if n else 0, c
     if t.shape[-1] <= 1 or t.stride(-1) == 1:
         dims = [(t.shape[i], t.stride(i)) for i in range(1, t.dim() - 1) if t.shape[i] != 1]
         if all(dims[i][1] == dims[i + 1][1] * dims[i + 1][0] for i in range(len(dims) - 1)):
@@ -160,11 +160,12 @@ def _norm_desc(x, weight, bias, groups: int, act: str, eps: float) -> L.splat_no
     d = L.splat_norm()
     d.dtype = _dtype("x", x)
     d.channels, d.groups, d.act, d.eps = x.shape[-1], int(groups), ACTS[act], float(eps)
-    d.images = x.shape[0]
-    pixels = 1
-    for s in x.shape[1:-1]:
-        pixels *= s
-    d.pixels = pixels
+    d.images, d.pixels = x.shape[0], 1
+    if x.numel():
+        d.pixels = x.numel() // (x.shape[0] * x.shape[-1])
+    else:
+        for s in x.shape[1:-1]:
+            d.pixels *= s
     kind = None
     for name, p in (("weight", weight), ("bias", bias)):
         if p is not None:
@@ -179,7 +180,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _flat(t: Optional[torch.Tensor]):
-    return None if t is None else t.contiguous()
+    return t if t is None or t.is_contiguous() else t.contiguous()
 
 
 def _group_norm(x, groups, weight, bias, eps, act, keep: bool):
@@ -260,7 +261,8 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     channels / groups channels of a group. act: none, relu, silu or gelu (with erf).
     weight and bias [channels], float32 or x's type. An NCHW tensor in torch's
     channels_last memory format is read in place as x.permute(0, 2, 3, 1)."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias)):
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (bias is not None and bias.requires_grad)):
         return _GroupNorm.apply(x, groups, weight, bias, eps, act)
     return _group_norm(x, groups, weight, bias, eps, act, False)[0]
 

@@ -479,3 +479,15 @@ def test_refusals(dev):
                  lambda: A.orthogonalize(torch.zeros(70000, 2, device=dev))):
         with pytest.raises(L.SplatError):
             call()
+
+
+def test_training_example(dev):
+    """The example's loop: table, renderer, shading and orthogonalised updates together."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_appearance.py")
+    spec = importlib.util.spec_from_file_location("train_appearance", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses = ex.train(steps=25, n=5000, width=160, height=96)
+    assert all(np.isfinite(losses)) and losses[-1] < 0.5 * losses[0]
