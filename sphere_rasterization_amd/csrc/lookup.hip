@@ -38,18 +38,19 @@ __global__ __launch_bounds__(LK_THREADS) void k_lookup(const T *__restrict__ tab
                                                        float scale, T *__restrict__ out, int64_t ldo) {
   const uint32_t base = blockIdx.x * (LK_THREADS * LK_ITEMS) + threadIdx.x;
   uint32_t row[LK_ITEMS], col[LK_ITEMS];
-  int64_t id[LK_ITEMS];
+  ID id[LK_ITEMS];
   Raw<T, VEC> x[LK_ITEMS];
 #pragma unroll
   for (int k = 0; k < LK_ITEMS; k++) {
     const uint32_t u = base + k * LK_THREADS;
     row[k] = div_by(u, units);
     col[k] = (u - row[k] * units.d) * VEC;
-    id[k] = u < total ? (int64_t)ids[row[k]] : -1;
+    id[k] = -1;
+    if (u < total) id[k] = ids[row[k]];
   }
 #pragma unroll
   for (int k = 0; k < LK_ITEMS; k++)
-    x[k] = load_if<T, VEC>(id[k] >= 0 && id[k] < rows, table + id[k] * ldt + col[k]);
+    x[k] = load_if<T, VEC>(id[k] >= 0 && (int64_t)id[k] < rows, table + (int64_t)id[k] * ldt + col[k]);
 #pragma unroll
   for (int k = 0; k < LK_ITEMS; k++)
     if (base + k * LK_THREADS < total) {
@@ -65,42 +66,60 @@ __global__ __launch_bounds__(LK_THREADS) void k_lookup(const T *__restrict__ tab
 // sort by id
 // ---------------------------------------------------------------------------
 // A token's key: its id, or `rows` (after every row) where the id is outside.
-template <typename ID>
-__device__ __forceinline__ uint32_t key_of(const ID *ids, uint32_t i, uint32_t rows) {
-  const int64_t id = (int64_t)ids[i];
+__device__ __forceinline__ uint32_t key_of(int64_t id, uint32_t rows) {
   return id >= 0 && id < (int64_t)rows ? (uint32_t)id : rows;
 }
 
-// Where a pass reads its (key, token) pairs: the caller's ids in the first pass, the
-// workspace after.
+// A pass's (key, token) pairs: from the caller's ids in the first pass, from the
+// workspace after. `word` is what is loaded; `pair` forms the pair once all are under way
+// (a compare next to its load, under the load's condition, would wait for that load).
+template <typename ID, bool FIRST>
+struct KeySource;
 template <typename ID>
-struct KeySource {
-  const ID *ids;
-  const uint2 *pairs;     // NULL in the first pass
+struct KeySource<ID, true> {
+  const ID *from;
   uint32_t n, rows;
-  __device__ uint32_t key(uint32_t i) const { return pairs ? pairs[i].x : key_of(ids, i, rows); }
-  __device__ uint2 pair(uint32_t i) const { return pairs ? pairs[i] : make_uint2(key_of(ids, i, rows), i); }
+  typedef ID Word;
+  __device__ Word word(uint32_t i) const {
+    ID x = -1;
+    if (i < n) x = from[i];
+    return x;
+  }
+  __device__ uint2 pair(Word x, uint32_t i) const { return make_uint2(key_of((int64_t)x, rows), i); }
+};
+template <typename ID>
+struct KeySource<ID, false> {
+  const uint2 *from;
+  uint32_t n, rows;
+  typedef uint2 Word;
+  __device__ Word word(uint32_t i) const {
+    uint2 x = make_uint2(0u, 0u);
+    if (i < n) x = from[i];
+    return x;
+  }
+  __device__ uint2 pair(Word x, uint32_t) const { return x; }
 };
 
-// counts[digit][tile]; also clears the rows' segment bounds (each thread a share).
-template <typename ID, int ITEMS>
-__global__ __launch_bounds__(ST_THREADS) void k_sort_count(KeySource<ID> src, int shift, int bits, uint32_t tiles,
+// counts[tile][digit]; also clears the rows' segment bounds (each thread a share).
+template <typename ID, bool FIRST, int ITEMS>
+__global__ __launch_bounds__(ST_THREADS) void k_sort_count(KeySource<ID, FIRST> src, int shift, int bits,
                                                            uint32_t *__restrict__ counts, int2 *bounds,
                                                            uint32_t nbounds) {
   __shared__ uint32_t h[RADIX];
   for (int d = threadIdx.x; d < RADIX; d += ST_THREADS) h[d] = 0;
-  __syncthreads();
-  const uint32_t mask = (1u << bits) - 1u, t0 = blockIdx.x * (uint32_t)(ST_THREADS * ITEMS);
+  const uint32_t mask = (1u << bits) - 1u, i0 = blockIdx.x * (uint32_t)(ST_THREADS * ITEMS) + threadIdx.x;
+  typename KeySource<ID, FIRST>::Word word[ITEMS];
 #pragma unroll
-  for (int j = 0; j < ITEMS; j++) {
-    const uint32_t i = t0 + j * ST_THREADS + threadIdx.x;
-    if (i < src.n) atomicAdd(&h[(src.key(i) >> shift) & mask], 1u);
-  }
+  for (int j = 0; j < ITEMS; j++) word[j] = src.word(i0 + j * ST_THREADS);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++)
+    if (i0 + j * ST_THREADS < src.n) atomicAdd(&h[(src.pair(word[j], 0).x >> shift) & mask], 1u);
   if (bounds)
     for (uint32_t r = blockIdx.x * ST_THREADS + threadIdx.x; r < nbounds; r += gridDim.x * ST_THREADS)
       bounds[r] = make_int2(0, 0);
   __syncthreads();
-  for (int d = threadIdx.x; d < (1 << bits); d += ST_THREADS) counts[(size_t)d * tiles + blockIdx.x] = h[d];
+  for (int d = threadIdx.x; d < (1 << bits); d += ST_THREADS) counts[((size_t)blockIdx.x << bits) + d] = h[d];
 }
 
 // Inclusive scan over the workgroup's threads (WAVES waves); s: WAVES words of LDS.
@@ -126,21 +145,46 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *s, uint32_t
   return x + before;
 }
 
-// One workgroup per digit: exclusive scan of its counts over the tiles, and its total.
-__global__ __launch_bounds__(ST_THREADS) void k_sort_scan(uint32_t *__restrict__ counts, uint32_t tiles,
+// Exclusive scan of each digit's counts over the tiles, and its total. A workgroup takes 16
+// digits, a thread one of them and 8 tiles at a time, so that it reads whole 64-byte runs
+// (a digit's counts side by side, as the scan alone would like, made every tile write and
+// read 512 scattered words).
+constexpr int SC_THREADS = 1024, SC_DIGITS = 16, SC_LANES = SC_THREADS / SC_DIGITS, SC_TILES = 8;
+__global__ __launch_bounds__(SC_THREADS) void k_sort_scan(uint32_t *__restrict__ counts, uint32_t tiles, uint32_t digits,
                                                           uint32_t *__restrict__ totals) {
-  __shared__ uint32_t s[ST_WAVES];
-  uint32_t *row = counts + (size_t)blockIdx.x * tiles;
-  uint32_t run = 0;
-  for (uint32_t t0 = 0; t0 < tiles; t0 += ST_THREADS) {
-    const uint32_t t = t0 + threadIdx.x;
-    const uint32_t c = t < tiles ? row[t] : 0u;
-    uint32_t total;
-    const uint32_t inc = block_scan<ST_WAVES>(c, s, &total);
-    if (t < tiles) row[t] = run + inc - c;
-    run += total;
+  __shared__ uint32_t s[SC_LANES][SC_DIGITS];
+  const uint32_t dl = threadIdx.x % SC_DIGITS, tl = threadIdx.x / SC_DIGITS, d = blockIdx.x * SC_DIGITS + dl;
+  uint32_t carry = 0;
+  for (uint32_t t0 = 0; t0 < tiles; t0 += SC_LANES * SC_TILES) {
+    uint32_t c[SC_TILES], sum = 0;
+#pragma unroll
+    for (int k = 0; k < SC_TILES; k++) {
+      const uint32_t t = t0 + tl * SC_TILES + k;
+      c[k] = 0;
+      if (t < tiles && d < digits) c[k] = counts[(size_t)t * digits + d];
+    }
+#pragma unroll
+    for (int k = 0; k < SC_TILES; k++) sum += c[k];
+    __syncthreads();
+    s[tl][dl] = sum;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll 8
+    for (uint32_t k = 0; k < SC_LANES; k++) {
+      const uint32_t v = s[k][dl];
+      if (k < tl) before += v;
+      all += v;
+    }
+    uint32_t run = carry + before;
+#pragma unroll
+    for (int k = 0; k < SC_TILES; k++) {
+      const uint32_t t = t0 + tl * SC_TILES + k;
+      if (t < tiles && d < digits) counts[(size_t)t * digits + d] = run;
+      run += c[k];
+    }
+    carry += all;
   }
-  if (threadIdx.x == 0) totals[blockIdx.x] = run;
+  if (tl == 0 && d < digits) totals[d] = carry;
 }
 
 // Rank of this lane's digit among the wave's items so far, adding the wave's items to
@@ -168,8 +212,8 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, int bits, bool ok,
 
 // The tile's pairs are put in digit order in LDS first, so that a wave's store covers a
 // few runs of consecutive pairs instead of 64 places.
-template <typename ID, int ITEMS>
-__global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID> src, int shift, int bits, uint32_t tiles,
+template <typename ID, bool FIRST, int ITEMS>
+__global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID, FIRST> src, int shift, int bits,
                                                              const uint32_t *__restrict__ counts,
                                                              const uint32_t *__restrict__ totals,
                                                              uint2 *__restrict__ out) {
@@ -182,22 +226,22 @@ __global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID> src, 
   for (int d = threadIdx.x; d < ST_WAVES * RADIX; d += ST_THREADS) (&hist[0][0])[d] = 0;
   const uint32_t mask = (1u << bits) - 1u, t0 = blockIdx.x * (uint32_t)ST_TILE;
   const uint32_t i0 = t0 + w * (ST_TILE / ST_WAVES) + lane;
+  typename KeySource<ID, FIRST>::Word word[ITEMS];
   uint2 pair[ITEMS];
   uint32_t rank[ITEMS];
 #pragma unroll
-  for (int j = 0; j < ITEMS; j++) {
-    const uint32_t i = i0 + j * WAVE;
-    pair[j] = i < src.n ? src.pair(i) : make_uint2(0u, 0u);
-  }
+  for (int j = 0; j < ITEMS; j++) word[j] = src.word(i0 + j * WAVE);
   constexpr int DPT = RADIX / ST_THREADS;
   uint32_t tot[DPT], cnt[DPT], sum = 0, all;
 #pragma unroll
   for (int k = 0; k < DPT; k++) {
     const uint32_t d = threadIdx.x * DPT + k;
     tot[k] = d <= mask ? totals[d] : 0u;
-    cnt[k] = d <= mask ? counts[(size_t)d * tiles + blockIdx.x] : 0u;
+    cnt[k] = d <= mask ? counts[((size_t)blockIdx.x << bits) + d] : 0u;
     sum += tot[k];
   }
+#pragma unroll
+  for (int j = 0; j < ITEMS; j++) pair[j] = src.pair(word[j], i0 + j * WAVE);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < ITEMS; j++)
@@ -528,12 +572,15 @@ __global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *_
   const uint32_t r0 = blockIdx.x * run, rows = a.rows - r0 < run ? a.rows - r0 : run;
   const Place q = place_of<VEC>(a, blockIdx.y);
   const uint32_t w = threadIdx.x >> 6, i0 = w * (WAVE * FW_ITEMS) + q.lane;
+  ID id[FW_ITEMS];
   uint32_t row[FW_ITEMS], rank[FW_ITEMS], mine = 0;
 #pragma unroll
   for (int j = 0; j < FW_ITEMS; j++) {
-    const uint32_t i = i0 + j * WAVE;
-    row[j] = i < a.n ? key_of(ids, i, a.rows) - r0 : ~0u;   // ids outside lie past every run
+    id[j] = -1;
+    if (i0 + j * WAVE < a.n) id[j] = ids[i0 + j * WAVE];
   }
+#pragma unroll
+  for (int j = 0; j < FW_ITEMS; j++) row[j] = key_of((int64_t)id[j], a.rows) - r0;   // ids outside lie past every run
 #pragma unroll
   for (int j = 0; j < FW_ITEMS; j++) {
     const uint64_t m = ballot64(row[j] < rows);
@@ -669,21 +716,33 @@ int sort_passes(const ID *ids, uint32_t n, uint32_t rows, int bits, int passes, 
   constexpr uint32_t TOKENS = ST_THREADS * ITEMS;
   const uint32_t tiles = (n + TOKENS - 1) / TOKENS;
   const int dbits = (bits + passes - 1) / passes;
-  for (int p = 0; p < passes; p++) {
-    KeySource<ID> src;
-    src.ids = ids;
-    src.pairs = p ? L.pairs[(p - 1) & 1] : nullptr;
+  auto pass = [&](auto src, auto count, auto scatter, int p) -> int {
+    const int shift = p * dbits, b = bits - shift < dbits ? bits - shift : dbits;
     src.n = n;
     src.rows = rows;
-    const int shift = p * dbits, b = bits - shift < dbits ? bits - shift : dbits;
-    hipLaunchKernelGGL((k_sort_count<ID, ITEMS>), dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, tiles, L.counts,
+    hipLaunchKernelGGL(count, dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, L.counts,
                        p ? (int2 *)nullptr : L.bounds, rows);
     SPLAT_LAUNCH_CHECK();
-    hipLaunchKernelGGL(k_sort_scan, dim3(1u << b), dim3(ST_THREADS), 0, stream, L.counts, tiles, L.totals);
+    hipLaunchKernelGGL(k_sort_scan, dim3(((1u << b) + SC_DIGITS - 1) / SC_DIGITS), dim3(SC_THREADS), 0, stream, L.counts,
+                       tiles, 1u << b, L.totals);
     SPLAT_LAUNCH_CHECK();
-    hipLaunchKernelGGL((k_sort_scatter<ID, ITEMS>), dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, tiles, L.counts,
-                       L.totals, L.pairs[p & 1]);
+    hipLaunchKernelGGL(scatter, dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, L.counts, L.totals,
+                       L.pairs[p & 1]);
     SPLAT_LAUNCH_CHECK();
+    return SPLAT_OK;
+  };
+  for (int p = 0; p < passes; p++) {
+    int st;
+    if (p == 0) {
+      KeySource<ID, true> src;
+      src.from = ids;
+      st = pass(src, k_sort_count<ID, true, ITEMS>, k_sort_scatter<ID, true, ITEMS>, p);
+    } else {
+      KeySource<ID, false> src;
+      src.from = L.pairs[(p - 1) & 1];
+      st = pass(src, k_sort_count<ID, false, ITEMS>, k_sort_scatter<ID, false, ITEMS>, p);
+    }
+    if (st) return st;
   }
   *half = (passes - 1) & 1;
   return SPLAT_OK;
