@@ -74,7 +74,7 @@ def train(steps=50, n=30_000, width=320, height=192, lr=0.02, seed=0, device="cu
                 v.mul_(0.9).add_(m.grad, alpha=0.1)
                 # a step of the same size for every direction, whatever the matrix's shape
                 m.add_(A.orthogonalize(v, scale=max(1.0, m.shape[0] / m.shape[1]) ** 0.5), alpha=-lr)
-        losses.append(float(loss))
+        losses.append(float(loss.detach()))
         if log and (step % 10 == 0 or step == steps - 1):
             log(f"step {step:4d}  loss {losses[-1]:.5f}")
     return losses

@@ -688,6 +688,140 @@ __global__ __launch_bounds__(SM_THREADS) void k_ortho_small(SmallArgs o) {
   }
 }
 
+// ---- narrow matrices --------------------------------------------------------------------
+// Few rows (at most 96) and a long axis: one launch per step instead of three. A
+// workgroup keeps `ns` columns of X; in a step it adds the slices' shares of X X^T, which
+// is small, forms B by itself, multiplies its own columns and leaves their share of the
+// next X X^T. Shares alternate between two places, since other workgroups may still read
+// the last ones. X^T of a slice passes from launch to launch as the image LDS holds.
+constexpr int NW_ROWS = 96;                        // LDS: X, X^T (64 or 128 columns), A, B, 4 bytes a value
+constexpr int NW_TILES = 2;                        // 16 x 16 tiles of a slice per wave, at most
+constexpr int NW_LDS = 128 << 10;
+
+struct NarrowArgs {
+  const void *g;
+  void *out;
+  int64_t gb, gr, ob, orow;
+  int dtype, rows, cols, tall, m, n, mp, ns, slices, last, norm_blocks;
+  float eps, s0, mul_a, mul_p, ca, cb, mul_x;
+  const double *norms;
+  _Float16 *image;                                 // [batch][slices][2 ns mp]
+  const float4 *from;                              // [batch][slices][tiles][lanes]: shares of X X^T
+  float4 *to;
+};
+
+template <bool FIRST>
+__global__ __launch_bounds__(SM_THREADS) void k_ortho_narrow(NarrowArgs o) {
+  __shared__ __align__(16) char lds[NW_LDS];
+  _Float16 *x = reinterpret_cast<_Float16 *>(lds), *y = x + 2 * o.mp * o.ns, *a = y + 2 * o.mp * o.ns,
+           *b = a + 2 * o.mp * o.mp;
+  float *result = reinterpret_cast<float *>(lds);  // in X's and X^T's place at the end
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int fr = lane & 15, fk = lane >> 4;
+  const int64_t mat = blockIdx.y;
+  const int j0 = blockIdx.x * o.ns, tm = o.mp / 16, tn = o.ns / 16, mm = tm * tm;
+  const int64_t slice = mat * o.slices + blockIdx.x;
+  half8 *image = reinterpret_cast<half8 *>(o.image + slice * 2 * o.mp * o.ns);
+  const int chunks = o.mp * o.ns / 4;              // of 16 bytes in a slice's image
+  if constexpr (FIRST) {
+    double *sums = reinterpret_cast<double *>(b);
+    double t = 0.0;
+    for (int k = tid; k < o.norm_blocks; k += SM_THREADS) t += o.norms[mat * NORM_BLOCKS + k];
+    t = wave_sum_f64(t);
+    if (lane == 0) sums[w] = t;
+    __syncthreads();
+    double all = 0.0;
+#pragma unroll
+    for (int k = 0; k < SM_WAVES; k++) all += sums[k];
+    const float inv = (float)((double)o.s0 / (sqrt(all) + (double)o.eps));
+    const char *g = (const char *)o.g + mat * o.gb * (o.dtype == SPLAT_F32 ? 4 : 2);
+    const int fast = o.tall ? o.mp : o.ns;         // the axis that memory holds side by side
+    for (int i = tid; i < o.mp * o.ns; i += SM_THREADS) {
+      const int q = i / fast, f = i - q * fast, r = o.tall ? f : q, c = o.tall ? q : f;
+      float v = 0.0f;
+      if (r < o.m && j0 + c < o.n)
+        v = read_as_f32(g, o.tall ? (j0 + c) * o.gr + r : r * o.gr + j0 + c, o.dtype) * inv;
+      small_put(x, o.mp, r, c, v);
+      small_put(y, o.ns, c, r, v);
+    }
+    __syncthreads();
+  } else {
+    for (int i = tid; i < chunks; i += SM_THREADS) reinterpret_cast<half8 *>(y)[i] = image[i];
+    // A: the slices' shares, first to last
+    for (int k = w; k < mm; k += SM_WAVES) {
+      const int it = k / tm, jt = k - it * tm;
+      const float4 *f = o.from + ((mat * o.slices) * mm + k) * WAVE + lane;
+      float4v v = {0.0f, 0.0f, 0.0f, 0.0f};
+      int s = 0;
+      for (; s + 8 <= o.slices; s += 8) {
+        float4 t[8];
+#pragma unroll
+        for (int u = 0; u < 8; u++) t[u] = f[(int64_t)(s + u) * mm * WAVE];
+#pragma unroll
+        for (int u = 0; u < 8; u++) v += float4v{t[u].x, t[u].y, t[u].z, t[u].w};
+      }
+      for (; s < o.slices; s++) {
+        const float4 t = f[(int64_t)s * mm * WAVE];
+        v += float4v{t.x, t.y, t.z, t.w};
+      }
+      small_put4(a, o.mp, jt * 16 + fr, it * 16 + fk * 4, v * o.mul_a);
+    }
+    __syncthreads();
+    for (int k = w; k < mm; k += SM_WAVES) {       // B = a I + b A + c A A
+      const int it = k / tm, jt = k - it * tm, J = jt * 16 + fr, I0 = it * 16 + fk * 4, at = I0 & 7, c = (I0 >> 3) & 3;
+      const half4 hi = *reinterpret_cast<const half4 *>(a + small_at(o.mp, I0 >> 5, J, c) + at);
+      const half4 lo = *reinterpret_cast<const half4 *>(a + small_at(o.mp, I0 >> 5, J, c + 4) + at);
+      float4v v = small_product(a, o.mp, it, a, o.mp, jt, o.mp / 32, lane);
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        v[e] = __builtin_fmaf(o.cb, (float)hi[e] + (float)lo[e], v[e] * o.mul_p);
+        if (I0 + e == J) v[e] += o.ca;
+      }
+      small_put4(b, o.mp, J, I0, v);
+    }
+    __syncthreads();
+    float4v acc[NW_TILES];                         // X <- B X, held until X^T has been read
+#pragma unroll
+    for (int u = 0; u < NW_TILES; u++) {
+      const int k = w + u * SM_WAVES;
+      if (k < tm * tn) acc[u] = small_product(b, o.mp, k % tm, y, o.ns, k / tm, o.mp / 32, lane) * o.mul_x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < NW_TILES; u++) {
+      const int k = w + u * SM_WAVES;
+      if (k < tm * tn) {
+        const int I0 = k % tm * 16 + fk * 4, J = k / tm * 16 + fr;
+        if (!o.last) {
+          small_put4(y, o.ns, J, I0, acc[u]);
+#pragma unroll
+          for (int e = 0; e < 4; e++) small_put(x, o.mp, I0 + e, J, acc[u][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e++) result[o.tall ? J * (o.mp + 1) + I0 + e : (I0 + e) * (o.ns + 1) + J] = acc[u][e];
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (FIRST || !o.last) {
+    for (int i = tid; i < chunks; i += SM_THREADS) image[i] = reinterpret_cast<const half8 *>(y)[i];
+    for (int k = w; k < mm; k += SM_WAVES) {
+      const int it = k / tm;
+      const float4v v = small_product(x, o.mp, it, x, o.mp, k - it * tm, o.ns / 32, lane);
+      o.to[(slice * mm + k) * WAVE + lane] = make_float4(v[0], v[1], v[2], v[3]);
+    }
+  } else {
+    const int fast = o.tall ? o.m : (o.n - j0 < o.ns ? o.n - j0 : o.ns), slow = o.tall ? (o.n - j0 < o.ns ? o.n - j0 : o.ns) : o.m;
+    const int ld = (o.tall ? o.mp : o.ns) + 1;
+    for (int i = tid; i < fast * slow; i += SM_THREADS) {
+      const int q = i / fast, f = i - q * fast;
+      const int64_t at = o.tall ? (int64_t)(j0 + q) * o.orow + f : q * o.orow + j0 + f;
+      write_from_f32(o.out, mat * o.ob + at, o.dtype, result[q * ld + f]);
+    }
+  }
+}
+
 // ---- host -----------------------------------------------------------------------------
 // Largest |a x + b x^3 + c x^5| for 0 <= x <= u.
 double sup_quintic(double a, double b, double c, double u) {
@@ -748,6 +882,46 @@ int small_lds(int rows, int cols) {
 // 489, 1024 x 8192 702 and 1252, 2048 x 4096 1197 and 1221 (128 x 128).
 bool share_out(int64_t tiles, int tl, int K) {
   return tiles < GROUPS && (tl == 128 ? K >= 512 : K >= 1024 && K >= 22 * tiles);
+}
+
+// Columns per workgroup of the narrow form; 0 where three launches a step are faster. Whole
+// calls in this form and in that, us: 9 x 1000 32 and 86, 64 x 300 44 and 72, 64 x 1024 48
+// and 88, 64 x 8192 93 and 105, eight of 64 x 1024 61 and 96, 96 x 1024 80 and 95; but 96 x
+// 4096 158 and 111 (every workgroup adds up every slice's 36 KB), and 64 of 64 x 512 132
+// and 120 (more workgroups than CUs).
+int narrow_cols(int64_t batch, int rows, int cols) {
+  const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  if (m > NW_ROWS || n > (m <= 64 ? 8192 : 1536)) return 0;
+  const int ns = n > 2048 ? 128 : 64;
+  return batch * ((n + ns - 1) / ns) <= 256 ? ns : 0;
+}
+
+struct NarrowLayout {
+  int mp, ns, slices;
+  double *norms;
+  _Float16 *image;
+  float4 *part[2];
+  size_t bytes;
+};
+
+NarrowLayout narrow_layout(void *base, int64_t batch, int rows, int cols) {
+  NarrowLayout L;
+  const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  L.mp = round_up(m, 32);
+  L.ns = narrow_cols(batch, rows, cols);
+  L.slices = (n + L.ns - 1) / L.ns;
+  char *p = (char *)base;
+  auto take = [&](size_t b) {
+    char *q = p;
+    p += ws_align(b);
+    return q;
+  };
+  const size_t all = (size_t)batch * L.slices;
+  L.norms = (double *)take(sizeof(double) * NORM_BLOCKS * (size_t)batch);
+  L.image = (_Float16 *)take(4 * all * L.mp * L.ns);
+  for (int k = 0; k < 2; k++) L.part[k] = (float4 *)take(4 * all * L.mp * L.mp);
+  L.bytes = (size_t)(p - (char *)base);
+  return L;
 }
 
 OrthoArgs ortho_layout(void *base, int64_t batch, int rows, int cols, size_t *bytes) {
@@ -820,10 +994,24 @@ int run_gemm(const GemmArgs &q, int tile, int I, int J, int64_t batch, hipStream
 
 size_t orthogonalize_workspace_bytes(int64_t batch, int rows, int cols) {
   if (small_lds(rows, cols)) return 0;
+  if (narrow_cols(batch, rows, cols)) return narrow_layout(nullptr, batch, rows, cols).bytes;
   size_t bytes = 0;
   ortho_layout(nullptr, batch, rows, cols, &bytes);
   return bytes;
 }
+
+namespace {
+
+// Partial sums of squares of every matrix into o.norms; *blocks per matrix.
+int run_norm(const OrthoArgs &o, int64_t batch, int *blocks, hipStream_t stream) {
+  const int64_t pieces = (int64_t)o.rows * ((o.cols + 8 * OR_THREADS - 1) / (8 * OR_THREADS));
+  *blocks = pieces < NORM_BLOCKS ? (int)pieces : NORM_BLOCKS;
+  hipLaunchKernelGGL(k_ortho_norm, dim3(*blocks, (unsigned)batch), dim3(OR_THREADS), 0, stream, o);
+  SPLAT_LAUNCH_CHECK();
+  return SPLAT_OK;
+}
+
+}  // namespace
 
 // Whether every step's singular values stay within a range that the scales can serve.
 int orthogonalize_bounds(int steps, float a, float b, float c) {
@@ -879,6 +1067,62 @@ int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int 
     SPLAT_LAUNCH_CHECK();
     return SPLAT_OK;
   }
+  if (narrow_cols(batch, rows, cols)) {
+    const NarrowLayout L = narrow_layout(ws, batch, rows, cols);
+    OrthoArgs q = {};
+    q.g = g;
+    q.dtype = dtype;
+    q.gb = gb;
+    q.gr = gr;
+    q.rows = rows;
+    q.cols = cols;
+    q.norms = L.norms;
+    NarrowArgs o = {};
+    int st = run_norm(q, batch, &o.norm_blocks, stream);
+    if (st) return st;
+    o.g = g;
+    o.out = out;
+    o.gb = gb;
+    o.gr = gr;
+    o.ob = ob;
+    o.orow = orow;
+    o.dtype = dtype;
+    o.rows = rows;
+    o.cols = cols;
+    o.tall = rows > cols;
+    o.m = o.tall ? cols : rows;
+    o.n = o.tall ? rows : cols;
+    o.mp = L.mp;
+    o.ns = L.ns;
+    o.slices = L.slices;
+    o.eps = eps;
+    o.norms = L.norms;
+    o.image = L.image;
+    double u = 1.0;
+    int ex = scale_exp(u);
+    o.s0 = ldexpf(1.0f, ex);
+    o.to = L.part[0];
+    const dim3 grid((unsigned)L.slices, (unsigned)batch);
+    hipLaunchKernelGGL(k_ortho_narrow<true>, grid, dim3(SM_THREADS), 0, stream, o);
+    SPLAT_LAUNCH_CHECK();
+    for (int k = 0; k < steps; k++) {
+      const int ea = scale_exp(u * u), eb = scale_exp(sup_quadratic(ca, cb, cc, u * u));
+      u = sup_quintic(ca, cb, cc, u);
+      const int en = scale_exp(u);
+      o.last = k + 1 == steps;
+      o.mul_a = ldexpf(1.0f, ea - 2 * ex);
+      o.mul_p = ldexpf(cc, eb - 2 * ea);
+      o.ca = ldexpf(ca, eb);
+      o.cb = ldexpf(cb, eb - ea);
+      o.mul_x = o.last ? ldexpf(scale, -(eb + ex)) : ldexpf(1.0f, en - eb - ex);
+      o.from = L.part[k & 1];
+      o.to = L.part[(k + 1) & 1];
+      ex = en;
+      hipLaunchKernelGGL(k_ortho_narrow<false>, grid, dim3(SM_THREADS), 0, stream, o);
+      SPLAT_LAUNCH_CHECK();
+    }
+    return SPLAT_OK;
+  }
   size_t bytes;
   OrthoArgs o = ortho_layout(ws, batch, rows, cols, &bytes);
   o.g = g;
@@ -889,10 +1133,8 @@ int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int 
   double u = 1.0;
   int ex = scale_exp(u);
   o.s0 = ldexpf(1.0f, ex);
-  const int64_t pieces = (int64_t)rows * ((cols + 8 * OR_THREADS - 1) / (8 * OR_THREADS));
-  const int nb = pieces < NORM_BLOCKS ? (int)pieces : NORM_BLOCKS;
-  hipLaunchKernelGGL(k_ortho_norm, dim3(nb, (unsigned)batch), dim3(OR_THREADS), 0, stream, o);
-  SPLAT_LAUNCH_CHECK();
+  int nb, st0 = run_norm(o, batch, &nb, stream);
+  if (st0) return st0;
   const int pr = o.tall ? o.np : o.mp, pc = o.tall ? o.mp : o.np;
   hipLaunchKernelGGL(k_ortho_pack, dim3(pc / 32, pr / 32, (unsigned)batch), dim3(OR_THREADS), 0, stream, o, nb);
   SPLAT_LAUNCH_CHECK();

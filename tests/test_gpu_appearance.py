@@ -362,7 +362,9 @@ def test_orthogonalize_batches_strides_and_scale(dev):
         assert np.linalg.norm(_np(A.orthogonalize(g, steps, coeffs)) - ref) <= _ortho_tol(ref, "f32", steps, max(1.0, coeffs[0]))
 
 
-@pytest.mark.parametrize("shape", [(130, 2500), (300, 4100), (3, 70, 2049), (513, 16400), (130, 200, 250), (2300, 60)])
+@pytest.mark.parametrize("shape", [(130, 2500), (300, 4100), (3, 70, 2049), (513, 16400), (130, 200, 250), (2300, 60),
+                                   (3, 33, 1025), (96, 8192), (8192, 65), (9, 8193), (1, 4000), (97, 1500), (40, 64, 500),
+                                   (90, 1537), (90, 1536)])
 def test_orthogonalize_tiles(dev, shape):
     """Long summed axes (a product's steps shared out over all workgroups) and many tiles."""
     from sphere_rasterization_amd import appearance as A
