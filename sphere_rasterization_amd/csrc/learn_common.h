@@ -33,6 +33,13 @@ __device__ __forceinline__ void to_f32(const Raw<T, N> &r, float (&o)[N]) {
   for (int i = 0; i < N; i++) o[i] = (float)x.v[i];
 }
 
+// The same bits at any element's address: the compiler then asks no more of the address,
+// and the hardware takes the access whole, aligned or not.
+template <typename T, int N>
+struct Loose {
+  typedef Raw<T, N> type __attribute__((aligned(alignof(T))));
+};
+
 template <typename T, int N>
 __device__ __forceinline__ void load_f32(const T *p, float (&o)[N]) {
   to_f32<T, N>(*reinterpret_cast<const Raw<T, N> *>(p), o);
@@ -69,6 +76,21 @@ __device__ __forceinline__ void stream_f32(T *p, const float (&o)[N]) {
   } else {
     store_f32<T, N>(p, o);
   }
+}
+
+// load_if and stream_f32 at any element's address.
+template <typename T, int N>
+__device__ __forceinline__ Raw<T, N> load_loose_if(bool ok, const T *p) {
+  Raw<T, N> x = {};
+  if (ok) x = *reinterpret_cast<const typename Loose<T, N>::type *>(p);
+  return x;
+}
+template <typename T, int N>
+__device__ __forceinline__ void stream_loose(T *p, const float (&o)[N]) {
+  Pack<T, N> x;
+#pragma unroll
+  for (int i = 0; i < N; i++) x.v[i] = (T)o[i];
+  __builtin_nontemporal_store(__builtin_bit_cast(Raw<T, N>, x), reinterpret_cast<typename Loose<T, N>::type *>(p));
 }
 
 // fp32 sums kept in the workspace: 16-byte accesses where N allows.

@@ -29,13 +29,21 @@ constexpr int CHUNK = 64;
 constexpr int64_t SMALL_TILES = 256 << 10;
 constexpr int tile_items(int64_t n) { return n <= SMALL_TILES ? 4 : 16; }
 
+// A row of any length at any address is walked in packs of VEC elements, the last of which
+// ends with the row: it overlaps the one before by what is missing. Both compute the
+// overlap alike and write the same values (sums that are added to what a row holds take
+// packs that divide it instead).
+__device__ __forceinline__ uint32_t col_of(uint32_t col, uint32_t dim, uint32_t vec) {
+  return col + vec <= dim ? col : dim - vec;
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 template <typename T, int VEC, typename ID>
 __global__ __launch_bounds__(LK_THREADS) void k_lookup(const T *__restrict__ table, int64_t ldt, int64_t rows,
                                                        const ID *__restrict__ ids, uint32_t total, FastDiv units,
-                                                       float scale, T *__restrict__ out, int64_t ldo) {
+                                                       uint32_t dim, float scale, T *__restrict__ out, int64_t ldo) {
   const uint32_t base = blockIdx.x * (LK_THREADS * LK_ITEMS) + threadIdx.x;
   uint32_t row[LK_ITEMS], col[LK_ITEMS];
   ID id[LK_ITEMS];
@@ -44,13 +52,13 @@ __global__ __launch_bounds__(LK_THREADS) void k_lookup(const T *__restrict__ tab
   for (int k = 0; k < LK_ITEMS; k++) {
     const uint32_t u = base + k * LK_THREADS;
     row[k] = div_by(u, units);
-    col[k] = (u - row[k] * units.d) * VEC;
+    col[k] = col_of((u - row[k] * units.d) * VEC, dim, VEC);
     id[k] = -1;
     if (u < total) id[k] = ids[row[k]];
   }
 #pragma unroll
   for (int k = 0; k < LK_ITEMS; k++)
-    x[k] = load_if<T, VEC>(id[k] >= 0 && (int64_t)id[k] < rows, table + (int64_t)id[k] * ldt + col[k]);
+    x[k] = load_loose_if<T, VEC>(id[k] >= 0 && (int64_t)id[k] < rows, table + (int64_t)id[k] * ldt + col[k]);
 #pragma unroll
   for (int k = 0; k < LK_ITEMS; k++)
     if (base + k * LK_THREADS < total) {
@@ -58,7 +66,7 @@ __global__ __launch_bounds__(LK_THREADS) void k_lookup(const T *__restrict__ tab
       to_f32<T, VEC>(x[k], v);
 #pragma unroll
       for (int j = 0; j < VEC; j++) v[j] *= scale;
-      stream_f32<T, VEC>(out + (int64_t)row[k] * ldo + col[k], v);
+      stream_loose<T, VEC>(out + (int64_t)row[k] * ldo + col[k], v);
     }
 }
 
@@ -293,18 +301,18 @@ struct SumArgs {
   int64_t ldy;
   const uint2 *sorted;      // (row, token) by row, then token
   int2 *bounds;             // [rows] segment of each row in `sorted`, (0, 0) without tokens
-  float *part1, *part2;     // sums of whole chunks of 64 and of 64 x 64 tokens [.][dim]
+  float *part1, *part2;     // sums of whole chunks of 64 and of 64 x 64 tokens [.][width]
   void *grad;
   int64_t ldg;
   uint32_t n, rows, chunks;
-  int dim, units, lg, slices, two_levels, accumulate;
+  int dim, width, units, lg, slices, two_levels, accumulate;   // width: units x VEC, a chunk sum's length
   float scale;
 };
 
 // This lane's place in a wave's share of the work.
 struct Place {
   uint32_t lane, g, G;      // row lane and row lanes per wave
-  int col;
+  int col, sum;             // first column of its pack, and the pack's place in a chunk sum
   bool on;
 };
 template <int VEC>
@@ -315,7 +323,8 @@ __device__ __forceinline__ Place place_of(const SumArgs &a, uint32_t slice) {
   q.g = q.lane >> a.lg;
   const int unit = (int)(slice << 6) + (int)(q.lane & ((1u << a.lg) - 1u));
   q.on = unit < a.units;
-  q.col = unit * VEC;
+  q.sum = unit * VEC;
+  q.col = (int)col_of((uint32_t)q.sum, (uint32_t)a.dim, VEC);
   return q;
 }
 
@@ -330,7 +339,7 @@ __device__ __forceinline__ void add_sums(const float *src, int64_t ld, uint32_t 
     for (int k = 0; k < U; k++) {
 #pragma unroll
       for (int j = 0; j < VEC; j++) v[k][j] = 0.0f;
-      if (q.on && p + k * q.G < p1) load_sums<VEC>(src + (int64_t)(p + k * q.G) * ld + q.col, v[k]);
+      if (q.on && p + k * q.G < p1) load_sums<VEC>(src + (int64_t)(p + k * q.G) * ld + q.sum, v[k]);
     }
 #pragma unroll
     for (int k = 0; k < U; k++)
@@ -354,7 +363,7 @@ __device__ __forceinline__ void add_tokens(const SumArgs &a, uint32_t p0, uint32
       for (int k = 0; k < U; k++) {
         const uint32_t t = k0 + k * q.G + q.g;
         const uint32_t at = __shfl(tok, (int)(t & 63u));
-        x[k] = load_if<T, VEC>(q.on && t < m, dy + (int64_t)at * a.ldy);
+        x[k] = load_loose_if<T, VEC>(q.on && t < m, dy + (int64_t)at * a.ldy);
       }
 #pragma unroll
       for (int k = 0; k < U; k++) {
@@ -396,7 +405,7 @@ __device__ __forceinline__ void chunk_sum(const SumArgs &a, uint32_t c, uint32_t
   for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
   add_tokens<T, VEC, DEEP>(a, c * CHUNK, c * CHUNK + CHUNK, q, acc);
   join_row_lanes<VEC>(acc, a.lg);
-  if (q.g == 0 && q.on) store_sums<VEC>(a.part1 + (size_t)c * a.dim + q.col, acc);
+  if (q.g == 0 && q.on) store_sums<VEC>(a.part1 + (size_t)c * a.width + q.sum, acc);
 }
 
 template <typename T, int VEC>
@@ -415,9 +424,9 @@ __device__ __forceinline__ void chunk_sum2(const SumArgs &a, uint32_t c, uint32_
   float acc[VEC];
 #pragma unroll
   for (int j = 0; j < VEC; j++) acc[j] = 0.0f;
-  add_sums<VEC, DEEP>(a.part1, a.dim, c * CHUNK, c * CHUNK + CHUNK, q, acc);
+  add_sums<VEC, DEEP>(a.part1, a.width, c * CHUNK, c * CHUNK + CHUNK, q, acc);
   join_row_lanes<VEC>(acc, a.lg);
-  if (q.g == 0 && q.on) store_sums<VEC>(a.part2 + (size_t)c * a.dim + q.col, acc);
+  if (q.g == 0 && q.on) store_sums<VEC>(a.part2 + (size_t)c * a.width + q.sum, acc);
 }
 
 template <int VEC>
@@ -434,11 +443,11 @@ __device__ __forceinline__ void write_row(const SumArgs &a, uint32_t row, int co
   for (int j = 0; j < VEC; j++) acc[j] *= a.scale;
   if (a.accumulate) {
     float old[VEC];
-    load_f32<T, VEC>(o, old);
+    to_f32<T, VEC>(load_loose_if<T, VEC>(true, o), old);
 #pragma unroll
     for (int j = 0; j < VEC; j++) acc[j] += old[j];
   }
-  stream_f32<T, VEC>(o, acc);
+  stream_loose<T, VEC>(o, acc);
 }
 
 // A row of more than 64 tokens, by a wave: its segment holds a multiple of 64, and the
@@ -458,11 +467,11 @@ __device__ __forceinline__ void heavy_row(const SumArgs &a, uint32_t c, uint32_t
   add_tokens<T, VEC, DEEP>(a, s, c * CHUNK, q, acc);
   const uint32_t d0 = (c + CHUNK - 1) / CHUNK, d1 = c1 / CHUNK;
   if (!a.two_levels || d0 >= d1) {
-    add_sums<VEC, DEEP>(a.part1, a.dim, c, c1, q, acc);
+    add_sums<VEC, DEEP>(a.part1, a.width, c, c1, q, acc);
   } else {
-    add_sums<VEC, DEEP>(a.part1, a.dim, c, d0 * CHUNK, q, acc);
-    add_sums<VEC, DEEP>(a.part2, a.dim, d0, d1, q, acc);
-    add_sums<VEC, DEEP>(a.part1, a.dim, d1 * CHUNK, c1, q, acc);
+    add_sums<VEC, DEEP>(a.part1, a.width, c, d0 * CHUNK, q, acc);
+    add_sums<VEC, DEEP>(a.part2, a.width, d0, d1, q, acc);
+    add_sums<VEC, DEEP>(a.part1, a.width, d1 * CHUNK, c1, q, acc);
   }
   add_tokens<T, VEC, DEEP>(a, c1 * CHUNK, e, q, acc);
   join_row_lanes<VEC>(acc, a.lg);
@@ -497,7 +506,7 @@ __device__ __forceinline__ void light_rows(const SumArgs &a, uint32_t set, uint3
       for (int k = 0; k < U; k++) at[k] = p + k < e ? a.sorted[p + k].y : 0u;
 #pragma unroll
       for (int k = 0; k < U; k++)
-        x[k] = load_if<T, VEC>(q.on && p + k < e, (const T *)a.dy + (int64_t)at[k] * a.ldy + q.col);
+        x[k] = load_loose_if<T, VEC>(q.on && p + k < e, (const T *)a.dy + (int64_t)at[k] * a.ldy + q.col);
 #pragma unroll
       for (int k = 0; k < U; k++) {
         float v[VEC];
@@ -550,7 +559,7 @@ __device__ __forceinline__ void add_few(const SumArgs &a, const uint16_t *buf, u
 #pragma unroll
     for (int k = 0; k < DEEP; k++) {
       const uint32_t t = k0 + k * q.G + q.g;
-      x[k] = load_if<T, VEC>(q.on && t < m, dy + (int64_t)(t < m ? buf[t] : 0) * a.ldy);
+      x[k] = load_loose_if<T, VEC>(q.on && t < m, dy + (int64_t)(t < m ? buf[t] : 0) * a.ldy);
     }
 #pragma unroll
     for (int k = 0; k < DEEP; k++) {
@@ -606,7 +615,7 @@ __global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *_
     if (a.accumulate || !q.on) return;
     for (uint32_t r = w * q.G + q.g; r < rows; r += FW_WAVES * q.G) {
       float zero[VEC] = {};
-      stream_f32<T, VEC>((T *)a.grad + (int64_t)(r0 + r) * a.ldg + q.col, zero);
+      stream_loose<T, VEC>((T *)a.grad + (int64_t)(r0 + r) * a.ldg + q.col, zero);
     }
     return;
   }
@@ -658,10 +667,21 @@ __global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *_
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
+// Elements per pack: 16 bytes, or less for shorter rows and where packs have to divide them.
+// Overlapping packs against the widest that divides the row and its alignment, lookup and
+// gradient in us: 1M rows of 33 fp32 29 and 99 (43 and 133), of 31 fp16 19 and 92 (40 and
+// 109), 47337 of 383 fp16 11 and 57 (24 and 92), 20000 of 2723 bf16 25 and 57 (62 and 90),
+// 1M of 20 fp16 11 and 88 (13 and 81).
+int pack_width(int bytes, int dim, bool divide) {
+  int v = 16 / bytes;
+  while (v > dim || (divide && dim % v)) v >>= 1;
+  return v;
+}
+
 template <typename T, int VEC, typename ID>
 int run_lookup(const void *table, int64_t ldt, int64_t rows, int dim, const void *ids, int64_t n, float scale,
                void *out, int64_t ldo, hipStream_t stream) {
-  const uint32_t units = (uint32_t)(dim / VEC);
+  const uint32_t units = (uint32_t)((dim + VEC - 1) / VEC);
   const FastDiv fd = fast_div(units);
   // the kernel's unit index has 31 bits: more tokens take more launches
   const int64_t step = ((1ll << 31) - 1) / units;
@@ -670,7 +690,7 @@ int run_lookup(const void *table, int64_t ldt, int64_t rows, int dim, const void
     const uint32_t total = (uint32_t)(m * units);
     const unsigned per = LK_THREADS * LK_ITEMS;
     hipLaunchKernelGGL((k_lookup<T, VEC, ID>), dim3((total + per - 1) / per), dim3(LK_THREADS), 0, stream,
-                       (const T *)table, ldt, rows, (const ID *)ids + i, total, fd, scale, (T *)out + i * ldo, ldo);
+                       (const T *)table, ldt, rows, (const ID *)ids + i, total, fd, (uint32_t)dim, scale, (T *)out + i * ldo, ldo);
     SPLAT_LAUNCH_CHECK();
   }
   return SPLAT_OK;
@@ -698,8 +718,8 @@ BwdLayout bwd_layout(void *base, int64_t n, int64_t rows, int dim) {
   L.counts = (uint32_t *)take(4 * RADIX * tiles);
   L.totals = (uint32_t *)take(4 * RADIX);
   L.bounds = (int2 *)take(8 * (size_t)rows);
-  L.part1 = (float *)take(4 * (size_t)(n / CHUNK) * dim);
-  L.part2 = (float *)take(4 * (size_t)(n / (CHUNK * CHUNK)) * dim);
+  L.part1 = (float *)take(4 * (size_t)(n / CHUNK) * (dim + 7));
+  L.part2 = (float *)take(4 * (size_t)(n / (CHUNK * CHUNK)) * (dim + 7));
   L.bytes = (size_t)(p - (char *)base);
   return L;
 }
@@ -760,23 +780,24 @@ int sort_tokens(const void *ids, uint32_t n, uint32_t rows, const BwdLayout &L, 
 
 // Every row zero: no token to add.
 template <typename T, int VEC>
-__global__ __launch_bounds__(256) void k_zero_rows(T *grad, int64_t ldg, uint64_t total, uint32_t units) {
+__global__ __launch_bounds__(256) void k_zero_rows(T *grad, int64_t ldg, uint64_t total, uint32_t units, uint32_t dim) {
   const float z[VEC] = {};
   for (uint64_t u = (uint64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (uint64_t)gridDim.x * 256) {
     const uint64_t r = u / units;
-    store_f32<T, VEC>(grad + (int64_t)r * ldg + (int64_t)(u - r * units) * VEC, z);
+    stream_loose<T, VEC>(grad + (int64_t)r * ldg + col_of((uint32_t)(u - r * units) * VEC, dim, VEC), z);
   }
 }
 
 template <typename T, int VEC>
 int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_t stream) {
-  a.units = a.dim / VEC;
+  a.units = (a.dim + VEC - 1) / VEC;
+  a.width = a.units * VEC;
   if (a.n == 0) {
     if (a.accumulate) return SPLAT_OK;
     const uint64_t total = (uint64_t)a.rows * a.units;
     const uint64_t blocks = (total + 255) / 256;
     hipLaunchKernelGGL((k_zero_rows<T, VEC>), dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream,
-                       (T *)a.grad, a.ldg, total, (uint32_t)a.units);
+                       (T *)a.grad, a.ldg, total, (uint32_t)a.units, (uint32_t)a.dim);
     SPLAT_LAUNCH_CHECK();
     return SPLAT_OK;
   }
@@ -829,9 +850,7 @@ int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_
 int launch_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t ldt, const void *ids, int id_type,
                   int64_t n, float scale, void *out, int64_t ldo, hipStream_t stream) {
   if (n == 0 || dim == 0) return SPLAT_OK;
-  const int64_t strides[2] = {ldt, ldo};
-  const void *ptrs[2] = {table, out};
-  const int vec = vec_width(dtype_bytes(dtype), dim, strides, 2, ptrs, 2);
+  const int vec = pack_width(dtype_bytes(dtype), dim, false);
 #define GO(T, V)                                                                                              \
   return id_type == SPLAT_I64 ? run_lookup<T, V, int64_t>(table, ldt, rows, dim, ids, n, scale, out, ldo, stream) \
                               : run_lookup<T, V, int32_t>(table, ldt, rows, dim, ids, n, scale, out, ldo, stream)
@@ -862,9 +881,7 @@ int launch_lookup_bwd(const void *d_out, int dtype, int64_t ldy, const void *ids
   SumArgs a = {};
   a.dy = d_out; a.ldy = ldy; a.grad = d_table; a.ldg = ldg;
   a.n = (uint32_t)n; a.rows = (uint32_t)rows; a.dim = dim; a.scale = scale; a.accumulate = accumulate;
-  const int64_t strides[2] = {ldy, ldg};
-  const void *ptrs[2] = {n ? d_out : d_table, d_table};
-  const int vec = vec_width(dtype_bytes(dtype), dim, strides, 2, ptrs, 2);
+  const int vec = pack_width(dtype_bytes(dtype), dim, accumulate != 0);
 #define GO(T, V) return run_lookup_bwd<T, V>(a, ids, id_type, ws, stream)
   if (dtype == SPLAT_F16) { BY_VEC(f16_t) }
   if (dtype == SPLAT_BF16) { BY_VEC(bf16_t) }

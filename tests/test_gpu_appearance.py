@@ -172,6 +172,37 @@ def test_lookup_no_valid_ids_nan_and_strides(dev):
     assert A.lookup_backward(torch.empty(3, 0, device=dev), i[:3], 10).shape == (10, 0)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,rows", [(300, 40), (6000, 9), (9000, 5000)])
+def test_lookup_rows_at_any_element(dev, n, rows, dt):
+    """Rows of 1 to 33 elements that start anywhere in wider arrays: the same as of their
+    contiguous copies, and nothing beside them is written."""
+    from sphere_rasterization_amd import appearance as A
+    rng = np.random.default_rng(n + rows)
+    ids = torch.from_numpy(_ids(rng, n, rows, True, np.int64)).to(dev)
+    for dim in (1, 2, 3, 4, 7, 8, 9, 15, 16, 17, 31, 33):
+        for left, right in ((1, 0), (3, 2), (0, 1)):
+            def wide(k):
+                a = _put(rng.standard_normal((k, left + dim + right)), dt, dev)
+                return a, a[:, left:left + dim]
+            table, dy = wide(rows)[1], wide(n)[1]
+            ref = torch.where(((ids >= 0) & (ids < rows))[:, None], table[ids.clamp(0, rows - 1)], torch.zeros_like(dy))
+            assert torch.equal(A.lookup(table, ids), ref)
+            whole = A.lookup_backward(dy.contiguous(), ids, rows, 0.37)
+            for accumulate in (False, True):
+                a, out = wide(rows)
+                old = a.clone()
+                A.lookup_backward(dy, ids, rows, 0.37, out=out, accumulate=accumulate)
+                if accumulate:
+                    packed = old[:, left:left + dim].contiguous()
+                    A.lookup_backward(dy.contiguous(), ids, rows, 0.37, out=packed, accumulate=True)
+                    assert torch.equal(out, packed)
+                else:
+                    assert torch.equal(out, whole)
+                assert torch.equal(a[:, :left], old[:, :left])
+                assert torch.equal(a[:, left + dim:], old[:, left + dim:])
+
+
 def test_lookup_past_32_bits(dev):
     """A table whose offsets in bytes and in elements pass 2^31."""
     from sphere_rasterization_amd import appearance as A
