@@ -10,11 +10,12 @@
 // row is summed in a fixed order:
 //   1. counting sort by digits of up to 9 bits, least significant first: counts per
 //      tile of 1024 or 4096 tokens, a scan per digit, a scatter that ranks equal digits
-//      within a wave by ballots;
+//      within a wave by ballots (few tokens: one launch that counts and scatters);
 //   2. the sorted list is cut into chunks of 64; a chunk that lies within one row's
 //      segment is summed to one fp32 row, and 64 such sums to one of the next level;
 //   3. each row is written by adding its tokens, or its loose tokens and whole chunks.
-// So a row that holds all n tokens costs no lane more than 4 x 64 + n / 4096 adds.
+// So a row that holds all n tokens costs no lane more than 4 x 64 + n / 4096 adds. Few
+// tokens in few rows skip all of this (k_few_grads).
 #include "learn_common.h"
 
 namespace {
@@ -25,6 +26,11 @@ constexpr int ST_THREADS = 256;              // sort tiles: 4 or 16 tokens a thr
 constexpr int ST_WAVES = ST_THREADS / WAVE;
 constexpr int RADIX_BITS = 9, RADIX = 1 << RADIX_BITS;
 constexpr int CHUNK = 64;
+// Tokens up to which a sorting workgroup counts every tile's keys itself: a launch instead
+// of three for a digit, of a longer chain. Gradient of fp32 rows of 32 in us: 8192 tokens,
+// 65536 rows, even ids 31 (36 with counts of their own), skewed 35 (39), all alike 36 (34);
+// 16384 tokens, 200000 rows 40 (37), 46 (42), 52 (36); 4096 x 16 fp16, 1M rows 34 (47).
+constexpr uint32_t COUNT_ALONE = 8192;
 // Tokens up to which tiles are small: more workgroups for the same chain of rankings.
 constexpr int64_t SMALL_TILES = 256 << 10;
 constexpr int tile_items(int64_t n) { return n <= SMALL_TILES ? 4 : 16; }
@@ -108,11 +114,20 @@ struct KeySource<ID, false> {
   __device__ uint2 pair(Word x, uint32_t) const { return x; }
 };
 
-// counts[tile][digit]; also clears the rows' segment bounds (each thread a share).
+// Rows without tokens keep empty bounds. Workgroup `block` of `blocks`.
+__device__ __forceinline__ void clear_bounds(int2 *bounds, uint32_t nbounds, uint32_t block, uint32_t blocks) {
+  for (uint64_t r = block * ST_THREADS + threadIdx.x; r < nbounds; r += blocks * ST_THREADS) bounds[r] = make_int2(0, 0);
+}
+
+// counts[tile][digit]; workgroups past the tiles clear the rows' segment bounds.
 template <typename ID, bool FIRST, int ITEMS>
 __global__ __launch_bounds__(ST_THREADS) void k_sort_count(KeySource<ID, FIRST> src, int shift, int bits,
-                                                           uint32_t *__restrict__ counts, int2 *bounds,
-                                                           uint32_t nbounds) {
+                                                           uint32_t *__restrict__ counts, uint32_t tiles,
+                                                           int2 *bounds, uint32_t nbounds) {
+  if (blockIdx.x >= tiles) {
+    clear_bounds(bounds, nbounds, blockIdx.x - tiles, gridDim.x - tiles);
+    return;
+  }
   __shared__ uint32_t h[RADIX];
   for (int d = threadIdx.x; d < RADIX; d += ST_THREADS) h[d] = 0;
   const uint32_t mask = (1u << bits) - 1u, i0 = blockIdx.x * (uint32_t)(ST_THREADS * ITEMS) + threadIdx.x;
@@ -123,9 +138,6 @@ __global__ __launch_bounds__(ST_THREADS) void k_sort_count(KeySource<ID, FIRST> 
 #pragma unroll
   for (int j = 0; j < ITEMS; j++)
     if (i0 + j * ST_THREADS < src.n) atomicAdd(&h[(src.pair(word[j], 0).x >> shift) & mask], 1u);
-  if (bounds)
-    for (uint32_t r = blockIdx.x * ST_THREADS + threadIdx.x; r < nbounds; r += gridDim.x * ST_THREADS)
-      bounds[r] = make_int2(0, 0);
   __syncthreads();
   for (int d = threadIdx.x; d < (1 << bits); d += ST_THREADS) counts[((size_t)blockIdx.x << bits) + d] = h[d];
 }
@@ -220,12 +232,19 @@ __device__ __forceinline__ uint32_t wave_rank(uint32_t digit, int bits, bool ok,
 
 // The tile's pairs are put in digit order in LDS first, so that a wave's store covers a
 // few runs of consecutive pairs instead of 64 places.
-template <typename ID, bool FIRST, int ITEMS>
+// COUNTS: a workgroup counts all keys for itself, and the pass is one launch; workgroups
+// past the tiles clear the rows' bounds.
+template <typename ID, bool FIRST, int ITEMS, bool COUNTS>
 __global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID, FIRST> src, int shift, int bits,
                                                              const uint32_t *__restrict__ counts,
                                                              const uint32_t *__restrict__ totals,
-                                                             uint2 *__restrict__ out) {
+                                                             uint2 *__restrict__ out, uint32_t tiles, int2 *bounds,
+                                                             uint32_t nbounds) {
   constexpr int ST_TILE = ST_THREADS * ITEMS;
+  if (COUNTS && blockIdx.x >= tiles) {
+    clear_bounds(bounds, nbounds, blockIdx.x - tiles, gridDim.x - tiles);
+    return;
+  }
   __shared__ uint32_t hist[ST_WAVES][RADIX];   // a wave's counts, then its first place in the tile, per digit
   __shared__ uint32_t away[RADIX];             // a digit's first place in the output less that in the tile
   __shared__ uint2 tile[ST_TILE];
@@ -241,12 +260,36 @@ __global__ __launch_bounds__(ST_THREADS) void k_sort_scatter(KeySource<ID, FIRST
   for (int j = 0; j < ITEMS; j++) word[j] = src.word(i0 + j * WAVE);
   constexpr int DPT = RADIX / ST_THREADS;
   uint32_t tot[DPT], cnt[DPT], sum = 0, all;
+  if (COUNTS) {
+    // keys of the tiles before this one, and of the others
+    __shared__ uint32_t h[2][RADIX];
+    for (int d = threadIdx.x; d < 2 * RADIX; d += ST_THREADS) (&h[0][0])[d] = 0;
+    __syncthreads();
+    constexpr int FLIGHT = 8;
+    for (uint32_t i = threadIdx.x; i < src.n; i += ST_THREADS * FLIGHT) {
+      typename KeySource<ID, FIRST>::Word x[FLIGHT];
 #pragma unroll
-  for (int k = 0; k < DPT; k++) {
-    const uint32_t d = threadIdx.x * DPT + k;
-    tot[k] = d <= mask ? totals[d] : 0u;
-    cnt[k] = d <= mask ? counts[((size_t)blockIdx.x << bits) + d] : 0u;
-    sum += tot[k];
+      for (int j = 0; j < FLIGHT; j++) x[j] = src.word(i + j * ST_THREADS);
+#pragma unroll
+      for (int j = 0; j < FLIGHT; j++)
+        if (i + j * ST_THREADS < src.n)
+          atomicAdd(&h[i + j * ST_THREADS >= t0][(src.pair(x[j], 0).x >> shift) & mask], 1u);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < DPT; k++) {
+      cnt[k] = h[0][threadIdx.x * DPT + k];
+      tot[k] = cnt[k] + h[1][threadIdx.x * DPT + k];
+      sum += tot[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < DPT; k++) {
+      const uint32_t d = threadIdx.x * DPT + k;
+      tot[k] = d <= mask ? totals[d] : 0u;
+      cnt[k] = d <= mask ? counts[((size_t)blockIdx.x << bits) + d] : 0u;
+      sum += tot[k];
+    }
   }
 #pragma unroll
   for (int j = 0; j < ITEMS; j++) pair[j] = src.pair(word[j], i0 + j * WAVE);
@@ -321,7 +364,7 @@ __device__ __forceinline__ Place place_of(const SumArgs &a, uint32_t slice) {
   q.lane = threadIdx.x & 63;
   q.G = 64u >> a.lg;
   q.g = q.lane >> a.lg;
-  const int unit = (int)(slice << 6) + (int)(q.lane & ((1u << a.lg) - 1u));
+  const int unit = (int)(slice << a.lg) + (int)(q.lane & ((1u << a.lg) - 1u));
   q.on = unit < a.units;
   q.sum = unit * VEC;
   q.col = (int)col_of((uint32_t)q.sum, (uint32_t)a.dim, VEC);
@@ -545,15 +588,22 @@ __global__ __launch_bounds__(256) void k_row_grads(SumArgs a) {
 // row to the whole workgroup, each wave taking every eighth part of 64 entries. Nothing is
 // sorted, and no workspace is needed. What bounds it is its chain of waits: ids, rows,
 // stores.
+// Every row of a run walks the run's whole list, so the rule bounds a run's rows times its
+// tokens. In us, even and skewed ids, here and sorted: 4096 tokens in 8000 rows x 64 fp32 10
+// and 16 (25 and 29), 1000 in 4000 x 16 fp16 10 and 10 (23 and 30); past the rule 4096 in
+// 60000 x 32 fp32 14 and 94 (25 and 27), 1000 in 1M x 16 fp16 103 and 975 (28 and 33).
 constexpr int FW_THREADS = 512, FW_WAVES = FW_THREADS / WAVE, FW_ITEMS = 8;
-constexpr int FEW = FW_THREADS * FW_ITEMS;
+constexpr int64_t FEW = FW_THREADS * FW_ITEMS;
 constexpr int FW_LONG = 256;               // entries from which the workgroup works together
-constexpr uint32_t FW_RUNS = 1024;         // runs of rows, at most
+constexpr int64_t FW_RUNS = 1024;          // runs of rows, at most
+constexpr int64_t few_run(int64_t rows) { return (rows + FW_RUNS - 1) / FW_RUNS; }
+constexpr bool few_tokens(int64_t n, int64_t rows) { return n <= FEW && few_run(rows) * (n + 1024) <= 65536; }
 
 // Adds the rows of the tokens buf[0 .. m), m <= 64, to acc, the wave's row lanes in turn.
 template <typename T, int VEC>
 __device__ __forceinline__ void add_few(const SumArgs &a, const uint16_t *buf, uint32_t m, const Place &q, float (&acc)[VEC]) {
   const T *dy = (const T *)a.dy + q.col;
+  float sum[VEC] = {};                         // of their own: chains stay short
   for (uint32_t k0 = 0; k0 < m; k0 += DEEP * q.G) {
     Raw<T, VEC> x[DEEP];
 #pragma unroll
@@ -566,14 +616,16 @@ __device__ __forceinline__ void add_few(const SumArgs &a, const uint16_t *buf, u
       float v[VEC];
       to_f32<T, VEC>(x[k], v);
 #pragma unroll
-      for (int j = 0; j < VEC; j++) acc[j] += v[j];
+      for (int j = 0; j < VEC; j++) sum[j] += v[j];
     }
   }
+#pragma unroll
+  for (int j = 0; j < VEC; j++) acc[j] += sum[j];
 }
 
 template <typename T, int VEC, typename ID>
 __global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *__restrict__ ids, uint32_t run) {
-  __shared__ uint32_t s_row[FEW];            // row within the run, then token, of each entry
+  __shared__ uint16_t s_row[FEW];            // row within the run, and token, of each entry
   __shared__ uint16_t s_tok[FEW];
   __shared__ uint16_t s_buf[FW_WAVES][128];
   __shared__ uint32_t s_cnt[FW_WAVES];
@@ -607,7 +659,7 @@ __global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *_
 #pragma unroll
   for (int j = 0; j < FW_ITEMS; j++)
     if (row[j] < rows) {
-      s_row[base + rank[j]] = row[j];
+      s_row[base + rank[j]] = (uint16_t)row[j];
       s_tok[base + rank[j]] = (uint16_t)(i0 + j * WAVE);
     }
   __syncthreads();
@@ -736,18 +788,26 @@ int sort_passes(const ID *ids, uint32_t n, uint32_t rows, int bits, int passes, 
   constexpr uint32_t TOKENS = ST_THREADS * ITEMS;
   const uint32_t tiles = (n + TOKENS - 1) / TOKENS;
   const int dbits = (bits + passes - 1) / passes;
-  auto pass = [&](auto src, auto count, auto scatter, int p) -> int {
+  const bool alone = n <= COUNT_ALONE;
+  auto pass = [&](auto src, auto count, auto scatter, auto whole, int p) -> int {
     const int shift = p * dbits, b = bits - shift < dbits ? bits - shift : dbits;
     src.n = n;
     src.rows = rows;
-    hipLaunchKernelGGL(count, dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, L.counts,
-                       p ? (int2 *)nullptr : L.bounds, rows);
+    const unsigned clear = p ? 0u : rows < 1024u * ST_THREADS ? (rows + ST_THREADS - 1) / ST_THREADS : 1024u;
+    if (alone) {
+      hipLaunchKernelGGL(whole, dim3(tiles + clear), dim3(ST_THREADS), 0, stream, src, shift, b, nullptr, nullptr,
+                         L.pairs[p & 1], tiles, L.bounds, rows);
+      SPLAT_LAUNCH_CHECK();
+      return SPLAT_OK;
+    }
+    hipLaunchKernelGGL(count, dim3(tiles + clear), dim3(ST_THREADS), 0, stream, src, shift, b, L.counts, tiles, L.bounds,
+                       rows);
     SPLAT_LAUNCH_CHECK();
     hipLaunchKernelGGL(k_sort_scan, dim3(((1u << b) + SC_DIGITS - 1) / SC_DIGITS), dim3(SC_THREADS), 0, stream, L.counts,
                        tiles, 1u << b, L.totals);
     SPLAT_LAUNCH_CHECK();
     hipLaunchKernelGGL(scatter, dim3(tiles), dim3(ST_THREADS), 0, stream, src, shift, b, L.counts, L.totals,
-                       L.pairs[p & 1]);
+                       L.pairs[p & 1], tiles, nullptr, 0u);
     SPLAT_LAUNCH_CHECK();
     return SPLAT_OK;
   };
@@ -756,11 +816,13 @@ int sort_passes(const ID *ids, uint32_t n, uint32_t rows, int bits, int passes, 
     if (p == 0) {
       KeySource<ID, true> src;
       src.from = ids;
-      st = pass(src, k_sort_count<ID, true, ITEMS>, k_sort_scatter<ID, true, ITEMS>, p);
+      st = pass(src, k_sort_count<ID, true, ITEMS>, k_sort_scatter<ID, true, ITEMS, false>,
+                k_sort_scatter<ID, true, 4, true>, p);
     } else {
       KeySource<ID, false> src;
       src.from = L.pairs[(p - 1) & 1];
-      st = pass(src, k_sort_count<ID, false, ITEMS>, k_sort_scatter<ID, false, ITEMS>, p);
+      st = pass(src, k_sort_count<ID, false, ITEMS>, k_sort_scatter<ID, false, ITEMS, false>,
+                k_sort_scatter<ID, false, 4, true>, p);
     }
     if (st) return st;
   }
@@ -788,6 +850,15 @@ __global__ __launch_bounds__(256) void k_zero_rows(T *grad, int64_t ldg, uint64_
   }
 }
 
+template <typename T, int VEC, typename ID>
+int run_few(SumArgs a, const void *ids, hipStream_t stream) {
+  const uint32_t run = (uint32_t)few_run(a.rows);
+  const dim3 grid((a.rows + run - 1) / run, (unsigned)a.slices);
+  hipLaunchKernelGGL((k_few_grads<T, VEC, ID>), grid, dim3(FW_THREADS), 0, stream, a, (const ID *)ids, run);
+  SPLAT_LAUNCH_CHECK();
+  return SPLAT_OK;
+}
+
 template <typename T, int VEC>
 int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_t stream) {
   a.units = (a.dim + VEC - 1) / VEC;
@@ -804,16 +875,8 @@ int run_lookup_bwd(SumArgs a, const void *ids, int id_type, void *ws, hipStream_
   a.lg = 0;
   while (a.lg < 6 && (1 << a.lg) < a.units) a.lg++;
   a.slices = (a.units + 63) / 64;
-  if (a.n <= FEW) {
-    const uint32_t run = (a.rows + FW_RUNS - 1) / FW_RUNS;
-    const dim3 grid((a.rows + run - 1) / run, (unsigned)a.slices);
-    if (id_type == SPLAT_I64)
-      hipLaunchKernelGGL((k_few_grads<T, VEC, int64_t>), grid, dim3(FW_THREADS), 0, stream, a, (const int64_t *)ids, run);
-    else
-      hipLaunchKernelGGL((k_few_grads<T, VEC, int32_t>), grid, dim3(FW_THREADS), 0, stream, a, (const int32_t *)ids, run);
-    SPLAT_LAUNCH_CHECK();
-    return SPLAT_OK;
-  }
+  if (few_tokens(a.n, a.rows))
+    return id_type == SPLAT_I64 ? run_few<T, VEC, int64_t>(a, ids, stream) : run_few<T, VEC, int32_t>(a, ids, stream);
   const BwdLayout L = bwd_layout(ws, a.n, a.rows, a.dim);
   int half = 0;
   const int st = id_type == SPLAT_I64 ? sort_tokens<int64_t>(ids, a.n, a.rows, L, &half, stream)
@@ -872,7 +935,7 @@ int launch_lookup(const void *table, int dtype, int64_t rows, int dim, int64_t l
 }
 
 size_t lookup_bwd_workspace_bytes(int64_t n, int64_t rows, int dim) {
-  return n <= FEW ? 0 : bwd_layout(nullptr, n, rows, dim).bytes;
+  return few_tokens(n, rows) ? 0 : bwd_layout(nullptr, n, rows, dim).bytes;
 }
 
 int launch_lookup_bwd(const void *d_out, int dtype, int64_t ldy, const void *ids, int id_type, int64_t n, int64_t rows,

@@ -99,6 +99,14 @@ def test_lookup_backward(dev, n, rows, dim, dt):
         _check(acc, full, tol + 2 * (U + RO[dt]) * (np.abs(full) + np.abs(_np(old))), "accumulated gradient")
 
 
+@pytest.mark.parametrize("n,rows,dim", [(4096, 12288, 5), (4096, 12289, 5), (4096, 200000, 3), (40, 70001, 8), (12, 70001, 8),
+                                        (8192, 3000, 5), (8193, 3000, 5), (5000, 300000, 2), (262145, 511, 3)])
+def test_lookup_backward_around_its_rules(dev, n, rows, dim):
+    """Sizes on both sides of where the gradient goes over to sorting, to sorting with
+    counts of its own, and to larger tiles."""
+    test_lookup_backward(dev, n, rows, dim, "f32")
+
+
 def test_lookup_large_and_skewed(dev):
     """Many tokens: several sort passes, both chunk levels, one row with a third of all."""
     from sphere_rasterization_amd import appearance as A
