@@ -749,8 +749,9 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_zero_params(NormArgs a) {
 }
 
 // ---- launches -----------------------------------------------------------------------
-// Pieces for a pass: about `target` workgroups, each with at least `least` pixel steps
-// per thread so that its constants and its share of the join are paid for.
+// Pieces for a pass over a.P > 0 pixels: about `target` workgroups, each with at least
+// `least` pixel steps per thread so that its constants and its share of the join are paid
+// for.
 void split(NormArgs &a, int vec, int64_t target, int64_t least) {
   a.units = a.C / vec;
   a.us = a.units < GN_THREADS ? a.units : GN_THREADS;
@@ -900,6 +901,7 @@ int dispatch(const NormArgs &a, int dtype, int vec, int act, bool bwd, hipStream
 // For any pack width: the pieces of the narrowest width are the most. Alignment decides
 // whether a group fits one workgroup, so only groups that fit at every width need nothing.
 size_t group_norm_workspace_bytes(const splat_norm *d, bool bwd) {
+  if (d->images == 0 || d->pixels == 0) return 0;      // no values, no passes
   NormArgs a = norm_args(d, nullptr, nullptr, nullptr);
   size_t most = 0;
   for (int vec = 16 / dtype_bytes(d->dtype); vec >= 1; vec >>= 1) {

@@ -123,6 +123,20 @@ def test_sizes_of_zero_touch_nothing():
                                    None) == L.SPLAT_OK
 
 
+@pytest.mark.parametrize("images", [0, 1, 2, 600])
+@pytest.mark.parametrize("channels,groups", [(8, 2), (9, 3), (1, 1), (4096, 1)])
+def test_group_norm_of_no_pixels(images, channels, groups):
+    """Neither query divides by the pixels, and the backward wants nothing for them."""
+    for dtype in (L.SPLAT_F32, L.SPLAT_F16, L.SPLAT_BF16):
+        d = _norm(images=images, pixels=0, channels=channels, groups=groups, dtype=dtype, param_dtype=dtype,
+                  x_pixel_stride=channels, y_pixel_stride=channels, dx_pixel_stride=channels, x_image_stride=channels,
+                  y_image_stride=channels, dx_image_stride=channels)
+        assert L.splat_group_norm_workspace_bytes(d, False) == 0
+        assert L.splat_group_norm_workspace_bytes(d, True) == 0
+        assert L.lib().splat_group_norm_bwd(C.byref(d), None, None, None, None, None, None, None, None, None, None, 0,
+                                            None) == L.SPLAT_OK
+
+
 def test_python_refusals_without_a_gpu():
     from sphere_rasterization_amd import appearance as A
     t = torch.zeros(4, 8)
