@@ -281,9 +281,10 @@ int check_norm(const splat_norm *m, bool bwd, bool writes) {
   const int64_t pix[3] = {m->x_pixel_stride, m->y_pixel_stride, m->dx_pixel_stride};
   for (int k = 0; k < (bwd && writes ? 3 : 2); k++)
     CHECK(stride_fits(img[k], m->images) && stride_fits(pix[k], m->pixels), SPLAT_ERR_INVALID_ARG, "stride");
-  // x and d_y may repeat pixels or images (stride 0); the image written may not
+  // x and d_y may repeat pixels or images (stride 0); the image written may not (without
+  // pixels there is none)
   const int o = bwd ? 2 : 1;
-  if (writes)
+  if (writes && m->pixels > 0)
     CHECK((m->pixels <= 1 || pix[o] >= m->channels) && (m->images <= 1 || img[o] >= m->channels),
           SPLAT_ERR_INVALID_ARG, "output pixels overlap");
   return SPLAT_OK;

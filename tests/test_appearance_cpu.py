@@ -137,6 +137,16 @@ def test_group_norm_of_no_pixels(images, channels, groups):
                                             None) == L.SPLAT_OK
 
 
+def test_packed_images_of_no_pixels_do_not_overlap():
+    """Packed images of no pixels lie zero elements apart, as a contiguous tensor's do."""
+    d = _norm(images=3, pixels=0, x_image_stride=0, y_image_stride=0, dx_image_stride=0)
+    assert L.lib().splat_group_norm_bwd(C.byref(d), None, None, P, P, None, None, P, None, None, None, 0,
+                                        None) == L.SPLAT_OK
+    d.pixels = 1
+    assert L.lib().splat_group_norm_bwd(C.byref(d), P, P, P, P, None, None, P, None, None, P, 1 << 20,
+                                        None) == L.SPLAT_ERR_INVALID_ARG
+
+
 def test_python_refusals_without_a_gpu():
     from sphere_rasterization_amd import appearance as A
     t = torch.zeros(4, 8)
