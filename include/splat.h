@@ -350,7 +350,8 @@ size_t splat_group_norm_workspace_bytes(const splat_norm *norm, int backward);
 
 /* y = act(weight (x - mean) rstd + bias), rstd = 1 / sqrt(var + eps). weight and bias
  * [channels] may be NULL (1 and 0). mean, rstd [images][groups] fp32 receive the
- * statistics, which splat_group_norm_bwd reads. */
+ * statistics, which splat_group_norm_bwd reads; those of no pixels are 0 and
+ * 1 / sqrt(eps). */
 int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, const void *bias, void *y,
                      float *mean, float *rstd, void *workspace, size_t ws_bytes, hipStream_t stream);
 

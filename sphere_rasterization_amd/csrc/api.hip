@@ -586,8 +586,8 @@ int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, 
                      float *mean, float *rstd, void *workspace, size_t ws_bytes, hipStream_t stream) {
   int st = check_norm(norm, false, true);
   if (st) return st;
-  if (norm->images == 0 || norm->pixels == 0) return SPLAT_OK;
-  CHECK(x && y && mean && rstd, SPLAT_ERR_INVALID_ARG, "NULL array");
+  if (norm->images == 0) return SPLAT_OK;
+  CHECK(((x && y) || norm->pixels == 0) && mean && rstd, SPLAT_ERR_INVALID_ARG, "NULL array");
   CHECK(aligned_to(x, norm->dtype) && aligned_to(y, norm->dtype) && aligned_to(weight, norm->param_dtype) &&
             aligned_to(bias, norm->param_dtype) && aligned_to(mean, SPLAT_F32) && aligned_to(rstd, SPLAT_F32),
         SPLAT_ERR_INVALID_ARG, "array not aligned to its element");

@@ -748,6 +748,14 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_zero_params(NormArgs a) {
   }
 }
 
+// The statistics of no pixels: mean 0 and variance 0.
+__global__ __launch_bounds__(GN_THREADS) void k_norm_empty_stats(NormArgs a) {
+  for (int64_t i = (int64_t)blockIdx.x * GN_THREADS + threadIdx.x; i < a.N * a.G; i += (int64_t)gridDim.x * GN_THREADS) {
+    a.mean[i] = 0.0f;
+    a.rstd[i] = 1.0f / sqrtf(a.eps);
+  }
+}
+
 // ---- launches -----------------------------------------------------------------------
 // Pieces for a pass over a.P > 0 pixels: about `target` workgroups, each with at least
 // `least` pixel steps per thread so that its constants and its share of the join are paid
@@ -920,12 +928,18 @@ size_t group_norm_workspace_bytes(const splat_norm *d, bool bwd) {
 
 int launch_group_norm(const splat_norm *d, const void *x, const void *w, const void *b, void *y, float *mean,
                       float *rstd, void *ws, hipStream_t stream) {
-  if (d->images == 0 || d->pixels == 0) return SPLAT_OK;
+  if (d->images == 0) return SPLAT_OK;
   NormArgs a = norm_args(d, x, w, b);
   a.y = y;
   a.mean = mean;
   a.rstd = rstd;
   a.part = (float2 *)ws;
+  if (d->pixels == 0) {
+    hipLaunchKernelGGL(k_norm_empty_stats, dim3(blocks_of((a.N * a.G + GN_THREADS - 1) / GN_THREADS)), dim3(GN_THREADS),
+                       0, stream, a);
+    SPLAT_LAUNCH_CHECK();
+    return SPLAT_OK;
+  }
   return dispatch(a, d->dtype, norm_vec(d, x, y, nullptr, GS_FWD), d->act, false, stream);
 }
 

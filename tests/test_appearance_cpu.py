@@ -147,6 +147,12 @@ def test_packed_images_of_no_pixels_do_not_overlap():
                                         None) == L.SPLAT_ERR_INVALID_ARG
 
 
+def test_group_norm_of_no_pixels_still_has_statistics_to_write():
+    f, d = L.lib().splat_group_norm, _norm(pixels=0)
+    for mean, rstd in ((None, P), (P, None), (C.c_void_p(258), P)):
+        assert f(C.byref(d), None, None, None, None, mean, rstd, None, 0, None) == L.SPLAT_ERR_INVALID_ARG
+
+
 def test_python_refusals_without_a_gpu():
     from sphere_rasterization_amd import appearance as A
     t = torch.zeros(4, 8)

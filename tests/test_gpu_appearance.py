@@ -337,6 +337,31 @@ def test_group_norm_constant_nonfinite_and_params(dev):
     assert y.shape == e.shape and (dw == 0).all() and (db == 0).all() and dw.shape == (8,)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 0, 8), (0, 0, 8), (3, 4, 0, 8), (0, 5, 8), (600, 0, 8)])
+def test_group_norm_of_no_values(dev, shape, dt):
+    """No pixels or no images: statistics of nothing are 0 and 1 / sqrt(eps), gradients zero."""
+    from sphere_rasterization_amd import appearance as A
+    eps, n = 1e-3, shape[0]
+    x = torch.empty(shape, dtype=DT[dt], device=dev)
+    w = torch.randn(8, device=dev, requires_grad=True)
+    b = torch.randn(8, device=dev, requires_grad=True)
+    for _ in range(2):                                        # the second time on used memory
+        held = torch.full((2, n, 2), 7.0, device=dev)
+        del held
+        y, mean, rstd = A.group_norm_forward(x, 2, w.detach(), b.detach(), eps, "silu")
+        assert y.shape == x.shape and y.dtype == x.dtype and mean.shape == rstd.shape == (n, 2)
+        assert (mean == 0).all()
+        ref = np.float32(eps) ** np.float64(-0.5)
+        assert ((rstd.double() - ref).abs() <= 4 * U * ref).all()
+    dx, dw, db = A.group_norm_backward(x, x, mean, rstd, w.detach(), b.detach(), "silu")
+    assert dx.shape == x.shape and (dw == 0).all() and (db == 0).all() and dw.shape == db.shape == (8,)
+    with torch.no_grad():
+        assert A.group_norm(x, 2, w, b, act="gelu").shape == x.shape
+    A.group_norm(x.requires_grad_(), 2, w, b, act="gelu").sum().backward()
+    assert x.grad.shape == x.shape and (w.grad == 0).all() and (b.grad == 0).all()
+
+
 def test_group_norm_strides(dev):
     """Images inside wider ones, channels_last tensors, transposed pixels, odd alignment,
     repeated gradients: the same bits as on packed copies."""
