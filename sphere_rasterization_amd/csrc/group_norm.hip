@@ -158,6 +158,11 @@ __device__ __forceinline__ int lane_pixels(int64_t pixels, int l, int TP) {
 }
 
 // ---- statistics ---------------------------------------------------------------------
+// d^2 for a difference from the mean of cnt values. With none before there is nothing to
+// differ from, and d is the value itself, whose square may overflow (past 1.8e19) where no
+// deviation does.
+__device__ __forceinline__ float square_from(float d, float cnt) { return cnt > 0.0f ? d * d : 0.0f; }
+
 template <typename T, int VEC>
 __global__ __launch_bounds__(GN_THREADS) void k_norm_stats(NormArgs a) {
   __shared__ float s_mean[GN_THREADS * VEC], s_m2[GN_THREADS * VEC];
@@ -192,7 +197,7 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_stats(NormArgs a) {
             qb = __builtin_fmaf(e, e, qb);
           }
           mean[j] = __builtin_fmaf(d, r, mean[j]);
-          m2[j] = __builtin_fmaf(d * d, f, m2[j] + qb);
+          m2[j] = __builtin_fmaf(square_from(d, cnt), f, m2[j] + qb);
         }
         cnt = all;
       }
@@ -204,7 +209,7 @@ __global__ __launch_bounds__(GN_THREADS) void k_norm_stats(NormArgs a) {
         for (int j = 0; j < VEC; j++) {
           const float d = v[j] - mean[j];
           mean[j] = __builtin_fmaf(d, r, mean[j]);
-          m2[j] = __builtin_fmaf(d * d, cnt * r, m2[j]);
+          m2[j] = __builtin_fmaf(square_from(d, cnt), cnt * r, m2[j]);
         }
         cnt = all;
       }

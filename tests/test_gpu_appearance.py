@@ -309,6 +309,27 @@ def test_group_norm_far_from_zero(dev):
         _check(y, f["y"], (rel + 2 * rel * rel + DEPTH * U) * (1 + np.abs(f["y"])), "y")
 
 
+@pytest.mark.parametrize("images,shape,c,groups,dt,sd", [
+    (1, (300, 200), 32, 8, "f32", 1e16), (1, (130, 129), 24, 4, "f32", 1e16), (2, (33, 47), 64, 8, "f32", 1e16),
+    (1, (9000,), 1, 1, "f32", 1e16), (200, (3, 5), 16, 8, "f32", 1e18), (200, (3, 5), 16, 8, "bf16", 1e18)])
+def test_group_norm_of_values_whose_squares_overflow(dev, images, shape, c, groups, dt, sd):
+    """1e20 +- sd: the values' squares are beyond fp32, their deviations' are not, nor the
+    sum of a group's (n sd^2 < 2^125), which any fp32 evaluation has to hold."""
+    from sphere_rasterization_amd import appearance as A
+    rng = np.random.default_rng(22)
+    x = _put(1e20 + sd * rng.standard_normal((images,) + shape + (c,)), dt, dev)
+    dy = _put(rng.standard_normal(x.shape), dt, dev)
+    y, mean, rstd = A.group_norm_forward(x, groups)
+    f = O.group_norm_backward(_np(dy), _np(x), groups)
+    # a mean off by DEPTH U of itself, in units of the deviation
+    rel = DEPTH * U * 1.1e20 * f["rstd"].max()
+    _check(mean, f["mean"], DEPTH * U * np.abs(f["mean"]) * 1.1, "mean")
+    _check(rstd, f["rstd"], (2 * DEPTH * U + 2 * rel * rel) * f["rstd"], "rstd")
+    _check(y, f["y"], (rel + 2 * rel * rel + DEPTH * U) * (1 + np.abs(f["y"])) + 1.01 * RO[dt] * np.abs(f["y"]), "y")
+    dx, dw, db = A.group_norm_backward(dy, x, mean, rstd)
+    assert all(torch.isfinite(t).all() for t in (dx, dw, db))
+
+
 def test_group_norm_constant_nonfinite_and_params(dev):
     from sphere_rasterization_amd import appearance as A
     x = torch.full((2, 5, 4), 7.0, device=dev)
