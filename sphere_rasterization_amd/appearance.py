@@ -6,7 +6,8 @@
     step = orthogonalize(momentum)                     # update of the network's matrices
 
 `lookup` and `group_norm` carry autograd; `lookup_backward`, `group_norm_forward` and
-`group_norm_backward` are the same kernels without it. Every step runs in libsplat's HIP
+`group_norm_backward` are the same kernels without it. Forward-mode derivatives are refused:
+a tensor with a tangent raises NotImplementedError. Every step runs in libsplat's HIP
 kernels (csrc/lookup.hip, csrc/group_norm.hip, csrc/orthogonalize.hip); torch provides
 device memory and the stream. Tensors are float32, float16 or bfloat16 on one GPU, and
 work is enqueued on that GPU's current stream. Arithmetic is fp32 with one rounding at
@@ -20,6 +21,7 @@ import math
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _lib as L
@@ -42,6 +44,15 @@ def _like(name: str, t: torch.Tensor, ref: torch.Tensor, shape, dtypes):
     if t.device != ref.device or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected {tuple(shape)} of {' or '.join(str(d) for d in dtypes)} on {ref.device}, "
                          f"got {tuple(t.shape)} of {t.dtype} on {t.device}")
+
+
+def _no_tangents(*tensors: Optional[torch.Tensor]):
+    """Refuses dual tensors: the kernels see no tangents, and would drop them in silence."""
+    if forward_ad._current_level < 0:        # outside every dual level
+        return
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("forward-mode derivatives of the appearance operators are not available")
 
 
 def _launch(t: torch.Tensor, fn, *args):
@@ -100,6 +111,7 @@ def lookup_backward(d_out: torch.Tensor, ids: torch.Tensor, rows: int, scale: fl
     """Gradient of `lookup` w.r.t. its table of `rows` rows: d_table[v] = scale * (sum of
     d_out over the tokens whose id is v). `out` [rows, dim] receives it (added to what it
     holds with accumulate=True); a new tensor of d_out's type otherwise."""
+    _no_tangents(d_out, out)
     dt = _dtype("d_out", d_out)
     it = _check_ids(ids, d_out)
     if d_out.dim() < 1 or tuple(d_out.shape[:-1]) != tuple(ids.shape):
@@ -139,6 +151,7 @@ def lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0) -> torch.
     """scale * table[ids]: rows of a feature table that primitives share, [*ids.shape, dim].
     Ids outside [0, rows) (primitives without an entry, -1 say) give zeros and receive no
     gradient. The gradient is dense, [rows, dim]."""
+    _no_tangents(table)
     if torch.is_grad_enabled() and table.requires_grad:
         return _Lookup.apply(table, ids, float(scale))
     return _lookup(table, ids, float(scale))
@@ -209,6 +222,7 @@ def group_norm_forward(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
                        bias: Optional[torch.Tensor] = None, eps: float = 1e-5, act: str = "none"):
     """(y, mean, rstd) of `group_norm`: mean and rstd [images, groups] are what the
     backward needs besides x."""
+    _no_tangents(x, weight, bias)
     y, stats = _group_norm(x, groups, weight, bias, eps, act, True)
     return y, stats[0], stats[1]
 
@@ -219,6 +233,7 @@ def group_norm_backward(d_y: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, 
     """(d_x, d_weight, d_bias) given d_y and the forward's x, mean and rstd; None for what
     `want` leaves out. d_weight and d_bias have the type of weight and bias (of x without
     either)."""
+    _no_tangents(d_y, x, mean, rstd, weight, bias)
     if mean.dim() != 2:
         raise ValueError(f"mean: expected [images, groups], got {tuple(mean.shape)}")
     d = _norm_desc(x, weight, bias, mean.shape[1], act, 0.0)
@@ -264,6 +279,7 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
     channels / groups channels of a group. act: none, relu, silu or gelu (with erf).
     weight and bias [channels], float32 or x's type. An NCHW tensor in torch's
     channels_last memory format is read in place as x.permute(0, 2, 3, 1)."""
+    _no_tangents(x, weight, bias)
     if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
                                     or (bias is not None and bias.requires_grad)):
         return _GroupNorm.apply(x, groups, weight, bias, eps, act)
@@ -278,6 +294,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = (3.
     one): X = g / (|g| + eps), then `steps` times X <- (a I + b A + c A A) X with A = X X^T
     (X transposed if rows > cols). For updates: no autograd. At most 65536 rows and
     columns and 65535 matrices."""
+    _no_tangents(g)
     if g.dim() < 2:
         raise ValueError(f"g: expected [..., rows, cols], got {tuple(g.shape)}")
     dt = _dtype("g", g)

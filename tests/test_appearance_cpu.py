@@ -169,3 +169,21 @@ def test_python_refusals_without_a_gpu():
         A.group_norm(t[0], 2)
     with pytest.raises(ValueError, match="rows, cols"):
         A.orthogonalize(t[0])
+
+
+def test_forward_mode_is_refused():
+    """A tangent can not be followed through the kernels: it is refused, not dropped."""
+    import torch.autograd.forward_ad as fwd
+    from sphere_rasterization_amd import appearance as A
+    t, ids, w = torch.zeros(4, 8), torch.zeros(3, dtype=torch.int64), torch.ones(8)
+    with fwd.dual_level():
+        dual, dual_w = fwd.make_dual(t, torch.ones_like(t)), fwd.make_dual(w, torch.ones_like(w))
+        for call in (lambda: A.lookup(dual, ids), lambda: A.group_norm(dual, 2), lambda: A.group_norm(t, 2, dual_w),
+                     lambda: A.group_norm(t, 2, w, dual_w), lambda: A.orthogonalize(dual),
+                     lambda: A.lookup_backward(dual[:3], ids, 4), lambda: A.group_norm_forward(dual, 2),
+                     lambda: A.group_norm_backward(dual, t, torch.zeros(4, 2), torch.zeros(4, 2)),
+                     lambda: A.lookup(dual.requires_grad_(), ids)):
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                call()
+        with pytest.raises(ValueError, match="GPU tensor"):   # no tangent: as ever
+            A.lookup(t, ids)
