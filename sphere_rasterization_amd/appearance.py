@@ -40,6 +40,16 @@ def _dtype(name: str, t: torch.Tensor) -> int:
     return code
 
 
+def _int32(name: str, v) -> int:
+    """v as the C calls take it: ctypes would keep the low 32 bits of a larger number."""
+    k = int(v)
+    if k != v:
+        raise ValueError(f"{name}: expected a whole number, got {v!r}")
+    if not -(1 << 31) <= k < 1 << 31:
+        raise ValueError(f"{name}: expected less than 2^31, got {k}")
+    return k
+
+
 def _like(name: str, t: torch.Tensor, ref: torch.Tensor, shape, dtypes):
     if t.device != ref.device or t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected {tuple(shape)} of {' or '.join(str(d) for d in dtypes)} on {ref.device}, "
@@ -98,8 +108,8 @@ def _lookup(table: torch.Tensor, ids: torch.Tensor, scale: float) -> torch.Tenso
         raise ValueError(f"table: expected [rows, dim], got {tuple(table.shape)}")
     dt = _dtype("table", table)
     it = _check_ids(ids, table)
+    rows, dim = table.shape[0], _int32("dim", table.shape[1])
     table, flat = _rows(table), ids.contiguous()
-    rows, dim = table.shape
     out = torch.empty(tuple(ids.shape) + (dim,), dtype=table.dtype, device=table.device)
     _launch(table, L.splat_lookup, table.data_ptr(), dt, rows, dim, table.stride(0), flat.data_ptr(), it, flat.numel(),
             scale, out.data_ptr(), dim)
@@ -116,7 +126,7 @@ def lookup_backward(d_out: torch.Tensor, ids: torch.Tensor, rows: int, scale: fl
     it = _check_ids(ids, d_out)
     if d_out.dim() < 1 or tuple(d_out.shape[:-1]) != tuple(ids.shape):
         raise ValueError(f"d_out: expected {tuple(ids.shape)} + (dim,), got {tuple(d_out.shape)}")
-    dim = d_out.shape[-1]
+    dim = _int32("dim", d_out.shape[-1])
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is None:
@@ -180,8 +190,8 @@ def _norm_desc(x, weight, bias, groups: int, act: str, eps: float) -> L.splat_no
     d = L.splat_norm()
     d.dtype = _dtype("x", x)
     shape = x.shape
-    d.images, d.pixels, d.channels = shape[0], math.prod(shape[1:-1]), shape[-1]
-    d.groups, d.act, d.eps = int(groups), ACTS[act], float(eps)
+    d.images, d.pixels, d.channels = shape[0], math.prod(shape[1:-1]), _int32("channels", shape[-1])
+    d.groups, d.act, d.eps = _int32("groups", groups), ACTS[act], float(eps)
     kind = None
     for name, p in (("weight", weight), ("bias", bias)):
         if p is not None:
@@ -300,7 +310,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coeffs: Sequence[float] = (3.
     dt = _dtype("g", g)
     if len(coeffs) != 3:
         raise ValueError("coeffs: expected three numbers")
-    rows, cols = g.shape[-2:]
+    rows, cols, steps = _int32("rows", g.shape[-2]), _int32("cols", g.shape[-1]), _int32("steps", steps)
     out = _packed_like(g)
     m = g.detach().reshape((-1, rows, cols)) if g.numel() else g.detach().new_empty((0, rows, cols))
     if (cols > 1 and m.stride(2) != 1) or (rows > 1 and m.stride(1) < cols):

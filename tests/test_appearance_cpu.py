@@ -187,3 +187,37 @@ def test_forward_mode_is_refused():
                 call()
         with pytest.raises(ValueError, match="GPU tensor"):   # no tangent: as ever
             A.lookup(t, ids)
+
+
+class _Huge:
+    """A tensor's face alone: sizes past 31 bits without their memory."""
+
+    def __init__(self, *shape, dtype=torch.float16):
+        self.shape, self.dtype, self.is_cuda, self.device = shape, dtype, True, torch.device("cuda:0")
+        self.requires_grad = False
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        n = 1
+        for k in self.shape:
+            n *= k
+        return n
+
+
+def test_sizes_past_31_bits_do_not_wrap():
+    """A size or count that C's int does not hold is refused, not taken modulo 2^32."""
+    from sphere_rasterization_amd import appearance as A
+    big, t = (1 << 32) + 8, torch.zeros(4, 8)
+    ids = _Huge(3, dtype=torch.int64)
+    gpu = _Huge(4, 8)
+    for call in (lambda: A.lookup(_Huge(1, big), ids), lambda: A.lookup_backward(_Huge(3, big), ids, 1),
+                 lambda: A.group_norm(gpu, (1 << 32) + 2), lambda: A.group_norm(gpu, -(1 << 32) + 2),
+                 lambda: A.group_norm(_Huge(2, big), 2), lambda: A.orthogonalize(_Huge(big, 1)),
+                 lambda: A.orthogonalize(_Huge(1, big)), lambda: A.orthogonalize(gpu, steps=(1 << 32) + 5)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    for call in (lambda: A.group_norm(gpu, 2.7), lambda: A.orthogonalize(gpu, steps=2.5)):
+        with pytest.raises(ValueError, match="whole number"):
+            call()
