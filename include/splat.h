@@ -366,8 +366,9 @@ int splat_group_norm_bwd(const splat_norm *norm, const void *d_y, const void *x,
  * A = X X^T; out = scale X, transposed back. Usual coefficients: 3.4445, -4.7750, 2.0315
  * with 5 steps, which bring singular values between about 0.01 and 1 to 0.7 .. 1.2.
  * Products keep 22 bits of each factor and fp32 sums. 1 <= steps <= 64; rows, cols <=
- * 65536; batch <= 65535; eps >= 0. Coefficients under which singular values could grow
- * past 1e4 return SPLAT_ERR_UNSUPPORTED. out may not overlap g.
+ * 65536; batch <= 65535; eps >= 0 (with 0 a matrix of zeros gives 0 / 0, NaN).
+ * Coefficients under which singular values could grow past 1e4 return
+ * SPLAT_ERR_UNSUPPORTED. out may not overlap g.
  * workspace: [splat_orthogonalize_workspace_bytes] device bytes (none for matrices that
  * one workgroup's LDS holds). */
 size_t splat_orthogonalize_workspace_bytes(int64_t batch, int rows, int cols);

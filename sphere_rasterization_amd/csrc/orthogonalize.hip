@@ -86,6 +86,15 @@ __device__ __forceinline__ void write_from_f32(void *p, int64_t i, int dtype, fl
   else ((bf16_t *)p)[i] = (bf16_t)v;
 }
 
+// What brings G to X S: G times pre times inv, inv = s0 / (norm + eps) / pre. The power of
+// two pre keeps inv within fp32 where the norm alone would not (below 1e-34 with eps = 0);
+// it is exact, and one in between.
+__device__ __forceinline__ void unit_scale(double sum_of_squares, float eps, float s0, float &pre, float &inv) {
+  const double d = sqrt(sum_of_squares) + (double)eps;
+  pre = d < 0x1p-64 ? 0x1p64f : d > 0x1p64 ? 0x1p-64f : 1.0f;
+  inv = (float)((double)s0 / d / (double)pre);
+}
+
 // Place of the hi part of value k of row r, for rows of K values; lo lies KB further.
 __device__ __forceinline__ int64_t packed(int r, int k, int K) {
   return ((int64_t)(r >> 6) * (K / KB) + k / KB) * BLOCK + (r & 63) * (2 * KB) + k % KB;
@@ -128,7 +137,8 @@ __global__ __launch_bounds__(OR_THREADS) void k_ortho_pack(OrthoArgs o, int norm
   q = wave_sum_f64(q);
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = q;
   __syncthreads();
-  const float inv = (float)((double)o.s0 / (sqrt((s[0] + s[1]) + (s[2] + s[3])) + (double)o.eps));
+  float pre, inv;
+  unit_scale((s[0] + s[1]) + (s[2] + s[3]), o.eps, o.s0, pre, inv);
   const char *g = (const char *)o.g + mat * o.gb * (o.dtype == SPLAT_F32 ? 4 : 2);
   // direct image: rows of G; cross image: its columns
   _Float16 *direct = (o.tall ? o.y : o.x) + mat * o.sx, *cross = (o.tall ? o.x : o.y) + mat * o.sx;
@@ -137,7 +147,7 @@ __global__ __launch_bounds__(OR_THREADS) void k_ortho_pack(OrthoArgs o, int norm
 #pragma unroll
   for (int k = 0; k < 32; k += 8) {
     const int r = r0 + ty + k, c = c0 + tx;
-    const float v = r < o.rows && c < o.cols ? read_as_f32(g, r * o.gr + c, o.dtype) * inv : 0.0f;
+    const float v = r < o.rows && c < o.cols ? read_as_f32(g, r * o.gr + c, o.dtype) * pre * inv : 0.0f;
     t[ty + k][tx] = v;
     const _Float16 hi = (_Float16)v;
     _Float16 *d = direct + packed(r, c, dlen);
@@ -614,11 +624,12 @@ __global__ __launch_bounds__(SM_THREADS) void k_ortho_small(SmallArgs o) {
   double all = 0.0;
 #pragma unroll
   for (int k = 0; k < SM_WAVES; k++) all += sums[k];
-  const float inv = (float)((double)o.s0 / (sqrt(all) + (double)o.eps));
+  float pre, inv;
+  unit_scale(all, o.eps, o.s0, pre, inv);
   for (int i = tid; i < o.mp * o.np; i += SM_THREADS) {
     const int r = i / o.np, c = i - r * o.np;     // of X
     float v = 0.0f;
-    if (r < o.m && c < o.n) v = read_as_f32(g, o.tall ? c * o.gr + r : r * o.gr + c, o.dtype) * inv;
+    if (r < o.m && c < o.n) v = read_as_f32(g, o.tall ? c * o.gr + r : r * o.gr + c, o.dtype) * pre * inv;
     small_put(x, o.mp, r, c, v);
     small_put(y, o.np, c, r, v);
   }
@@ -733,14 +744,15 @@ __global__ __launch_bounds__(SM_THREADS) void k_ortho_narrow(NarrowArgs o) {
     double all = 0.0;
 #pragma unroll
     for (int k = 0; k < SM_WAVES; k++) all += sums[k];
-    const float inv = (float)((double)o.s0 / (sqrt(all) + (double)o.eps));
+    float pre, inv;
+    unit_scale(all, o.eps, o.s0, pre, inv);
     const char *g = (const char *)o.g + mat * o.gb * (o.dtype == SPLAT_F32 ? 4 : 2);
     const int fast = o.tall ? o.mp : o.ns;         // the axis that memory holds side by side
     for (int i = tid; i < o.mp * o.ns; i += SM_THREADS) {
       const int q = i / fast, f = i - q * fast, r = o.tall ? f : q, c = o.tall ? q : f;
       float v = 0.0f;
       if (r < o.m && j0 + c < o.n)
-        v = read_as_f32(g, o.tall ? (j0 + c) * o.gr + r : r * o.gr + j0 + c, o.dtype) * inv;
+        v = read_as_f32(g, o.tall ? (j0 + c) * o.gr + r : r * o.gr + j0 + c, o.dtype) * pre * inv;
       small_put(x, o.mp, r, c, v);
       small_put(y, o.ns, c, r, v);
     }

@@ -481,6 +481,23 @@ def test_orthogonalize_zero_tiny_huge_and_low_rank(dev):
     assert A.orthogonalize(torch.empty(2, 0, 4, device=dev)).shape == (2, 0, 4)
 
 
+@pytest.mark.parametrize("shape", [(40, 60), (70, 400), (150, 260), (2, 33, 45)])
+def test_orthogonalize_without_eps(dev, shape):
+    """eps = 0, matrices of any size of value (one workgroup, narrow, tiles): the result does
+    not depend on it, down to where fp32 itself runs out."""
+    from sphere_rasterization_amd import appearance as A
+    g = np.random.default_rng(34).standard_normal(shape)
+    for s in (1e-43, 1e-39, 1e-36, 1e-33, 1e-20, 1.0, 1e20, 6e37):
+        t = _put(g * s, "f32", dev)
+        ref = O.orthogonalize(_np(t), eps=0.0)
+        got = A.orthogonalize(t, eps=0.0)
+        for p, q in zip(_np(got).reshape((-1,) + shape[-2:]), ref.reshape((-1,) + shape[-2:])):
+            assert np.linalg.norm(p - q) <= _ortho_tol(q, "f32"), s
+    whole = A.orthogonalize(_put(g, "f32", dev), eps=0.0)     # powers of two: the same bits
+    for k in (-100, -60, 60, 100):
+        assert torch.equal(A.orthogonalize(torch.ldexp(_put(g, "f32", dev), torch.tensor(k, device=dev)), eps=0.0), whole), k
+
+
 # ---- together ------------------------------------------------------------------------------
 
 def test_autograd(dev):
