@@ -498,6 +498,24 @@ def test_orthogonalize_without_eps(dev, shape):
         assert torch.equal(A.orthogonalize(torch.ldexp(_put(g, "f32", dev), torch.tensor(k, device=dev)), eps=0.0), whole), k
 
 
+@pytest.mark.parametrize("shape", [
+    (1, 7), (8, 8), (64, 32), (65, 32), (96, 96), (3, 64, 128),                        # one workgroup, both LDS sizes
+    (128, 96), (257, 70), (40, 700), (64, 1024), (64, 2500), (90, 1500), (1025, 9),               # narrow, 64 and 128 columns a slice
+    (200, 250), (300, 400), (700, 129), (2, 130, 300),                                 # 64 x 64 tiles
+    (130, 2500), (97, 4096),                                                           # and shared out
+    (130, 200, 250), (520, 97, 120), (6, 1024, 1300), (513, 16400)])                   # 128 x 128 tiles, and shared out
+def test_orthogonalize_holds_both_parts(dev, shape):
+    """The error of every form is that of two-part factors, far below one with a part lost."""
+    from tests import ortho_parts as H
+    from sphere_rasterization_amd import appearance as A
+    g = _put(np.random.default_rng(shape[-2] * 7 + shape[-1]).standard_normal(shape), "f32", dev)
+    flat = (-1,) + shape[-2:]
+    got, src = _np(A.orthogonalize(g)).reshape(flat), _np(g).reshape(flat)
+    some = range(len(src)) if len(src) < 8 else (0, 1, len(src) // 2, len(src) - 1)
+    for k in some:
+        assert H.error(got[k], O.orthogonalize(src[k])) <= H.BOUND, k
+
+
 # ---- together ------------------------------------------------------------------------------
 
 def test_autograd(dev):

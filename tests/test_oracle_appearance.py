@@ -61,3 +61,15 @@ def test_orthogonalize_is_the_products(shape):
     # singular values of a full-rank matrix end near one
     sv = np.linalg.svd(A.orthogonalize(rng.standard_normal((6, 6))), compute_uv=False)
     assert sv.max() < 1.3
+
+
+@pytest.mark.parametrize("shape", [(1, 7), (8, 8), (64, 32), (65, 130), (257, 70), (96, 96), (40, 700), (90, 1500), (200, 250)])
+def test_the_bound_tells_both_parts_of_a_factor_from_one(shape):
+    """Two parts per factor stay below the bound; any cross product left out does not."""
+    from tests import ortho_parts as H
+    g = np.random.default_rng(shape[0] * 7 + shape[1]).standard_normal(shape).astype(np.float32)
+    ref = A.orthogonalize(g)
+    assert H.error(H.orthogonalize(g), ref) <= H.BOUND / 4
+    for product in H.PRODUCTS:
+        for lost in (H.CROSS[:1], H.CROSS[1:], H.CROSS):
+            assert H.error(H.orthogonalize(g, {product: lost}), ref) > 2 * H.BOUND, (product, lost)
