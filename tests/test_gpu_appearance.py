@@ -404,6 +404,38 @@ def test_group_norm_strides(dev):
             assert (p - q).abs().max() <= 1e-4 * max(1.0, float(q.abs().max()))
 
 
+def _act_and_slope(dev, z, kind, groups):
+    """The fp32 kernels' activation and slope at exactly z: a weight of zero leaves the bias."""
+    from sphere_rasterization_amd import appearance as A
+    b = torch.from_numpy(z).to(dev)
+    x, w = torch.randn(1, 1, len(z), device=dev), torch.zeros(len(z), device=dev)
+    y, mean, rstd = A.group_norm_forward(x, groups, w, b, 1e-5, kind)
+    db = A.group_norm_backward(torch.ones_like(x), x, mean, rstd, w, b, kind)[2]      # one pixel: db is the slope
+    return _np(y).reshape(-1), _np(db)
+
+
+@pytest.mark.parametrize("groups", [1, 32])                   # three launches; one
+def test_gelu_in_fp32_holds_its_tail(dev, groups):
+    """Roundings counted, in units of U. The exponential: 3 of its argument, each of which
+    moves it by z^2 / 2 of its value, and 2 of its own. The tail beyond 1.25: reciprocal 4,
+    polynomial 3, products 2, fit 0.4, and the exponential's. Within: 4 of F - 1/2 and the
+    half's sum. Then the activation's product, or the slope's."""
+    z = np.concatenate([np.linspace(-9, 9, 65536 - 512), -np.geomspace(1e-8, 12, 256),
+                        np.geomspace(1e-8, 30, 256)]).astype(np.float32)
+    y, slope = _act_and_slope(dev, z, "gelu", groups)
+    import scipy.special as sp
+    zd = z.astype(np.float64)
+    a, tail = np.abs(zd), 0.5 * sp.erfc(np.abs(zd) / np.sqrt(2.0))
+    whole, density = np.where(zd < 0, tail, 1.0 - tail), np.exp(-0.5 * zd * zd) / np.sqrt(2.0 * np.pi)
+    e_exp = 2 + 1.5 * zd * zd
+    e_far = (10 + e_exp) * tail + np.where(zd < 0, 0.0, 1.0)
+    e_int = U * np.where(a < 1.25, 1 + 4 * (0.5 - tail), e_far) * 1.01
+    tiny = 2.0 ** -126 * (1 + a)                              # below fp32's normal range nothing is promised
+    assert (np.abs(y - zd * whole) <= a * e_int + U * a * whole + tiny).all()
+    e_slope = e_int + U * (a * density * (3 + e_exp) + np.abs(whole + zd * density))
+    assert (np.abs(slope - (whole + zd * density)) <= e_slope * 1.01 + tiny).all()
+
+
 # ---- orthogonalize ----------------------------------------------------------------------
 
 def _ortho_tol(ref, dt, steps=5, a=3.4445):
