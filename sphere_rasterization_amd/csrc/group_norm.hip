@@ -94,11 +94,35 @@ __device__ __forceinline__ void normal_f32(float z, float &integral, float &dens
   density = e * 0.39894228f;
 }
 
+// 1 / (1 + exp(-z)) and its complement to fp32: for results of 32 bits. The exponential of
+// -|z| cannot overflow; the rest of its argument's product goes in as a factor, and the
+// reciprocal gets a Newton step. Without either, silu at z = -20 is off by 11 roundings and
+// at -80 by 40. The complement is 1 - s, whose error offsets that of s in the slope, until
+// s is too near one. Forward and backward of 1024x1024x32 fp32: 187 us, 183 without.
+__device__ __forceinline__ void logistic_f32(float z, float &s, float &rest) {
+  constexpr float L = 1.44269502f, L2 = 1.92596303e-08f;                   // log2(e), and what L lacks
+  const float a = fminf(fabsf(z), 150.0f);                                 // the exponential is 0 from 104
+  const float hi = a * -L, lo = __builtin_fmaf(a, -L, -hi) - a * L2, e = __builtin_amdgcn_exp2f(hi);
+  const float t = __builtin_fmaf(e * lo, 0.693147182f, e), x = 1.0f + t;
+  float r = fast_rcp(x);
+  r = __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
+  const float tr = t * r;
+  s = z < 0.0f ? tr : r;
+  rest = z > 2.0f ? tr : 1.0f - s;
+}
+
 // EXACT: for results of 32 bits.
 template <int ACT, bool EXACT>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (ACT == SPLAT_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if constexpr (ACT == SPLAT_ACT_SILU) return z * fast_rcp(1.0f + __expf(-z));
+  if constexpr (ACT == SPLAT_ACT_SILU) {
+    if constexpr (EXACT) {
+      float t, rest;
+      logistic_f32(z, t, rest);
+      return z * t;
+    }
+    return z * fast_rcp(1.0f + __expf(-z));
+  }
   if constexpr (ACT == SPLAT_ACT_GELU) {
     float a, density;
     if constexpr (EXACT) {
@@ -115,6 +139,11 @@ template <int ACT, bool EXACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == SPLAT_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if constexpr (ACT == SPLAT_ACT_SILU) {
+    if constexpr (EXACT) {
+      float t, rest;
+      logistic_f32(z, t, rest);
+      return t * __builtin_fmaf(z, rest, 1.0f);
+    }
     const float t = fast_rcp(1.0f + __expf(-z));
     return t * __builtin_fmaf(z, 1.0f - t, 1.0f);
   }

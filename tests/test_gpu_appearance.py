@@ -436,6 +436,23 @@ def test_gelu_in_fp32_holds_its_tail(dev, groups):
     assert (np.abs(slope - (whole + zd * density)) <= e_slope * 1.01 + tiny).all()
 
 
+@pytest.mark.parametrize("groups", [1, 32])
+def test_silu_in_fp32_holds_its_tail(dev, groups):
+    """At most 8 roundings of the result at any z: exponential 2, its argument's remainder 1,
+    sum 1, reciprocal 2, products 2."""
+    z = np.concatenate([np.linspace(-85, 85, 65536 - 512), -np.geomspace(1e-8, 9, 256),
+                        np.geomspace(1e-8, 9, 256)]).astype(np.float32)
+    y, slope = _act_and_slope(dev, z, "silu", groups)
+    zd = z.astype(np.float64)
+    s, q = 1.0 / (1.0 + np.exp(-zd)), 1.0 / (1.0 + np.exp(zd))
+    assert (np.abs(y - zd * s) <= 8 * U * 1.01 * np.abs(zd * s)).all()
+    assert (np.abs(slope - s * (1 + zd * q)) <= 8 * U * 1.01 * s * (1 + np.abs(zd) * q)).all()
+    ends = np.array([np.inf, 1e30, 200.0, -200.0, -1e30, 0.0, -0.0, 3.0] * 8, np.float32)
+    y, slope = _act_and_slope(dev, ends, "silu", 1)
+    assert np.array_equal(y[:7], [np.inf, np.float32(1e30), 200.0, 0.0, 0.0, 0.0, 0.0])
+    assert np.array_equal(slope[1:7], [1.0, 1.0, 0.0, 0.0, 0.5, 0.5])
+
+
 # ---- orthogonalize ----------------------------------------------------------------------
 
 def _ortho_tol(ref, dt, steps=5, a=3.4445):
