@@ -258,6 +258,16 @@ bool aligned_ids(const void *p, int itype) { return ((uintptr_t)p & (itype == SP
 bool stride_fits(int64_t stride, int64_t count) {
   return count <= 1 || (stride >= 0 && stride <= (int64_t)(1ll << 58) / count);
 }
+// Whether `outer` rows of `inner` pieces of `width` values overlap nowhere: the rows apart,
+// or interleaved. After stride_fits: strides of counts above one are >= 0 and no product
+// overflows.
+bool apart(int64_t outer_stride, int64_t outer, int64_t inner_stride, int64_t inner, int64_t width) {
+  if (inner > 1 && inner_stride < width) return false;
+  if (outer <= 1) return true;
+  if (outer_stride < width) return false;
+  return inner <= 1 || outer_stride >= (inner - 1) * inner_stride + width ||
+         inner_stride >= (outer - 1) * outer_stride + width;
+}
 bool lookup_bwd_size(int64_t n, int64_t rows, int dim) {
   return n >= 0 && n < (1ll << 31) && rows >= 0 && rows < (1ll << 31) - 1 && dim >= 0 && dim <= MAX_DIM;
 }
@@ -595,6 +605,9 @@ int splat_group_norm(const splat_norm *norm, const void *x, const void *weight, 
     CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
     CHECK(ws_bytes >= need, SPLAT_ERR_CAPACITY, "group norm workspace too small");
   }
+  CHECK(norm->pixels == 0 ||
+            apart(norm->y_image_stride, norm->images, norm->y_pixel_stride, norm->pixels, norm->channels),
+        SPLAT_ERR_INVALID_ARG, "output images overlap");
   return launch_group_norm(norm, x, weight, bias, y, mean, rstd, workspace, stream);
 }
 
@@ -615,6 +628,9 @@ int splat_group_norm_bwd(const splat_norm *norm, const void *d_y, const void *x,
             aligned_to(d_weight, norm->param_dtype) && aligned_to(d_bias, norm->param_dtype) &&
             aligned_to(mean, SPLAT_F32) && aligned_to(rstd, SPLAT_F32),
         SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
+  CHECK(!d_x || norm->pixels == 0 ||
+            apart(norm->dx_image_stride, norm->images, norm->dx_pixel_stride, norm->pixels, norm->channels),
+        SPLAT_ERR_INVALID_ARG, "output images overlap");
   return launch_group_norm_bwd(norm, d_y, x, mean, rstd, weight, bias, d_x, d_weight, d_bias, workspace, stream);
 }
 
@@ -639,6 +655,7 @@ int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int c
   CHECK(stride_fits(g_row_stride, rows) && stride_fits(out_row_stride, rows) && stride_fits(g_batch_stride, batch) &&
             stride_fits(out_batch_stride, batch) && g_batch_stride >= 0 && out_batch_stride >= 0,
         SPLAT_ERR_INVALID_ARG, "stride");
+  CHECK(apart(out_batch_stride, batch, out_row_stride, rows, cols), SPLAT_ERR_INVALID_ARG, "output matrices overlap");
   CHECK(aligned_to(g, dtype) && aligned_to(out, dtype), SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
   if (const size_t need = orthogonalize_workspace_bytes(batch, rows, cols)) {
     CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");

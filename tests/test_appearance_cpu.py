@@ -153,6 +153,26 @@ def test_group_norm_of_no_pixels_still_has_statistics_to_write():
         assert f(C.byref(d), None, None, None, None, mean, rstd, None, 0, None) == L.SPLAT_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("ob,orow,code", [
+    (0, 400, -1), (400, 400, -1), (119_999, 400, -1), (120_000, 400, -2), (120_000, 399, -1), (400, 800, -2),
+    (399, 800, -1), (400, 799, -1), (119_600 + 400, 400, -2), (299 * 500 + 400, 500, -2), (299 * 500 + 399, 500, -1)])
+def test_output_matrices_that_overlap_are_refused(ob, orow, code):
+    """Two 300 x 400 results one after the other or interleaved by rows; nothing between. The
+    accepted ones stop at their workspace (-2)."""
+    a = dict(g=P, dtype=0, batch=2, rows=300, cols=400, gb=120000, gr=400, steps=5, a=3.4445, b=-4.775, c=2.0315,
+             eps=1e-7, scale=1.0, out=P, ob=ob, orow=orow, ws=P, nbytes=64)
+    assert L.lib().splat_orthogonalize(*a.values(), None) == code
+
+
+@pytest.mark.parametrize("image,pixel", [((8 << 20) - 1, 8), (8, 8), (8, 15), (9, 16), (0, 8), (1 << 20, 9)])
+def test_output_images_that_overlap_are_refused(image, pixel):
+    """Two images of 2^20 pixels of 8 channels are written apart or interleaved by pixels."""
+    d = _norm(pixels=1 << 20, y_image_stride=image, y_pixel_stride=pixel)
+    assert L.lib().splat_group_norm(C.byref(d), *[P] * 7, 1 << 40, None) == L.SPLAT_ERR_INVALID_ARG
+    d = _norm(pixels=1 << 20, x_image_stride=8 << 20, y_image_stride=8 << 20, dx_image_stride=image, dx_pixel_stride=pixel)
+    assert L.lib().splat_group_norm_bwd(C.byref(d), *[P] * 10, 1 << 40, None) == L.SPLAT_ERR_INVALID_ARG
+
+
 def test_python_refusals_without_a_gpu():
     from sphere_rasterization_amd import appearance as A
     t = torch.zeros(4, 8)

@@ -565,6 +565,23 @@ def test_orthogonalize_holds_both_parts(dev, shape):
         assert H.error(got[k], O.orthogonalize(src[k])) <= H.BOUND, k
 
 
+def test_interleaved_outputs_of_the_c_calls(dev):
+    """Matrices interleaved by rows and images interleaved by pixels do not overlap."""
+    from sphere_rasterization_amd import _lib as L
+    from sphere_rasterization_amd import appearance as A
+    s = torch.cuda.current_stream().cuda_stream
+    g, out = torch.randn(2, 40, 60, device=dev), torch.zeros(40, 2, 60, device=dev)
+    L.splat_orthogonalize(g.data_ptr(), L.SPLAT_F32, 2, 40, 60, 2400, 60, 5, *COEFFS, 1e-7, 1.0, out.data_ptr(), 60, 120,
+                          None, 0, s)
+    assert torch.equal(out.transpose(0, 1), A.orthogonalize(g))
+    x, y, st = torch.randn(3, 50, 8, device=dev), torch.zeros(50, 3, 8, device=dev), torch.zeros(2, 3, 2, device=dev)
+    d = L.splat_norm()
+    d.channels, d.groups, d.eps, d.images, d.pixels = 8, 2, 1e-5, 3, 50
+    d.x_image_stride, d.x_pixel_stride, d.y_image_stride, d.y_pixel_stride = 400, 8, 8, 24
+    L.splat_group_norm(d, x.data_ptr(), None, None, y.data_ptr(), st.data_ptr(), st[1].data_ptr(), None, 0, s)
+    assert torch.equal(y.transpose(0, 1), A.group_norm(x, 2))
+
+
 # ---- together ------------------------------------------------------------------------------
 
 def test_autograd(dev):
