@@ -129,7 +129,8 @@ def lookup_backward(d_out: torch.Tensor, ids: torch.Tensor, rows: int, scale: fl
     dim = _int32("dim", d_out.shape[-1])
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((rows, dim), dtype=d_out.dtype, device=d_out.device)
     else:
         _like("out", out, d_out, (rows, dim), (d_out.dtype,))
@@ -140,6 +141,8 @@ def lookup_backward(d_out: torch.Tensor, ids: torch.Tensor, rows: int, scale: fl
     _keep, ws, nbytes = _workspace(L.splat_lookup_bwd_workspace_bytes(n, rows, dim), d_out)
     _launch(d_out, L.splat_lookup_bwd, dy.data_ptr(), dt, dy.stride(0), flat.data_ptr(), it, n, rows, dim, scale,
             out.data_ptr(), out.stride(0), 1 if accumulate else 0, ws, nbytes)
+    if given:                                # a graph that has saved it has to know
+        torch.autograd.graph.increment_version(out)
     return out
 
 

@@ -225,6 +225,20 @@ def test_lookup_past_32_bits(dev):
     assert int((table != 0).any(dim=1).sum()) == 4
 
 
+def test_lookup_backward_into_a_tensor_is_seen_by_autograd(dev):
+    """A tensor that a graph has saved may not change unnoticed."""
+    from sphere_rasterization_amd import appearance as A
+    dy, ids = torch.ones(3, 8, device=dev), torch.tensor([0, 2, 2], device=dev)
+    out, w = torch.zeros(4, 8, device=dev), torch.ones(4, 8, device=dev, requires_grad=True)
+    loss = (w * out).sum()                                    # saves out
+    A.lookup_backward(dy, ids, 4, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():                              # tensors without versions
+        held = torch.zeros(4, 8, device=dev)
+        assert torch.equal(A.lookup_backward(dy, ids, 4, out=held, accumulate=True), out)
+
+
 # ---- group norm ------------------------------------------------------------------------
 
 DEPTH = 64
