@@ -13,7 +13,7 @@
 // consecutive packs of a pixel, then the next pixel. The writing pass takes the pieces in
 // reverse order, so that it finds in the last-level cache what the pass of sums read
 // last, and its stores pass by that cache (forward and backward of 1024x1024x32 fp32:
-// 202 us without, 185 with; of six 1280x720x24 bf16: 480 and 435).
+// 204 us without, 186 with; of six 1280x720x24 bf16: 454 and 400).
 //
 // The variance is never formed as E[x^2] - mu^2: each batch of NB pixels is centred on
 // its own mean in registers, and (mean, M2) pairs are joined by
@@ -849,10 +849,12 @@ void split(NormArgs &a, int vec, int64_t target, int64_t least) {
   a.items = a.N * a.slices * a.chunks;
 }
 
-// Measured (us for a whole call): 1920x1080x32 fp16 forward at 768, 1024, 2048, 4096
-// workgroups of the statistics 96, 98, 94, 95; six 1280x720x24 bf16 forward and backward at
-// 768, 1024, 2048 of the gradient's sums 480, 526, 498: its registers let three workgroups
-// share a CU, so 768 is one round.
+// Measured (us for a whole call) at 768, 1024, 2048 and 4096 workgroups of the statistics:
+// 1920x1080x32 fp16 forward 79, 81, 83, 83, forward and backward of 1024x1024x32 fp32 184,
+// 184, 186, 186 and of six 1280x720x24 bf16 401, 401, 401, 407 (the first was 96, 98, 94, 95
+// when 2048 was taken, before parameters were loaded under one branch). The last at 768,
+// 1024, 2048 of the gradient's sums 401, 403, 398 (480, 526, 498 when 768 was taken: its
+// registers let three workgroups share a CU, so that is one round).
 constexpr int64_t STAT_BLOCKS = 2048, SUM_BLOCKS = 768, SUM_LEAST = 16;
 constexpr int64_t APPLY_BLOCKS = 4096, APPLY_LEAST = 8;   // passes that write
 

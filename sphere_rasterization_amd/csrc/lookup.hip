@@ -723,7 +723,8 @@ __global__ __launch_bounds__(FW_THREADS) void k_few_grads(SumArgs a, const ID *_
 // Overlapping packs against the widest that divides the row and its alignment, lookup and
 // gradient in us: 1M rows of 33 fp32 29 and 99 (43 and 133), of 31 fp16 19 and 92 (40 and
 // 109), 47337 of 383 fp16 11 and 57 (24 and 92), 20000 of 2723 bf16 25 and 57 (62 and 90),
-// 1M of 20 fp16 11 and 88 (13 and 81).
+// 1M of 36 bf16 18 and 91 (19 and 88). They lose in the gradient of short rows that half a
+// pack divides: 1M of 20 fp16 12 and 88 (12 and 82), of 12 fp16 10 and 88 (10 and 81).
 int pack_width(int bytes, int dim, bool divide) {
   int v = 16 / bytes;
   while (v > dim || (divide && dim % v)) v >>= 1;

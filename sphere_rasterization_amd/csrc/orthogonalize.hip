@@ -876,10 +876,12 @@ int64_t lower_tiles(int len, int tl) { return (int64_t)(len / tl) * (len / tl + 
 
 int round_up(int x, int k) { return (x + k - 1) / k * k; }
 
-// LDS bytes of the one-workgroup form; 0 if the matrix is too large for it. Where it fits
-// it is the faster one, us against 3 launches a step: 32 x 32 12 against 58, 64 x 128 32
-// against 63, 32 x 500 44 against 80, 128 x 96 70 against 72, 300 matrices of 96 x 96 92
-// against 271.
+// LDS bytes of the one-workgroup form; 0 if the matrix is too large for it. It is taken
+// wherever it fits. us in this form, in the narrow one and in 3 launches a step: 32 x 32 13,
+// 29, 59; 32 x 200 24, 32, 68; 64 x 64 22, 37, 59; 64 x 128 32, 39, 63; 64 x 192 42, 41, 66;
+// 96 x 96 44, 58, 70; eight of 64 x 192 42, 43, 69; 300 of 96 x 96 93 and 270 (too many
+// workgroups for the narrow form). The loss is on few rows and a long axis: 32 x 500 45, 31,
+// 78, eight of them 45, 32, 83.
 constexpr int SMALL_LDS = 64 << 10, LARGE_LDS = 160 << 10;
 int small_lds(int rows, int cols) {
   const int64_t m = round_up(rows < cols ? rows : cols, 32), n = round_up(rows < cols ? cols : rows, 32);
