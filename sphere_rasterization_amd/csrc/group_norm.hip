@@ -46,32 +46,48 @@ struct NormArgs {
 // ---- activations ----------------------------------------------------------------
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
-// The normal distribution's tail T(|z|) = erfc(|z| / sqrt 2) / 2 and its density at z, by
-// Abramowitz and Stegun 7.1.26 (absolute error of erf below 1.5e-7): erfc(u) =
-// t P(t) exp(-u^2), t = 1 / (1 + p u), P of degree 4. With u^2 = z^2 / 2 the exponential
-// is the density up to a factor, which goes into the exponent, and its inverse and the
-// tail's half into P: the passes with this activation are bound by these instructions.
-// For results of 16 bits, whose rounding hides the fit's error.
-__device__ __forceinline__ void normal_tail(float z, float &tail, float &density) {
+// The normal distribution's tail T(|z|) = erfc(|z| / sqrt 2) / 2 and its density at z, for
+// 16-bit images: T = t P(t) exp(-z^2 / 2), t = 1 / (1 + p |z|), P of degree 4. The
+// exponential is the density up to a factor, which goes into the exponent, and its inverse
+// into P: the passes with gelu are bound by these instructions.
+__device__ __forceinline__ float normal_density(float z) {
   // log2 of exp(-z^2 / 2) / sqrt(2 pi)
-  density = __builtin_amdgcn_exp2f(__builtin_fmaf(z * -0.72134752f, z, -1.32574806f));
-  const float t = fast_rcp(__builtin_fmaf(0.23164189f, fabsf(z), 1.0f));   // p / sqrt 2
-  constexpr float F = 1.25331414f;                                         // sqrt(2 pi) / 2
-  float p = __builtin_fmaf(1.061405429f * F, t, -1.453152027f * F);
-  p = __builtin_fmaf(p, t, 1.421413741f * F);
-  p = __builtin_fmaf(p, t, -0.284496736f * F);
-  p = __builtin_fmaf(p, t, 0.254829592f * F);
-  tail = p * (t * density);
+  return __builtin_amdgcn_exp2f(__builtin_fmaf(z * -0.72134752f, z, -1.32574806f));
+}
+template <bool SLOPE>
+__device__ __forceinline__ float normal_tail(float z, float density) {
+  if constexpr (SLOPE) {
+    // For gelu's slope, whose sums may be fp32: Abramowitz and Stegun 7.1.26 (absolute error
+    // of erf below 1.5e-7); p and P for erfc(u) at u = |z| / sqrt 2, halved.
+    const float t = fast_rcp(__builtin_fmaf(0.23164189f, fabsf(z), 1.0f));
+    constexpr float F = 1.25331414f;                                       // sqrt(2 pi) / 2
+    float p = __builtin_fmaf(1.061405429f * F, t, -1.453152027f * F);
+    p = __builtin_fmaf(p, t, 1.421413741f * F);
+    p = __builtin_fmaf(p, t, -0.284496736f * F);
+    p = __builtin_fmaf(p, t, 0.254829592f * F);
+    return p * (t * density);
+  } else {
+    // For gelu itself, small where the tail is: a least-maximum fit of the relative error,
+    // 3.7e-5 up to 5.7, where fp16 ends, and 6e-4 up to 14, with an absolute error below
+    // 1.9e-6: at most 0.08 steps of fp16 and 0.03 of bf16, where the fit above is off by 1.3
+    // and 3.7 steps far below zero.
+    const float t = fast_rcp(__builtin_fmaf(0.36f, fabsf(z), 1.0f));
+    float p = __builtin_fmaf(-0.235040769f, t, 0.601457357f);
+    p = __builtin_fmaf(p, t, 0.129469812f);
+    p = __builtin_fmaf(p, t, 0.400783777f);
+    p = __builtin_fmaf(p, t, 0.356639355f);
+    return p * (t * density);
+  }
 }
 
-// The normal distribution's integral F(z) and its density, to fp32: for results of 32 bits.
+// The normal distribution's integral F(z) and its density, to fp32: for fp32 images.
 // F = 1/2 + z R(z^2) up to |z| = 1.25, R of degree 5; beyond, the tail t Q(t) exp(-z^2 / 2),
 // t = 1 / (1 + 0.3 |z|), Q of degree 8. R and Q are least-maximum fits of the relative
 // error of (F - 1/2) / z (9.6e-9) and of exp(z^2 / 2) (1 - F) / t (1.9e-8). Weighted by the
 // normal density, gelu's and its slope's error is 3.7e-8 and 3.9e-8 of them, that of
-// 0.5 z (1 + erf(z / sqrt 2)) in fp32 3.7e-8 and 4.0e-8, and with the short fit above
+// 0.5 z (1 + erf(z / sqrt 2)) in fp32 3.7e-8 and 4.0e-8, and with 7.1.26
 // 8.6e-8 and 1.0e-7; the negative tail, lost to 1 + erf, is kept. Forward and
-// backward of 1024x1024x32 fp32: 189 us, 185 with the short fit.
+// backward of 1024x1024x32 fp32: 189 us, 185 with 7.1.26.
 __device__ __forceinline__ void normal_f32(float z, float &integral, float &density) {
   const float v = z * z, e = __builtin_amdgcn_exp2f(v * -0.72134752f);
   const float t = fast_rcp(__builtin_fmaf(0.3f, fabsf(z), 1.0f));
@@ -111,7 +127,7 @@ __device__ __forceinline__ void logistic_f32(float z, float &s, float &rest) {
   rest = z > 2.0f ? tr : 1.0f - s;
 }
 
-// EXACT: for results of 32 bits.
+// EXACT: for fp32 images.
 template <int ACT, bool EXACT>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (ACT == SPLAT_ACT_RELU) return z < 0.0f ? 0.0f : z;
@@ -124,13 +140,13 @@ __device__ __forceinline__ float act_of(float z) {
     return z * fast_rcp(1.0f + __expf(-z));
   }
   if constexpr (ACT == SPLAT_ACT_GELU) {
-    float a, density;
     if constexpr (EXACT) {
+      float a, density;
       normal_f32(z, a, density);
       return z * a;
     }
-    normal_tail(z, a, density);
-    return z * (z < 0.0f ? a : 1.0f - a);
+    const float tail = normal_tail<false>(z, normal_density(z));
+    return z * (z < 0.0f ? tail : 1.0f - tail);
   }
   return z;
 }
@@ -153,7 +169,8 @@ __device__ __forceinline__ float act_slope(float z) {
       normal_f32(z, a, density);
       return __builtin_fmaf(z, density, a);
     }
-    normal_tail(z, a, density);
+    density = normal_density(z);
+    a = normal_tail<true>(z, density);
     return __builtin_fmaf(z, density, z < 0.0f ? a : 1.0f - a);
   }
   return 1.0f;

@@ -451,6 +451,27 @@ def test_gelu_in_fp32_holds_its_tail(dev, groups):
 
 
 @pytest.mark.parametrize("groups", [1, 32])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_gelu_in_16_bits_is_rounded_once(dev, dt, groups):
+    """Every value of the type from -12 to 12: half a step of the result, and the part before
+    the rounding, for which a tenth of a step is allowed."""
+    from sphere_rasterization_amd import appearance as A
+    import scipy.special as sp
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(DT[dt]).float()
+    v = v[torch.isfinite(v) & (v.abs() <= 12)]
+    v = torch.cat([v, torch.zeros(-len(v) % 32)])
+    b = v.to(DT[dt]).to(dev)
+    x, w = torch.randn(1, 1, len(v), device=dev).to(DT[dt]), torch.zeros(len(v), device=dev, dtype=DT[dt])
+    y = _np(A.group_norm(x, groups, w, b, act="gelu")).reshape(-1)
+    z = v.double().numpy()
+    ref = z * 0.5 * sp.erfc(-z / np.sqrt(2.0))
+    least = {"f16": 2.0 ** -24, "bf16": 2.0 ** -133}[dt]
+    step = np.maximum(2.0 ** (np.floor(np.log2(np.maximum(np.abs(ref), 1e-300)))) * 2 * RO[dt], least)
+    assert (np.abs(y - ref) <= 0.6 * step + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("groups", [1, 32])
 def test_silu_in_fp32_holds_its_tail(dev, groups):
     """At most 8 roundings of the result at any z: exponential 2, its argument's remainder 1,
     sum 1, reciprocal 2, products 2."""
