@@ -377,6 +377,68 @@ int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int c
                         void *out, int64_t out_batch_stride, int64_t out_row_stride, void *workspace,
                         size_t ws_bytes, hipStream_t stream);
 
+/* ---- dense layers ------------------------------------------------------------------
+ * A layer of the shading network in one call, y = residual + drop(act(x W + b)), its
+ * gradient, and dropout on its own. Arrays, strides and workspaces as above.
+ *
+ * HOST struct: dropout with probability p in [0, 1]. Element i of an array [rows][cols],
+ * i = row cols + col, is set to zero where u_i < round(p 2^32) and multiplied by
+ * 1 / (1 - p) elsewhere (all zeros for p = 1). u_i is counter-based, so no mask is stored
+ * and the backward draws the same one: Philox4x32-10 (Salmon et al. 2011) with the key
+ * (seed low, seed high) and the counter (k low, k high + 2^31 h, offset low, offset high),
+ * k = i / 8, gives eight 16-bit pieces, the low half of each word first; u_i is piece i % 8
+ * for h = 0 times 2^16 plus piece i % 8 for h = 1. Calls with the same seed and different
+ * offsets draw different numbers. state: NULL, or two 64-bit words on the DEVICE that
+ * take the place of seed and are added to offset, read when the kernels run: a captured
+ * step that adds to state[1] draws anew on every replay. p = 0 draws nothing. */
+typedef struct {
+  double p;
+  uint64_t seed, offset;
+  const uint64_t *state;
+} splat_drop;
+
+/* y = residual + drop(x) over [rows][cols]; residual may be NULL. For the gradient call
+ * it with d_y in the place of x. rows, cols and their product below 2^62; y may be x or
+ * the residual, and otherwise overlaps neither. */
+int splat_dropout(const splat_drop *drop, int dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride,
+                  const void *residual, int64_t residual_stride, void *y, int64_t y_stride, hipStream_t stream);
+
+/* HOST struct: a dense layer of `in` inputs and `out` outputs over `rows` rows. bias_dtype
+ * (bias and its gradient): SPLAT_F32 or dtype. x [rows][in], residual and y (forward) or
+ * d_y (backward) [rows][out], d_x [rows][in] with row strides; W and d_W are [in][out]
+ * with one of their two strides 1 and the other at least the length of the first's axis.
+ * The strides of the backward's outputs are not looked at in the forward, nor the
+ * residual's in the backward. rows < 2^31, in and out <= 2^20. */
+typedef struct {
+  int32_t dtype, bias_dtype, act, in, out;
+  int64_t rows;
+  int64_t x_stride, w_in_stride, w_out_stride, residual_stride, y_stride;
+  int64_t dx_stride, dw_in_stride, dw_out_stride;
+  splat_drop drop;
+} splat_dense;
+
+/* 1 where the backward is faster with `pre` (large products with an activation), else 0. */
+int splat_linear_saves(const splat_dense *dense);
+
+/* Workspace bytes of splat_linear (backward = 0) or splat_linear_bwd (1); 0 where none is
+ * needed. Any call with these sizes, types and layouts of W and d_W fits, whatever its
+ * other strides and alignment. */
+size_t splat_linear_workspace_bytes(const splat_dense *dense, int backward);
+
+/* y = residual + drop(act(z)), z = x W + b. bias and residual may be NULL. pre: NULL, or
+ * [rows][out] of dtype, packed, which receives z rounded to dtype. Products of 16-bit
+ * values are exact, those of fp32 values rounded to fp32; sums are fp32. y overlaps no input. */
+int splat_linear(const splat_dense *dense, const void *x, const void *w, const void *bias, const void *residual,
+                 void *y, void *pre, void *workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Gradients w.r.t. x, W and b given d_y (overwritten; a NULL output is not computed):
+ * dz = drop'(d_y) act'(z), d_x = dz W^T, d_W = x^T dz, d_b = column sums of dz; the
+ * residual's gradient is d_y itself. pre: what the forward wrote, or NULL: z is then
+ * computed anew from x, W and b. drop has to be the forward's, the state's words too. */
+int splat_linear_bwd(const splat_dense *dense, const void *d_y, const void *x, const void *w, const void *bias,
+                     const void *pre, void *d_x, void *d_w, void *d_bias, void *workspace, size_t ws_bytes,
+                     hipStream_t stream);
+
 const char *splat_status_string(int status);
 
 #ifdef __cplusplus

@@ -29,7 +29,8 @@ EXPORTS = ["splat_projected_bytes", "splat_total_tiles", "splat_sort_workspace_b
            "splat_render_bwd", "splat_interpolate", "splat_interpolate_bwd", "splat_lookup",
            "splat_lookup_bwd_workspace_bytes", "splat_lookup_bwd", "splat_group_norm_workspace_bytes",
            "splat_group_norm", "splat_group_norm_bwd", "splat_orthogonalize_workspace_bytes",
-           "splat_orthogonalize", "splat_status_string"]
+           "splat_orthogonalize", "splat_dropout", "splat_linear_saves", "splat_linear_workspace_bytes",
+           "splat_linear", "splat_linear_bwd", "splat_status_string"]
 
 
 class splat_camera(C.Structure):
@@ -67,6 +68,17 @@ class splat_norm(C.Structure):
                 ("x_image_stride", C.c_int64), ("x_pixel_stride", C.c_int64),
                 ("y_image_stride", C.c_int64), ("y_pixel_stride", C.c_int64),
                 ("dx_image_stride", C.c_int64), ("dx_pixel_stride", C.c_int64)]
+
+
+class splat_drop(C.Structure):
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64), ("state", C.c_void_p)]
+
+
+class splat_dense(C.Structure):
+    _fields_ = ([(k, C.c_int32) for k in ("dtype", "bias_dtype", "act", "inputs", "outputs")]
+                + [(k, C.c_int64) for k in ("rows", "x_stride", "w_in_stride", "w_out_stride", "residual_stride",
+                                            "y_stride", "dx_stride", "dw_in_stride", "dw_out_stride")]
+                + [("drop", splat_drop)])
 
 
 class SplatError(RuntimeError):
@@ -130,6 +142,17 @@ def lib():
         L.splat_orthogonalize.restype = i32
         L.splat_orthogonalize.argtypes = [vp, i32, i64, i32, i32, i64, i64, i32, f32, f32, f32, f32, f32, vp, i64,
                                           i64, vp, sz, vp]
+        drop_p, dense_p = C.POINTER(splat_drop), C.POINTER(splat_dense)
+        L.splat_dropout.restype = i32
+        L.splat_dropout.argtypes = [drop_p, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+        L.splat_linear_saves.restype = i32
+        L.splat_linear_saves.argtypes = [dense_p]
+        L.splat_linear_workspace_bytes.restype = sz
+        L.splat_linear_workspace_bytes.argtypes = [dense_p, i32]
+        L.splat_linear.restype = i32
+        L.splat_linear.argtypes = [dense_p, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.splat_linear_bwd.restype = i32
+        L.splat_linear_bwd.argtypes = [dense_p, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.splat_status_string.restype = C.c_char_p
         L.splat_status_string.argtypes = [i32]
         _L = L
@@ -256,3 +279,26 @@ def splat_orthogonalize(g, dtype, batch, rows, cols, g_batch_stride, g_row_strid
                                                                    g_row_stride, steps, a, b, c, eps, scale, out,
                                                                    out_batch_stride, out_row_stride, workspace,
                                                                    ws_bytes, stream))
+
+
+def splat_dropout(drop, dtype, rows, cols, x, x_stride, residual, residual_stride, y, y_stride, stream):
+    return _check("splat_dropout", lib().splat_dropout(C.byref(drop), dtype, rows, cols, x, x_stride, residual,
+                                                       residual_stride, y, y_stride, stream))
+
+
+def splat_linear_saves(dense):
+    return lib().splat_linear_saves(C.byref(dense)) != 0
+
+
+def splat_linear_workspace_bytes(dense, backward):
+    return lib().splat_linear_workspace_bytes(C.byref(dense), 1 if backward else 0)
+
+
+def splat_linear(dense, x, w, bias, residual, y, pre, workspace, ws_bytes, stream):
+    return _check("splat_linear", lib().splat_linear(C.byref(dense), x, w, bias, residual, y, pre, workspace, ws_bytes,
+                                                     stream))
+
+
+def splat_linear_bwd(dense, d_y, x, w, bias, pre, d_x, d_w, d_bias, workspace, ws_bytes, stream):
+    return _check("splat_linear_bwd", lib().splat_linear_bwd(C.byref(dense), d_y, x, w, bias, pre, d_x, d_w, d_bias,
+                                                             workspace, ws_bytes, stream))

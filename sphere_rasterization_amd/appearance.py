@@ -2,14 +2,18 @@
 
     feat = lookup(table, ids)                          # features of n primitives from one table
     img = autograd.render(rz, feat=feat)               # rendered feature image
-    y = group_norm(h, 8, weight, bias, act="silu")     # inside a channels-last shading network
+    h = linear(img, w, b, act="silu", residual=r,      # a dense layer of a channels-last
+               p=0.1, rng=(seed, step))                # shading network, with dropout
+    y = group_norm(h, 8, weight, bias, act="silu")     # its normalisation
+    y = dropout(y, 0.1, (seed, step), residual=r)
     step = orthogonalize(momentum)                     # update of the network's matrices
 
-`lookup` and `group_norm` carry autograd; `lookup_backward`, `group_norm_forward` and
-`group_norm_backward` are the same kernels without it. Forward-mode derivatives are refused:
+`lookup`, `linear`, `group_norm` and `dropout` carry autograd; `lookup_backward`,
+`linear_forward`, `linear_backward`, `group_norm_forward`, `group_norm_backward` and
+`dropout_backward` are the same kernels without it. Forward-mode derivatives are refused:
 a tensor with a tangent raises NotImplementedError. Every step runs in libsplat's HIP
-kernels (csrc/lookup.hip, csrc/group_norm.hip, csrc/orthogonalize.hip); torch provides
-device memory and the stream. Tensors are float32, float16 or bfloat16 on one GPU, and
+kernels (csrc/lookup.hip, csrc/linear.hip, csrc/dropout.hip, csrc/group_norm.hip,
+csrc/orthogonalize.hip); torch provides device memory and the stream. Tensors are float32, float16 or bfloat16 on one GPU, and
 work is enqueued on that GPU's current stream. Arithmetic is fp32 with one rounding at
 the end, sums run in a fixed order (equal inputs give equal bits), and no call waits for
 the device. Tensors whose last axis is not contiguous, or whose pixels are not evenly
@@ -297,6 +301,229 @@ def group_norm(x: torch.Tensor, groups: int, weight: Optional[torch.Tensor] = No
                                     or (bias is not None and bias.requires_grad)):
         return _GroupNorm.apply(x, groups, weight, bias, eps, act)
     return _group_norm(x, groups, weight, bias, eps, act, False)[0]
+
+
+# ---- dense layers and dropout --------------------------------------------------------
+
+def _word(name: str, v) -> int:
+    k = int(v)
+    if k != v or not 0 <= k < 1 << 64:
+        raise ValueError(f"{name}: expected a whole number from 0 to 2^64 - 1, got {v!r}")
+    return k
+
+
+def _fill_drop(d: L.splat_drop, p: float, rng, ref: torch.Tensor):
+    """Sets d for tensors on ref's device and returns the state to keep (None without one)."""
+    d.p = float(p)
+    if not 0.0 <= d.p <= 1.0:
+        raise ValueError(f"p: expected a number from 0 to 1, got {p!r}")
+    if rng is None:
+        if d.p > 0.0:
+            raise ValueError("rng: dropout needs (seed, offset) or (state, offset)")
+        return None
+    if not isinstance(rng, (tuple, list)) or len(rng) != 2:
+        raise ValueError("rng: expected (seed, offset) or (state, offset)")
+    seed, d.offset = rng[0], _word("offset", rng[1])
+    if not isinstance(seed, torch.Tensor):
+        d.seed = _word("seed", seed)
+        return None
+    _like("state", seed, ref, (2,), (torch.int64,))
+    if seed.stride(0) != 1:
+        raise ValueError("state: expected two neighbouring words")
+    d.state = seed.data_ptr()
+    return seed
+
+
+def _flat_rows(t: torch.Tensor, width: int) -> torch.Tensor:
+    """t [..., width] as [rows, width] with contiguous rows that do not overlap; a copy where
+    the rows are not evenly spaced."""
+    return _rows(t.reshape(-1, width) if width else t.reshape(t.shape[:-1].numel(), 0))
+
+
+def _by_strides(t: torch.Tensor) -> torch.Tensor:
+    """A matrix of which one axis is contiguous and whose rows (or columns) do not overlap."""
+    r, c = t.shape
+    (si, so), one = t.stride(), r <= 1 or c <= 1
+    if not one and ((so == 1 and si >= c) or (si == 1 and so >= r)):
+        return t
+    return t.contiguous()
+
+
+def _dense_desc(x, weight, bias, act: str, p, rng):
+    """(descriptor, state to keep, W as the kernels read it)."""
+    if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[0]:
+        raise ValueError(f"expected x [..., in] and weight [in, out], got {tuple(x.shape)} and {tuple(weight.shape)}")
+    if act not in ACTS:
+        raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
+    d = L.splat_dense()
+    d.inputs, d.outputs = _int32("in", weight.shape[0]), _int32("out", weight.shape[1])
+    d.dtype = _dtype("x", x)
+    _like("weight", weight, x, weight.shape, (x.dtype,))
+    if bias is not None:
+        _like("bias", bias, x, (d.outputs,), (torch.float32, x.dtype))
+    d.bias_dtype = _DTYPES[x.dtype if bias is None else bias.dtype]
+    d.act = ACTS[act]
+    d.rows = math.prod(x.shape[:-1])
+    state = _fill_drop(d.drop, p, rng, x)
+    weight = _by_strides(weight)
+    d.w_in_stride, d.w_out_stride = weight.stride()
+    return d, state, weight
+
+
+def _linear(x, weight, bias, act, residual, p, rng, keep: bool):
+    """y and, where the backward is faster with it and `keep`, z."""
+    d, _state, weight = _dense_desc(x, weight, bias, act, p, rng)
+    shape = tuple(x.shape[:-1]) + (d.outputs,)
+    if residual is not None:
+        _like("residual", residual, x, shape, (x.dtype,))
+        residual = _flat_rows(residual, d.outputs)
+        d.residual_stride = residual.stride(0)
+    x = _flat_rows(x, d.inputs)
+    d.x_stride, d.y_stride = x.stride(0), d.outputs
+    y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    pre = _packed_like(y) if keep and L.splat_linear_saves(d) else None
+    bias = _flat(bias)
+    _keep, ws, nbytes = _workspace(L.splat_linear_workspace_bytes(d, False), x)
+    _launch(x, L.splat_linear, d, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre),
+            ws, nbytes)
+    return y, pre
+
+
+def linear_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+                   residual: Optional[torch.Tensor] = None, p: float = 0.0, rng=None):
+    """(y, pre) of `linear`: pre is x @ weight + bias, rounded to x's type, where the backward
+    is faster when it reads it, and None where it computes it anew."""
+    _no_tangents(x, weight, bias, residual)
+    return _linear(x, weight, bias, act, residual, p, rng, True)
+
+
+def linear_backward(d_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    act: str = "none", pre: Optional[torch.Tensor] = None, p: float = 0.0, rng=None,
+                    want: Sequence[str] = ("x", "weight", "bias")):
+    """(d_x, d_weight, d_bias) given d_y and the forward's inputs; None for what `want` leaves
+    out. The residual's gradient is d_y. pre: what `linear_forward` returned, or None (it is
+    then computed anew). rng has to draw what the forward's drew: a state's words are read
+    again. d_weight is laid out as weight is; d_bias has the type of bias (of x without one)."""
+    _no_tangents(d_y, x, weight, bias, pre)
+    d, _state, weight = _dense_desc(x, weight, bias, act, p, rng)
+    _like("d_y", d_y, x, tuple(x.shape[:-1]) + (d.outputs,), (x.dtype,))
+    if pre is not None:
+        _like("pre", pre, x, d_y.shape, (x.dtype,))
+        pre = _flat(pre)
+    shape = x.shape
+    x, d_y = _flat_rows(x, d.inputs), _flat_rows(d_y, d.outputs)
+    d.x_stride, d.y_stride, d.dx_stride = x.stride(0), d_y.stride(0), d.inputs
+    dx = torch.empty(shape, dtype=x.dtype, device=x.device) if "x" in want else None
+    if d.w_out_stride == 1:
+        dw = torch.empty((d.inputs, d.outputs), dtype=x.dtype, device=x.device)
+    else:
+        dw = torch.empty((d.outputs, d.inputs), dtype=x.dtype, device=x.device).t()
+    d.dw_in_stride, d.dw_out_stride = dw.stride()
+    if "weight" not in want:
+        dw = None
+    db = None
+    if "bias" in want:
+        db = torch.empty(d.outputs, dtype=x.dtype if bias is None else bias.dtype, device=x.device)
+    bias = _flat(bias)
+    _keep, ws, nbytes = _workspace(L.splat_linear_workspace_bytes(d, True), x)
+    _launch(x, L.splat_linear_bwd, d, d_y.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(pre), _ptr(dx),
+            _ptr(dw), _ptr(db), ws, nbytes)
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, act, residual, p, rng):
+        y, pre = _linear(x, weight, bias, act, residual, p, rng, True)
+        state = rng[0] if rng is not None and isinstance(rng[0], torch.Tensor) else None
+        ctx.save_for_backward(x, weight, bias, pre, state)
+        ctx.act, ctx.p, ctx.rng = act, p, None if rng is None else (None if state is not None else rng[0], rng[1])
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y):
+        x, weight, bias, pre, state = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        rng = ctx.rng if state is None else (state, ctx.rng[1])
+        dx = dw = db = None
+        if need[0] or need[1] or need[2]:
+            want = [n for n, k in (("x", need[0]), ("weight", need[1]), ("bias", need[2])) if k]
+            dx, dw, db = linear_backward(d_y, x, weight, bias, ctx.act, pre, ctx.p, rng, want)
+        return dx, dw, db, None, d_y if need[4] else None, None, None
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, p: float = 0.0, rng=None) -> torch.Tensor:
+    """residual + drop(act(x @ weight + bias)) in one pass: x [..., in], weight [in, out] of
+    x's type with either axis contiguous (the transpose of an [out, in] matrix is read in
+    place), bias [out] in float32 or x's type, residual [..., out]. act: none, relu, silu or
+    gelu (with erf). p and rng: as in `dropout`, over the elements of the result in order.
+    Products of 16-bit values are summed in fp32; the result is rounded once. in and out up
+    to 2^20, fewer than 2^31 rows."""
+    _no_tangents(x, weight, bias, residual)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, residual)):
+        return _Linear.apply(x, weight, bias, act, residual, p, rng)
+    return _linear(x, weight, bias, act, residual, p, rng, False)[0]
+
+
+def _dropout(x, p, rng, residual):
+    dt = _dtype("x", x)
+    d = L.splat_drop()
+    _state = _fill_drop(d, p, rng, x)
+    if residual is not None:
+        _like("residual", residual, x, x.shape, (x.dtype,))
+    y = _packed_like(x)
+    cols = x.shape[-1] if x.dim() else 1
+    if x.is_contiguous() and (residual is None or residual.is_contiguous()):
+        rows, cols, xs, rs = 1, x.numel(), 0, 0
+    else:
+        rows = x.numel() // cols if cols else 0
+        x, residual = _flat_rows(x, cols), None if residual is None else _flat_rows(residual, cols)
+        xs, rs = x.stride(0), 0 if residual is None else residual.stride(0)
+    _launch(x, L.splat_dropout, d, dt, rows, cols, x.data_ptr(), xs, _ptr(residual), rs, y.data_ptr(), cols)
+    return y
+
+
+def dropout_backward(d_y: torch.Tensor, p: float, rng) -> torch.Tensor:
+    """Gradient of `dropout` w.r.t. x: the same elements of d_y, multiplied by 1 / (1 - p).
+    The residual's gradient is d_y."""
+    _no_tangents(d_y)
+    return _dropout(d_y, p, rng, None)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, rng, residual):
+        state = rng[0] if rng is not None and isinstance(rng[0], torch.Tensor) else None
+        y = _dropout(x, p, rng, residual)
+        ctx.save_for_backward(state)
+        ctx.p, ctx.rng = p, None if rng is None else (None if state is not None else rng[0], rng[1])
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_y):
+        (state,) = ctx.saved_tensors
+        rng = ctx.rng if state is None else (state, ctx.rng[1])
+        need = ctx.needs_input_grad
+        return (dropout_backward(d_y, ctx.p, rng) if need[0] else None), None, None, d_y if need[3] else None
+
+
+def dropout(x: torch.Tensor, p: float, rng, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """residual + drop(x): each element is set to zero with probability p and multiplied by
+    1 / (1 - p) otherwise. The choice is drawn from Philox4x32-10 by the element's place in x
+    (in order, whatever the strides) and never stored: the backward draws it again.
+
+    rng: (seed, offset), whole numbers from 0 to 2^64 - 1; the same pair draws the same
+    elements, another offset (a number for each step and layer) others. Or (state, offset):
+    an int64 tensor of two words on x's GPU, the seed and a number that is added to offset,
+    read when the kernels run, so that a captured step that adds to state[1] at its end
+    draws anew on every replay. p = 0 leaves every element."""
+    _no_tangents(x, residual)
+    if torch.is_grad_enabled() and (x.requires_grad or (residual is not None and residual.requires_grad)):
+        return _Dropout.apply(x, p, rng, residual)
+    return _dropout(x, p, rng, residual)
 
 
 # ---- orthogonalised updates ----------------------------------------------------------

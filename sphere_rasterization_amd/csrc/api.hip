@@ -43,6 +43,14 @@ int orthogonalize_bounds(int steps, float a, float b, float c);
 int launch_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int cols, int64_t gb, int64_t gr,
                          int steps, float ca, float cb, float cc, float eps, float scale, void *out, int64_t ob,
                          int64_t orow, void *ws, hipStream_t stream);
+int launch_dropout(const splat_drop *drop, int dtype, int64_t rows, int64_t cols, const void *x, int64_t xs,
+                   const void *res, int64_t rs, void *y, int64_t ys, hipStream_t stream);
+bool linear_saves(const splat_dense *d);
+size_t linear_workspace_bytes(const splat_dense *d, bool bwd);
+int launch_linear(const splat_dense *d, const void *x, const void *w, const void *bias, const void *res, void *y,
+                  void *pre, void *ws, hipStream_t stream);
+int launch_linear_bwd(const splat_dense *d, const void *dy, const void *x, const void *w, const void *bias, const void *pre,
+                      void *dx, void *dw, void *db, void *ws, hipStream_t stream);
 
 namespace {
 
@@ -297,6 +305,66 @@ int check_norm(const splat_norm *m, bool bwd, bool writes) {
   if (writes && m->pixels > 0)
     CHECK((m->pixels <= 1 || pix[o] >= m->channels) && (m->images <= 1 || img[o] >= m->channels),
           SPLAT_ERR_INVALID_ARG, "output pixels overlap");
+  return SPLAT_OK;
+}
+
+bool overlap_free_matrix(int64_t in, int64_t out, int64_t si, int64_t so) {
+  if (in <= 1 && out <= 1) return true;
+  if (in <= 1) return so >= 1;
+  if (out <= 1) return si >= 1;
+  return (so == 1 && si >= out) || (si == 1 && so >= in);
+}
+
+int check_drop(const splat_drop *d) {
+  CHECK(d != nullptr, SPLAT_ERR_INVALID_ARG, "drop is NULL");
+  CHECK(d->p >= 0.0 && d->p <= 1.0, SPLAT_ERR_INVALID_ARG, "p must lie in [0, 1]");
+  CHECK(((uintptr_t)d->state & 7u) == 0, SPLAT_ERR_INVALID_ARG, "state not aligned to its words");
+  return SPLAT_OK;
+}
+
+// `dw`: whether the strides of d_W are looked at.
+int check_dense(const splat_dense *m, bool dw) {
+  CHECK(m != nullptr, SPLAT_ERR_INVALID_ARG, "dense is NULL");
+  CHECK(known_dtype(m->dtype), SPLAT_ERR_INVALID_ARG, "dtype");
+  CHECK(m->bias_dtype == SPLAT_F32 || m->bias_dtype == m->dtype, SPLAT_ERR_INVALID_ARG, "bias dtype");
+  CHECK(m->act >= SPLAT_ACT_NONE && m->act <= SPLAT_ACT_GELU, SPLAT_ERR_INVALID_ARG, "act");
+  CHECK(m->rows >= 0 && m->rows < (1ll << 31) && m->in >= 0 && m->in <= (1 << 20) && m->out >= 0 && m->out <= (1 << 20),
+        SPLAT_ERR_INVALID_ARG, "layer size");
+  CHECK(overlap_free_matrix(m->in, m->out, m->w_in_stride, m->w_out_stride) && stride_fits(m->w_in_stride, m->in) &&
+            stride_fits(m->w_out_stride, m->out),
+        SPLAT_ERR_INVALID_ARG, "strides of W");
+  CHECK(!dw || (overlap_free_matrix(m->in, m->out, m->dw_in_stride, m->dw_out_stride) &&
+                stride_fits(m->dw_in_stride, m->in) && stride_fits(m->dw_out_stride, m->out)),
+        SPLAT_ERR_INVALID_ARG, "strides of d_W");
+  return check_drop(&m->drop);
+}
+
+bool row_stride(int64_t stride, int64_t rows, int64_t width) {
+  return rows <= 1 || (stride >= width && stride_fits(stride, rows));
+}
+
+// What a stride of one row or column may hold is not looked at: the kernels get packed ones.
+splat_dense settled(const splat_dense *m) {
+  splat_dense d = *m;
+  if (d.rows <= 1) {
+    d.x_stride = d.dx_stride = d.in;
+    d.residual_stride = d.y_stride = d.out;
+  }
+  auto fix = [&](int64_t &si, int64_t &so) {
+    if (d.in <= 1 && d.out <= 1) si = so = 1;
+    else if (d.in <= 1) si = so == 1 ? d.out : 1;
+    else if (d.out <= 1) so = si == 1 ? d.in : 1;
+  };
+  fix(d.w_in_stride, d.w_out_stride);
+  fix(d.dw_in_stride, d.dw_out_stride);
+  return d;
+}
+
+int check_ws(const void *workspace, size_t ws_bytes, size_t need) {
+  if (need) {
+    CHECK(workspace && aligned16(workspace), SPLAT_ERR_INVALID_ARG, "workspace NULL or not 16-byte aligned");
+    CHECK(ws_bytes >= need, SPLAT_ERR_CAPACITY, "workspace too small");
+  }
   return SPLAT_OK;
 }
 
@@ -663,6 +731,79 @@ int splat_orthogonalize(const void *g, int dtype, int64_t batch, int rows, int c
   }
   return launch_orthogonalize(g, dtype, batch, rows, cols, g_batch_stride, g_row_stride, steps, a, b, c, eps, scale,
                               out, out_batch_stride, out_row_stride, workspace, stream);
+}
+
+int splat_dropout(const splat_drop *drop, int dtype, int64_t rows, int64_t cols, const void *x, int64_t x_stride,
+                  const void *residual, int64_t residual_stride, void *y, int64_t y_stride, hipStream_t stream) {
+  int st = check_drop(drop);
+  if (st) return st;
+  CHECK(known_dtype(dtype), SPLAT_ERR_INVALID_ARG, "dtype");
+  constexpr int64_t most = 1ll << 62;
+  CHECK(rows >= 0 && cols >= 0 && rows < most && cols < most && (rows == 0 || cols <= (most - 1) / rows),
+        SPLAT_ERR_INVALID_ARG, "dropout size");
+  if (rows == 0 || cols == 0) return SPLAT_OK;
+  CHECK(x && y, SPLAT_ERR_INVALID_ARG, "NULL array");
+  CHECK(row_stride(x_stride, rows, cols) && row_stride(y_stride, rows, cols) &&
+            (!residual || row_stride(residual_stride, rows, cols)),
+        SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(aligned_to(x, dtype) && aligned_to(y, dtype) && aligned_to(residual, dtype), SPLAT_ERR_INVALID_ARG,
+        "array not aligned to its element");
+  return launch_dropout(drop, dtype, rows, cols, x, rows == 1 ? cols : x_stride, residual,
+                        rows == 1 || !residual ? cols : residual_stride, y, rows == 1 ? cols : y_stride, stream);
+}
+
+int splat_linear_saves(const splat_dense *dense) {
+  if (check_dense(dense, false) != SPLAT_OK) return 0;
+  const splat_dense d = settled(dense);
+  return linear_saves(&d) ? 1 : 0;
+}
+
+size_t splat_linear_workspace_bytes(const splat_dense *dense, int backward) {
+  if (check_dense(dense, backward != 0) != SPLAT_OK) return 0;
+  const splat_dense d = settled(dense);
+  return linear_workspace_bytes(&d, backward != 0);
+}
+
+int splat_linear(const splat_dense *dense, const void *x, const void *w, const void *bias, const void *residual,
+                 void *y, void *pre, void *workspace, size_t ws_bytes, hipStream_t stream) {
+  int st = check_dense(dense, false);
+  if (st) return st;
+  const splat_dense d = settled(dense);
+  CHECK(row_stride(d.x_stride, d.rows, d.in) && row_stride(d.y_stride, d.rows, d.out) &&
+            (!residual || row_stride(d.residual_stride, d.rows, d.out)),
+        SPLAT_ERR_INVALID_ARG, "row stride");
+  if (d.rows == 0 || d.out == 0) return SPLAT_OK;
+  CHECK(((x && w) || d.in == 0) && y, SPLAT_ERR_INVALID_ARG, "NULL array");
+  CHECK(aligned_to(x, d.dtype) && aligned_to(w, d.dtype) && aligned_to(bias, d.bias_dtype) &&
+            aligned_to(residual, d.dtype) && aligned_to(y, d.dtype) && aligned_to(pre, d.dtype),
+        SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
+  if ((st = check_ws(workspace, ws_bytes, linear_workspace_bytes(&d, false)))) return st;
+  return launch_linear(&d, x, w, bias, residual, y, pre, workspace, stream);
+}
+
+int splat_linear_bwd(const splat_dense *dense, const void *d_y, const void *x, const void *w, const void *bias,
+                     const void *pre, void *d_x, void *d_w, void *d_bias, void *workspace, size_t ws_bytes,
+                     hipStream_t stream) {
+  int st = check_dense(dense, d_w != nullptr);
+  if (st) return st;
+  splat_dense d = settled(dense);
+  if (!d_w) {
+    d.dw_in_stride = d.out;
+    d.dw_out_stride = 1;
+  }
+  CHECK(row_stride(d.x_stride, d.rows, d.in) && row_stride(d.y_stride, d.rows, d.out) &&
+            (!d_x || row_stride(d.dx_stride, d.rows, d.in)),
+        SPLAT_ERR_INVALID_ARG, "row stride");
+  CHECK(aligned_to(d_y, d.dtype) && aligned_to(x, d.dtype) && aligned_to(w, d.dtype) && aligned_to(bias, d.bias_dtype) &&
+            aligned_to(pre, d.dtype) && aligned_to(d_x, d.dtype) && aligned_to(d_w, d.dtype) &&
+            aligned_to(d_bias, d.bias_dtype),
+        SPLAT_ERR_INVALID_ARG, "array not aligned to its element");
+  if (!d_x && !d_w && !d_bias) return SPLAT_OK;
+  if (d.rows > 0 && d.out > 0) {
+    CHECK(d_y && ((x && w) || d.in == 0), SPLAT_ERR_INVALID_ARG, "NULL array");
+    if ((st = check_ws(workspace, ws_bytes, linear_workspace_bytes(&d, true)))) return st;
+  }
+  return launch_linear_bwd(&d, d_y, x, w, bias, pre, d_x, d_w, d_bias, workspace, stream);
 }
 
 const char *splat_status_string(int status) {
