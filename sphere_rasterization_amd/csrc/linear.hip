@@ -4,30 +4,16 @@
 // Every product is C[i][j] = sum over c of Q[i][c] P[j][c] with j the axis along which C is
 // stored: Q and P are x, W, dz or their transposes, read where they lie, whichever of
 // their two axes is contiguous.
-#include "activation.h"
-#include "learn_common.h"
-#include "random.h"
+#include "linear_common.h"
+#include "linear_rows.h"
 
 namespace {
 
-typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bhalf8 __attribute__((ext_vector_type(8)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 typedef short short4v __attribute__((ext_vector_type(4)));
-typedef uint32_t word4 __attribute__((ext_vector_type(4)));
-
-constexpr int LN_THREADS = 256;
 
 // What happens to a value on its way to memory.
 enum { OUT_STORE, OUT_LAYER, OUT_PART };
-
-struct LayerArgs {
-  const void *bias, *res;
-  void *pre;
-  int64_t rs;                    // row stride of the residual; pre is packed
-  int bias_f32, act, draw;
-  DropArgs drop;
-};
 
 struct Operand {
   const void *p;                 // [outer][c] with c contiguous, or [c][outer] (transposed)
@@ -44,119 +30,6 @@ struct ProductArgs {
   float *part;                   // [splits][I][J] sums
   LayerArgs layer;
 };
-
-// ---- the end of a value's way ---------------------------------------------------------
-
-// Elements col .. col + 7 of row `row`; `n` of them exist.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, float (&o)[8]) {
-  constexpr int N = 16 / sizeof(T);
-  if (n == 8) {
-#pragma unroll
-    for (int m = 0; m < 8; m += N) {
-      float t[N];
-      const Raw<T, N> r = *reinterpret_cast<const typename Loose<T, N>::type *>(p + m);
-      to_f32<T, N>(r, t);
-#pragma unroll
-      for (int j = 0; j < N; j++) o[m + j] = t[j];
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++) o[j] = j < n ? (float)p[j] : 0.0f;
-  }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *p, int n, const float (&o)[8]) {
-  constexpr int N = 16 / sizeof(T);
-  if (n == 8) {
-#pragma unroll
-    for (int m = 0; m < 8; m += N) {
-      Pack<T, N> t;
-#pragma unroll
-      for (int j = 0; j < N; j++) t.v[j] = (T)o[m + j];
-      *reinterpret_cast<typename Loose<T, N>::type *>(p + m) = __builtin_bit_cast(Raw<T, N>, t);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-      if (j < n) p[j] = (T)o[j];
-  }
-}
-
-// Which of elements at .. at + 7 are kept, `at` any element.
-__device__ __forceinline__ uint32_t keeps_from(int64_t at, const DropArgs &d, const DropKey &k) {
-  const uint32_t sh = (uint32_t)at & 7;
-  uint32_t bits = drop_keeps((uint64_t)at >> 3, d, k);
-  if (sh) bits = (bits | drop_keeps(((uint64_t)at >> 3) + 1, d, k) << 8) >> sh;
-  return bits;
-}
-
-template <typename T>
-__device__ __forceinline__ void activate(float (&v)[8], int act) {
-  constexpr bool EXACT = sizeof(T) == 4;
-  if (act == SPLAT_ACT_RELU) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = act_of<SPLAT_ACT_RELU, EXACT>(v[j]);
-  } else if (act == SPLAT_ACT_SILU) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = act_of<SPLAT_ACT_SILU, EXACT>(v[j]);
-  } else if (act == SPLAT_ACT_GELU) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = act_of<SPLAT_ACT_GELU, EXACT>(v[j]);
-  }
-}
-
-// d times the slope of the activation at z.
-template <typename T>
-__device__ __forceinline__ void slope_times(float (&d)[8], const float (&z)[8], int act) {
-  constexpr bool EXACT = sizeof(T) == 4;
-  if (act == SPLAT_ACT_RELU) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) d[j] *= act_slope<SPLAT_ACT_RELU, EXACT>(z[j]);
-  } else if (act == SPLAT_ACT_SILU) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) d[j] *= act_slope<SPLAT_ACT_SILU, EXACT>(z[j]);
-  } else if (act == SPLAT_ACT_GELU) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) d[j] *= act_slope<SPLAT_ACT_GELU, EXACT>(z[j]);
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void load_bias(const LayerArgs &l, int64_t col, int n, float (&b)[8]) {
-  if (!l.bias) {
-#pragma unroll
-    for (int j = 0; j < 8; j++) b[j] = 0.0f;
-  } else if (l.bias_f32) {
-    load8<float>((const float *)l.bias + col, n, b);
-  } else {
-    load8<T>((const T *)l.bias + col, n, b);
-  }
-}
-
-// z = v + b to y (and pre) for n columns from col of one row.
-template <typename T>
-__device__ __forceinline__ void finish_layer(const LayerArgs &l, const DropKey &key, T *y, int64_t ys, int64_t J,
-                                             int64_t row, int64_t col, int n, float (&v)[8]) {
-  float b[8];
-  load_bias<T>(l, col, n, b);
-#pragma unroll
-  for (int j = 0; j < 8; j++) v[j] += b[j];
-  if (l.pre) store8<T>((T *)l.pre + row * J + col, n, v);
-  activate<T>(v, l.act);
-  if (l.draw) {
-    const uint32_t keep = keeps_from(row * J + col, l.drop, key);
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] = keep >> j & 1 ? v[j] * l.drop.scale : 0.0f;
-  }
-  if (l.res) {
-    float r[8];
-    load8<T>((const T *)l.res + row * l.rs + col, n, r);
-#pragma unroll
-    for (int j = 0; j < 8; j++) v[j] += r[j];
-  }
-  store8<T>(y + row * ys + col, n, v);
-}
 
 // ---- tiles -------------------------------------------------------------------------------
 
@@ -672,13 +545,18 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
 
 }  // namespace
 
-bool linear_saves(const splat_dense *d) { return d->act != SPLAT_ACT_NONE; }
+bool linear_saves(const splat_dense *d) { return d->act != SPLAT_ACT_NONE && !linear_by_rows(d); }
 
-size_t linear_workspace_bytes(const splat_dense *d, bool bwd) { return plan_of(d, bwd).total; }
+size_t linear_workspace_bytes(const splat_dense *d, bool bwd) {
+  if (d->rows == 0 || d->out == 0) return 0;
+  if (linear_by_rows(d)) return bwd ? linear_rows_workspace_bytes(d) : 0;
+  return plan_of(d, bwd).total;
+}
 
 int launch_linear(const splat_dense *d, const void *x, const void *w, const void *bias, const void *res, void *y,
                   void *pre, void *ws, hipStream_t stream) {
   LayerArgs l = {bias, res, pre, d->residual_stride, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, drop_args(&d->drop)};
+  if (linear_by_rows(d)) return launch_linear_rows(d, x, w, l, y, stream);
   if (d->dtype == SPLAT_F32) return forward<float>(d, x, w, l, y, d->y_stride, (float *)ws, stream);
   if (d->dtype == SPLAT_F16) return forward<f16_t>(d, x, w, l, y, d->y_stride, (float *)ws, stream);
   return forward<bf16_t>(d, x, w, l, y, d->y_stride, (float *)ws, stream);
@@ -686,6 +564,10 @@ int launch_linear(const splat_dense *d, const void *x, const void *w, const void
 
 int launch_linear_bwd(const splat_dense *d, const void *dy, const void *x, const void *w, const void *bias, const void *pre,
                       void *dx, void *dw, void *db, void *ws, hipStream_t stream) {
+  if (linear_by_rows(d) && d->rows > 0 && d->out > 0) {
+    const LayerArgs l = {bias, nullptr, nullptr, 0, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, drop_args(&d->drop)};
+    return launch_linear_rows_bwd(d, dy, x, w, l, dx, dw, db, ws, stream);
+  }
   if (d->dtype == SPLAT_F32) return backward<float>(d, dy, x, w, bias, pre, dx, dw, db, ws, stream);
   if (d->dtype == SPLAT_F16) return backward<f16_t>(d, dy, x, w, bias, pre, dx, dw, db, ws, stream);
   return backward<bf16_t>(d, dy, x, w, bias, pre, dx, dw, db, ws, stream);
