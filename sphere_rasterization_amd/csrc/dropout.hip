@@ -4,7 +4,7 @@
 // Bound by memory: 2 (with a residual 3) accesses an element, beside one Philox draw of ten
 // rounds per eight elements: 20 products of 32 x 32 to 64 bits, which issue at a quarter of
 // the rate, and 20 three-way exclusive ors.
-#include "learn_common.h"
+#include "eight.h"
 #include "random.h"
 
 namespace {
@@ -19,45 +19,21 @@ struct DropoutArgs {
   DropArgs drop;
 };
 
-template <typename T>
-__device__ __forceinline__ float dropped(float x, float r, bool res, bool keep, float scale) {
-  const float v = keep ? x * scale : 0.0f;
-  return res ? v + r : v;
-}
-
-// Packed arrays: a thread takes eight elements at any alignment.
+// Packed arrays: a thread takes eight elements, at any alignment.
 template <typename T, bool RES, bool DRAW>
 __global__ __launch_bounds__(DR_THREADS) void k_dropout(DropoutArgs a) {
-  constexpr int N = 16 / sizeof(T), M = 8 / N;
   const DropKey key = DRAW ? drop_key(a.drop) : DropKey{};
   const int64_t n = a.rows * a.cols;
-  const T *x = (const T *)a.x, *r = (const T *)a.res;
-  T *y = (T *)a.y;
   for (int64_t b = (int64_t)blockIdx.x * DR_THREADS + threadIdx.x; b < a.blocks; b += (int64_t)gridDim.x * DR_THREADS) {
     const int64_t at = b * 8;
-    if (at + 8 <= n) {
-      Raw<T, N> xv[M], rv[M] = {};
+    const int m = n - at < 8 ? (int)(n - at) : 8;
+    float v[8], r[8];
+    load8<T>((const T *)a.x + at, m, v);
+    if constexpr (RES) load8<T>((const T *)a.res + at, m, r);
+    if constexpr (DRAW) drop8<true>(v, at, a.drop, key);
 #pragma unroll
-      for (int m = 0; m < M; m++) xv[m] = *reinterpret_cast<const typename Loose<T, N>::type *>(x + at + m * N);
-      if constexpr (RES) {
-#pragma unroll
-        for (int m = 0; m < M; m++) rv[m] = *reinterpret_cast<const typename Loose<T, N>::type *>(r + at + m * N);
-      }
-      const uint32_t keep = DRAW ? drop_keeps((uint64_t)b, a.drop, key) : 0xFFu;
-#pragma unroll
-      for (int m = 0; m < M; m++) {
-        float f[N], q[N], o[N];
-        to_f32<T, N>(xv[m], f);
-        to_f32<T, N>(rv[m], q);
-#pragma unroll
-        for (int j = 0; j < N; j++) o[j] = dropped<T>(f[j], q[j], RES, keep >> (m * N + j) & 1, a.drop.scale);
-        stream_loose<T, N>(y + at + m * N, o);
-      }
-    } else {
-      const uint32_t keep = DRAW ? drop_keeps((uint64_t)b, a.drop, key) : 0xFFu;
-      for (int j = 0; at + j < n; j++)
-        y[at + j] = (T)dropped<T>((float)x[at + j], RES ? (float)r[at + j] : 0.0f, RES, keep >> j & 1, a.drop.scale);
-    }
+    for (int j = 0; j < 8; j++) v[j] = RES ? v[j] + r[j] : v[j];
+    stream8<T>((T *)a.y + at, m, v);
   }
 }
 
@@ -66,22 +42,28 @@ template <typename T>
 __global__ __launch_bounds__(DR_THREADS) void k_dropout_rows(DropoutArgs a, bool draw) {
   const DropKey key = draw ? drop_key(a.drop) : DropKey{};
   const int64_t n = a.rows * a.cols;
-  const T *x = (const T *)a.x, *r = (const T *)a.res;
-  T *y = (T *)a.y;
   for (int64_t b = (int64_t)blockIdx.x * DR_THREADS + threadIdx.x; b < a.blocks; b += (int64_t)gridDim.x * DR_THREADS) {
     const int64_t at = b * 8;
-    const uint32_t keep = draw ? drop_keeps((uint64_t)b, a.drop, key) : 0xFFu;
-    int64_t row = at / a.cols, col = at - row * a.cols;
+    int64_t row[8], col[8];
+    float v[8];
+    row[0] = at / a.cols;
+    col[0] = at - row[0] * a.cols;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      if (at + j >= n) break;
-      y[row * a.ys + col] = (T)dropped<T>((float)x[row * a.xs + col], r ? (float)r[row * a.rs + col] : 0.0f, r != nullptr,
-                                          keep >> j & 1, a.drop.scale);
-      if (++col == a.cols) {
-        col = 0;
-        row++;
+      if (j > 0) {
+        const bool next = col[j - 1] + 1 == a.cols;
+        row[j] = row[j - 1] + (next ? 1 : 0);
+        col[j] = next ? 0 : col[j - 1] + 1;
       }
+      v[j] = at + j < n ? (float)((const T *)a.x)[row[j] * a.xs + col[j]] : 0.0f;
     }
+    if (draw) drop8<true>(v, at, a.drop, key);
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+      if (at + j < n) {
+        const float r = a.res ? (float)((const T *)a.res)[row[j] * a.rs + col[j]] : 0.0f;
+        ((T *)a.y)[row[j] * a.ys + col[j]] = (T)(a.res ? v[j] + r : v[j]);
+      }
   }
 }
 

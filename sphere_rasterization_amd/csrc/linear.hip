@@ -305,11 +305,7 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
         load8<T>((const T *)a.z + m * a.N + col, n, z);
         slope_times<T>(d, z, a.act);
       }
-      if (a.draw) {
-        const uint32_t keep = keeps_from(m * a.N + col, a.drop, key);
-#pragma unroll
-        for (int j = 0; j < 8; j++) d[j] = keep >> j & 1 ? d[j] * a.drop.scale : 0.0f;
-      }
+      if (a.draw) drop8<false>(d, m * a.N + col, a.drop, key);
       if (a.dz) store8<T>((T *)a.dz + m * a.N + col, n, d);
 #pragma unroll
       for (int j = 0; j < 8; j++) t[j] += d[j];
@@ -556,7 +552,11 @@ size_t linear_workspace_bytes(const splat_dense *d, bool bwd) {
 int launch_linear(const splat_dense *d, const void *x, const void *w, const void *bias, const void *res, void *y,
                   void *pre, void *ws, hipStream_t stream) {
   LayerArgs l = {bias, res, pre, d->residual_stride, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, drop_args(&d->drop)};
-  if (linear_by_rows(d)) return launch_linear_rows(d, x, w, l, y, stream);
+  if (linear_by_rows(d) && !pre) {
+    if (d->dtype == SPLAT_F32) return launch_linear_rows_f32(d, x, w, l, y, stream);
+    if (d->dtype == SPLAT_F16) return launch_linear_rows_f16(d, x, w, l, y, stream);
+    return launch_linear_rows_bf16(d, x, w, l, y, stream);
+  }
   if (d->dtype == SPLAT_F32) return forward<float>(d, x, w, l, y, d->y_stride, (float *)ws, stream);
   if (d->dtype == SPLAT_F16) return forward<f16_t>(d, x, w, l, y, d->y_stride, (float *)ws, stream);
   return forward<bf16_t>(d, x, w, l, y, d->y_stride, (float *)ws, stream);
@@ -566,7 +566,9 @@ int launch_linear_bwd(const splat_dense *d, const void *dy, const void *x, const
                       void *dx, void *dw, void *db, void *ws, hipStream_t stream) {
   if (linear_by_rows(d) && d->rows > 0 && d->out > 0) {
     const LayerArgs l = {bias, nullptr, nullptr, 0, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, drop_args(&d->drop)};
-    return launch_linear_rows_bwd(d, dy, x, w, l, dx, dw, db, ws, stream);
+    if (d->dtype == SPLAT_F32) return launch_linear_rows_bwd_f32(d, dy, x, w, l, dx, dw, db, ws, stream);
+    if (d->dtype == SPLAT_F16) return launch_linear_rows_bwd_f16(d, dy, x, w, l, dx, dw, db, ws, stream);
+    return launch_linear_rows_bwd_bf16(d, dy, x, w, l, dx, dw, db, ws, stream);
   }
   if (d->dtype == SPLAT_F32) return backward<float>(d, dy, x, w, bias, pre, dx, dw, db, ws, stream);
   if (d->dtype == SPLAT_F16) return backward<f16_t>(d, dy, x, w, bias, pre, dx, dw, db, ws, stream);

@@ -1,9 +1,28 @@
-// Layers of at most 64 inputs and outputs (linear_rows.hip).
+// Layers of at most 64 inputs and outputs (linear_rows_kernels.h).
 #pragma once
 #include "linear_common.h"
 
-bool linear_by_rows(const splat_dense *d);
-size_t linear_rows_workspace_bytes(const splat_dense *d);   // of the backward; the forward needs none
-int launch_linear_rows(const splat_dense *d, const void *x, const void *w, const LayerArgs &l, void *y, hipStream_t stream);
-int launch_linear_rows_bwd(const splat_dense *d, const void *dy, const void *x, const void *w, const LayerArgs &l, void *dx,
-                           void *dw, void *db, void *ws, hipStream_t stream);
+// Arrays of fewer than eight elements, which a 16-byte access would pass, go the other way.
+static inline bool linear_by_rows(const splat_dense *d) {
+  return d->in >= 1 && d->in <= 64 && d->out <= 64 && d->rows * (d->in < d->out ? d->in : d->out) >= 8;
+}
+
+// Workgroups of the backward, each with sums of its own: four 16-row waves, up to as many
+// workgroups as the chip holds at once.
+static inline int linear_rows_groups(const splat_dense *d) {
+  const int64_t g = (d->rows + 63) / 64, most = d->in <= 32 && d->out <= 32 ? 1024 : 512;
+  return (int)(g < most ? g : most);
+}
+static inline size_t linear_rows_workspace_bytes(const splat_dense *d) {
+  return ws_align(sizeof(float) * (size_t)linear_rows_groups(d) * (d->in + 1) * d->out);
+}
+
+int launch_linear_rows_f32(const splat_dense *d, const void *x, const void *w, const LayerArgs &l, void *y, hipStream_t stream);
+int launch_linear_rows_bwd_f32(const splat_dense *d, const void *dy, const void *x, const void *w, const LayerArgs &l, void *dx,
+                               void *dw, void *db, void *ws, hipStream_t stream);
+int launch_linear_rows_f16(const splat_dense *d, const void *x, const void *w, const LayerArgs &l, void *y, hipStream_t stream);
+int launch_linear_rows_bwd_f16(const splat_dense *d, const void *dy, const void *x, const void *w, const LayerArgs &l, void *dx,
+                               void *dw, void *db, void *ws, hipStream_t stream);
+int launch_linear_rows_bf16(const splat_dense *d, const void *x, const void *w, const LayerArgs &l, void *y, hipStream_t stream);
+int launch_linear_rows_bwd_bf16(const splat_dense *d, const void *dy, const void *x, const void *w, const LayerArgs &l, void *dx,
+                               void *dw, void *db, void *ws, hipStream_t stream);

@@ -27,13 +27,18 @@ __device__ __forceinline__ DropKey drop_key(const DropArgs &d) {
   return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)offset, (uint32_t)(offset >> 32)};
 }
 
+// a ^ b ^ c in one instruction (the bits of a truth table).
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return __builtin_amdgcn_bitop3_b32(a, b, c, 0x96);
+}
+
 __device__ __forceinline__ uint4 philox(uint32_t x0, uint32_t x1, const DropKey &k) {
   uint32_t x2 = k.o0, x3 = k.o1, k0 = k.k0, k1 = k.k1;
 #pragma unroll
   for (int r = 0; r < 10; r++) {
     const uint64_t a = (uint64_t)x0 * 0xD2511F53u, b = (uint64_t)x2 * 0xCD9E8D57u;
-    x0 = (uint32_t)(b >> 32) ^ x1 ^ k0;
-    x2 = (uint32_t)(a >> 32) ^ x3 ^ k1;
+    x0 = xor3((uint32_t)(b >> 32), x1, k0);
+    x2 = xor3((uint32_t)(a >> 32), x3, k1);
     x1 = (uint32_t)b;
     x3 = (uint32_t)a;
     k0 += 0x9E3779B9u;
@@ -42,31 +47,54 @@ __device__ __forceinline__ uint4 philox(uint32_t x0, uint32_t x1, const DropKey 
   return make_uint4(x0, x1, x2, x3);
 }
 
-// Which of elements 8 block .. 8 block + 7 are kept, as bits. u_i is 16 bits of the draw
-// (block, 0) above the same 16 bits of the draw (block, 1); the second is needed only where
-// the first equals the threshold's, once in 65536 elements: 32 bits of resolution at the
-// price of 16, which is what leaves dropout of 16-bit images bound by memory.
-__device__ __forceinline__ uint32_t drop_keeps(uint64_t block, const DropArgs &d, const DropKey &k) {
-  const uint32_t b0 = (uint32_t)block, b1 = (uint32_t)(block >> 32);
-  const uint4 w4 = philox(b0, b1, k);
-  const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-  uint32_t keep = 0, tie = 0;
+// Which of elements 8 block .. 8 block + 7 are kept, as bits.
+// u_i is 16 bits of that draw above the same 16 bits of the draw (block, 1); the second is
+// needed only where the first equals the threshold's, once in 65536 elements: 32 bits of
+// resolution at the price of 16. The branch is one of the whole wave, so that the compiler
+// cannot trade it for drawing twice.
+__device__ __forceinline__ uint32_t piece_of(const uint4 &w, int j) {
+  const uint32_t v = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+  return j & 1 ? v >> 16 : v & 0xFFFFu;
+}
+__device__ __forceinline__ bool any_tie(const uint4 &w, uint32_t high) {
+  bool tie = false;
 #pragma unroll
-  for (int j = 0; j < 8; j++) {
-    const uint32_t u = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
-    keep |= u > d.high ? 1u << j : 0u;
-    tie |= u == d.high ? 1u << j : 0u;
-  }
-  if (tie) {
-    const uint4 v4 = philox(b0, b1 | 0x80000000u, k);
-    const uint32_t v[4] = {v4.x, v4.y, v4.z, v4.w};
+  for (int j = 0; j < 8; j++) tie |= piece_of(w, j) == high;
+  return __builtin_expect(ballot64(tie) != 0, 0);
+}
+__device__ __forceinline__ uint32_t keep_bits(uint64_t block, const DropArgs &d, const DropKey &k) {
+  const uint4 w = philox((uint32_t)block, (uint32_t)(block >> 32), k);
+  uint32_t keep = 0;
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const uint32_t u = j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xFFFFu;
-      if ((tie >> j & 1) && u >= d.low) keep |= 1u << j;
-    }
+  for (int j = 0; j < 8; j++) keep |= piece_of(w, j) > d.high ? 1u << j : 0u;
+  if (any_tie(w, d.high)) {
+    const uint4 v = philox((uint32_t)block, (uint32_t)(block >> 32) | 0x80000000u, k);
+#pragma unroll
+    for (int j = 0; j < 8; j++) keep |= piece_of(w, j) == d.high && piece_of(v, j) >= d.low ? 1u << j : 0u;
   }
   return keep;
+}
+
+// Dropout of elements at .. at + 7, `at` any element, or (ALIGNED) a multiple of eight.
+template <bool ALIGNED>
+__device__ __forceinline__ void drop8(float (&v)[8], int64_t at, const DropArgs &d, const DropKey &k) {
+  const uint64_t block = (uint64_t)at >> 3;
+  const uint32_t sh = ALIGNED ? 0u : (uint32_t)at & 7;
+  const bool apart = !ALIGNED && ballot64(sh != 0) != 0;
+  if (!apart) {
+    const uint4 w = philox((uint32_t)block, (uint32_t)(block >> 32), k);
+    if (!any_tie(w, d.high)) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] = piece_of(w, j) > d.high ? v[j] * d.scale : 0.0f;
+      return;
+    }
+  }
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (uint32_t t = 0; t < (apart ? 2u : 1u); t++) bits |= keep_bits(block + t, d, k) << (8 * t);
+  bits >>= sh;
+#pragma unroll
+  for (int j = 0; j < 8; j++) v[j] = bits >> j & 1 ? v[j] * d.scale : 0.0f;
 }
 
 static inline DropArgs drop_args(const splat_drop *d) {
