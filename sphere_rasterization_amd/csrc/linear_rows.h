@@ -7,8 +7,7 @@ static inline bool linear_by_rows(const splat_dense *d) {
   return d->in >= 1 && d->in <= 64 && d->out <= 64 && d->rows * (d->in < d->out ? d->in : d->out) >= 8;
 }
 
-// Workgroups of the backward, each with sums of its own: four 16-row waves, up to as many
-// workgroups as the chip holds at once.
+// Workgroups of the backward at most, each with sums of its own.
 static inline int linear_rows_groups(const splat_dense *d) {
   const int64_t g = (d->rows + 63) / 64, most = d->in <= 32 && d->out <= 32 ? 1024 : 512;
   return (int)(g < most ? g : most);

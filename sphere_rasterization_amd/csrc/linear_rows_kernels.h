@@ -102,6 +102,12 @@ __device__ __forceinline__ word4 load_chunk(const T *row, int at, const RowEnd<T
   return v;
 }
 
+// Orders a wave's own LDS accesses: the hardware keeps them in program order.
+__device__ __forceinline__ void wave_lds_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <typename T, int KP, int NP, bool EASY>
 struct Rows {
   static constexpr int E = 16 / sizeof(T);            // values per chunk
@@ -119,7 +125,7 @@ struct Rows {
   // Rows in flight ahead of those at work, in sixteens: a wave waits for its stores too before
   // it sees a load that it issued after them, and with one load ahead it mostly waited.
   static constexpr int SIZE = KP * NP * (int)sizeof(T) / 2;
-  static constexpr int AHEAD = EASY && SIZE <= 2 ? 2 : 1;
+  static constexpr int AHEAD = EASY && SIZE <= 2 && sizeof(T) == 2 ? 2 : 1;
   static constexpr int SUM_BYTES = (KP * 32 * NP * 32 + NP * 32) * 4;
 
   // W in LDS by outputs [out][in] and, where the pointer is given, by inputs; zeros beyond it.
@@ -135,31 +141,35 @@ struct Rows {
   }
 
   // Operands of z: row i of fragment t of 32 outputs p stands for output 32 p + 8 (i / 4) + 4 t + i % 4.
-  static __device__ __forceinline__ void fragments(const T *by_out, word4 (&f)[NP][2][KC]) {
+  static __device__ __forceinline__ void fragments(const T *by_out, word4 (&f)[NP][2][KC], int p) {
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int p = 0; p < NP; p++)
+    for (int t = 0; t < 2; t++)
 #pragma unroll
-      for (int t = 0; t < 2; t++)
+      for (int c = 0; c < KC; c++)
+        f[p][t][c] = *reinterpret_cast<const word4 *>(by_out + (32 * p + 8 * (i >> 2) + 4 * t + (i & 3)) * KW + (c * 4 + g) * E);
+  }
+  static __device__ __forceinline__ void fragments(const T *by_out, word4 (&f)[NP][2][KC]) {
 #pragma unroll
-        for (int c = 0; c < KC; c++)
-          f[p][t][c] = *reinterpret_cast<const word4 *>(by_out + (32 * p + 8 * (i >> 2) + 4 * t + (i & 3)) * KW + (c * 4 + g) * E);
+    for (int p = 0; p < NP; p++) fragments(by_out, f, p);
   }
 
   // Operands of dx, the same with inputs for outputs: eight neighbouring outputs 32 p + 8 g of
   // input row i in DC chunks.
-  static __device__ __forceinline__ void fragments_t(const T *by_in, word4 (&f)[KP][2][NP][DC]) {
+  static __device__ __forceinline__ void fragments_t(const T *by_in, word4 (&f)[KP][2][NP][DC], int q) {
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (int q = 0; q < KP; q++)
+    for (int t = 0; t < 2; t++)
 #pragma unroll
-      for (int t = 0; t < 2; t++)
+      for (int p = 0; p < NP; p++)
 #pragma unroll
-        for (int p = 0; p < NP; p++)
+        for (int c = 0; c < DC; c++)
+          f[q][t][p][c] =
+              *reinterpret_cast<const word4 *>(by_in + (32 * q + 8 * (i >> 2) + 4 * t + (i & 3)) * NW + 32 * p + 8 * g + c * E);
+  }
+  static __device__ __forceinline__ void fragments_t(const T *by_in, word4 (&f)[KP][2][NP][DC]) {
 #pragma unroll
-          for (int c = 0; c < DC; c++)
-            f[q][t][p][c] =
-                *reinterpret_cast<const word4 *>(by_in + (32 * q + 8 * (i >> 2) + 4 * t + (i & 3)) * NW + 32 * p + 8 * g + c * E);
+    for (int q = 0; q < KP; q++) fragments_t(by_in, f, q);
   }
 
   // A lane's row of x: its chunks, from `row` = its first value on.
@@ -202,6 +212,21 @@ struct Rows {
     }
   }
 
+  // Sixteen rows of n values from a tile in LDS to memory, neighbouring lanes on neighbouring
+  // 16 bytes: rows past 64 bytes straight from the products' layout, four lanes to a row, took
+  // 104 us in place of 84 for 2M rows of 64 fp16 outputs. n a multiple of a chunk.
+  template <int SIDE>
+  static __device__ __forceinline__ void store_rows(const char *tile, int pitch, T *p, int64_t stride, int n, int64_t rows) {
+    const int per = n / E;
+#pragma unroll
+    for (int u = 0; u < SIDE * 16 / E / 64; u++) {
+      const int q = (threadIdx.x & 63) + 64 * u, r = q / per, c = q - r * per;
+      if (r < 16 && r < rows)
+        *reinterpret_cast<typename Loose<T, E>::type *>(p + r * stride + c * E) =
+            *reinterpret_cast<const word4 *>(tile + r * pitch + c * 16);
+    }
+  }
+
   // Four rows 4 g .. 4 g + 3 of column col + i of a tile of 16-bit values.
   static __device__ __forceinline__ uint2 turned(const char *tile, int pitch, int col) {
     typedef __attribute__((address_space(3))) short4v *lds4;
@@ -210,12 +235,6 @@ struct Rows {
     return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(short4v *)const_cast<char *>(at)));
   }
 };
-
-// Orders a wave's own LDS accesses: the hardware keeps them in program order.
-__device__ __forceinline__ void wave_lds_order() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_wave_barrier();
-}
 
 // What a lane's place among the outputs needs: how many of its eight exist, and their bias.
 template <typename T, int NP>
@@ -232,12 +251,17 @@ __device__ __forceinline__ void lane_outputs(const RowsArgs &a, int (&n)[NP], fl
 template <typename T, int KP, int NP, int ACT, bool DRAW, bool EASY>
 __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 2 ? 4 : KP * NP < 4 ? 3 : 2) void k_rows(RowsArgs a) {
   typedef Rows<T, KP, NP, EASY> R;
+  // rows of more than 32 outputs leave through LDS
+  constexpr bool BOUNCE = EASY && NP == 2;
+  constexpr int OP = NP * 32 * sizeof(T) + 16;
   __shared__ __attribute__((aligned(16))) T lw[R::BY_OUT];
+  __shared__ __attribute__((aligned(16))) char lo[BOUNCE ? LN_THREADS / WAVE * 16 * OP : 16];
+  char *const ot = lo + (BOUNCE ? (threadIdx.x >> 6) * 16 * OP : 0);
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int64_t step = (int64_t)gridDim.x * (LN_THREADS / WAVE) * 16;
   int64_t base = ((int64_t)blockIdx.x * (LN_THREADS / WAVE) + (threadIdx.x >> 6)) * 16;
   const T *px = (const T *)a.x + (base + i) * a.xs, *pr = (const T *)a.layer.res + (base + i) * a.layer.rs;
-  T *py = (T *)a.y + (base + i) * a.ys;
+  T *py = (T *)a.y + (base + (BOUNCE ? 0 : i)) * a.ys;
   word4 nx[R::AHEAD][R::KC], nr[R::AHEAD][NP][R::DC];
   int64_t ahead = base + i;                      // the row that is loaded next
   const RowEnd<T> ex(a.x, a.M, a.xs, a.K), er(a.layer.res, a.M, a.layer.rs, a.N);
@@ -287,8 +311,14 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 2 ? 4 : KP * NP < 4 ? 3 : 
 #pragma unroll
             for (int j = 0; j < 8; j++) v[j] += q[j];
           }
-          store8<T>(py + 32 * p + 8 * g, EASY ? 8 : n[p], v);
+          if constexpr (BOUNCE) store8<T>(reinterpret_cast<T *>(ot + i * OP) + 32 * p + 8 * g, 8, v);
+          else store8<T>(py + 32 * p + 8 * g, EASY ? 8 : n[p], v);
         }
+      }
+      if constexpr (BOUNCE) {
+        wave_lds_order();
+        R::template store_rows<NP * 32>(ot, OP, py, a.ys, a.N, a.M - base);
+        wave_lds_order();
       }
       py += step * a.ys;
       base += step;
@@ -313,11 +343,13 @@ __device__ __forceinline__ void split8(const float (&d)[8], word4 &hi, word4 &lo
 }
 
 template <typename T, int KP, int NP, int ACT, bool DRAW, bool EASY>
-__global__ __launch_bounds__(LN_THREADS, sizeof(T) == 4 && KP * NP == 4 ? 1 : KP * NP > 1 ? 2 : 3) void k_rows_bwd(RowsArgs a) {
+__global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(RowsArgs a) {
   typedef Rows<T, KP, NP, EASY> R;
   constexpr int WAVES = LN_THREADS / WAVE;
+  // fp32 and 64 x 64: W, 128 registers a lane, stays in LDS, so that two waves fit a SIMD
+  constexpr bool KEEP = sizeof(T) == 4 && KP * NP == 4;
   constexpr int A = R::W_BYTES > R::SUM_BYTES ? R::W_BYTES : R::SUM_BYTES;
-  constexpr int LDS = WAVES * R::WAVE_BYTES > A ? WAVES * R::WAVE_BYTES : A;
+  constexpr int LDS = KEEP ? R::W_BYTES + WAVES * R::WAVE_BYTES : WAVES * R::WAVE_BYTES > A ? WAVES * R::WAVE_BYTES : A;
   __shared__ __attribute__((aligned(16))) char lds[LDS];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, w = threadIdx.x >> 6;
   const int64_t step = (int64_t)gridDim.x * WAVES * 16;
@@ -341,10 +373,12 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 4 && KP * NP == 4 ? 1 : KP
   R::stage_w(a, by_out, by_in);
   __syncthreads();
   word4 f[NP][2][R::KC], ft[KP][2][NP][R::DC];
-  R::fragments(by_out, f);
-  R::fragments_t(by_in, ft);
-  __syncthreads();
-  char *xt = lds + w * R::WAVE_BYTES, *zt = xt + 16 * R::XP, *zt2 = zt + 16 * R::ZP;
+  if constexpr (!KEEP) {
+    R::fragments(by_out, f);
+    R::fragments_t(by_in, ft);
+    __syncthreads();
+  }
+  char *xt = lds + (KEEP ? R::W_BYTES : 0) + w * R::WAVE_BYTES, *zt = xt + 16 * R::XP, *zt2 = zt + 16 * R::ZP;
   float b[NP][8];
   int n[NP];
   lane_outputs<T, NP>(a, n, b);
@@ -382,6 +416,7 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 4 && KP * NP == 4 ? 1 : KP
         R::widen(dy[p], v);
         if (slope) {
           float z[8];
+          if constexpr (KEEP) R::fragments(by_out, f, p);
           R::product(f, x, p, z);
 #pragma unroll
           for (int j = 0; j < 8; j++) z[j] += b[p][j];
@@ -415,6 +450,7 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 4 && KP * NP == 4 ? 1 : KP
 #pragma unroll
         for (int q = 0; q < KP; q++) {
           float4v lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+          if constexpr (KEEP) R::fragments_t(by_in, ft, q);
 #pragma unroll
           for (int p = 0; p < NP; p++) {
 #pragma unroll
@@ -432,7 +468,7 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 4 && KP * NP == 4 ? 1 : KP
           const int col = 32 * q + 8 * g, left = a.K - col;
           if (in && left > 0) {
             const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            store8<T>(po + col, EASY || left > 8 ? 8 : left, v);
+            store8<T>(po + col, EASY && sizeof(T) == 2 || left > 8 ? 8 : left, v);
           }
         }
         po += step * a.dxs;
@@ -544,39 +580,57 @@ __global__ __launch_bounds__(1024) void k_rows_join(const float *part, int group
   }
 }
 
-constexpr int FWD_GROUPS = 2048;
-int fwd_groups(int64_t M) { return (int)((M + 63) / 64 < FWD_GROUPS ? (M + 63) / 64 : FWD_GROUPS); }
+// As many workgroups as the chip holds at once: a wave's share of the rows is then the same
+// for all, and W is staged once for each. (2M rows of 64 to 64 bf16: 100 us, 109 with twice as
+// many.) Asked once for each kernel.
+template <typename K>
+int resident(K kernel) {
+  int per = 0, cus = 0, dev = 0;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, LN_THREADS, 0) != hipSuccess || per < 1) per = 1;
+  if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+      cus < 1)
+    cus = 256;
+  return per * cus;
+}
 
 template <typename T, int KP, int NP, int ACT, bool DRAW, bool EASY>
-void launch_one(const RowsArgs &a, bool bwd, int groups, hipStream_t s) {
-  if (bwd) hipLaunchKernelGGL((k_rows_bwd<T, KP, NP, ACT, DRAW, EASY>), dim3((unsigned)groups), dim3(LN_THREADS), 0, s, a);
-  else hipLaunchKernelGGL((k_rows<T, KP, NP, ACT, DRAW, EASY>), dim3((unsigned)groups), dim3(LN_THREADS), 0, s, a);
+int launch_one(const RowsArgs &a, bool bwd, int most, hipStream_t s) {
+  const int64_t need = (a.M + 63) / 64;              // four waves of 16 rows
+  if (bwd) {
+    static const int fit = resident(k_rows_bwd<T, KP, NP, ACT, DRAW, EASY>);
+    int groups = fit < most ? fit : most;
+    if (need < groups) groups = (int)need;
+    hipLaunchKernelGGL((k_rows_bwd<T, KP, NP, ACT, DRAW, EASY>), dim3((unsigned)groups), dim3(LN_THREADS), 0, s, a);
+    return groups;
+  }
+  static const int fit = resident(k_rows<T, KP, NP, ACT, DRAW, EASY>);
+  const int groups = need < fit ? (int)need : fit;
+  hipLaunchKernelGGL((k_rows<T, KP, NP, ACT, DRAW, EASY>), dim3((unsigned)groups), dim3(LN_THREADS), 0, s, a);
+  return groups;
 }
 template <typename T, int KP, int NP, bool DRAW>
-void by_act(const RowsArgs &a, bool bwd, int groups, hipStream_t s) {
+int by_act(const RowsArgs &a, bool bwd, int most, hipStream_t s) {
   // rows of whole chunks and of whole draws; for others one kernel serves all activations
   const bool easy = a.K % (16 / (int)sizeof(T)) == 0 && a.N % 8 == 0;
-  if (!easy) return launch_one<T, KP, NP, ANY_ACT, DRAW, false>(a, bwd, groups, s);
+  if (!easy) return launch_one<T, KP, NP, ANY_ACT, DRAW, false>(a, bwd, most, s);
   switch (a.layer.act) {
-    case SPLAT_ACT_RELU: return launch_one<T, KP, NP, SPLAT_ACT_RELU, DRAW, true>(a, bwd, groups, s);
-    case SPLAT_ACT_SILU: return launch_one<T, KP, NP, SPLAT_ACT_SILU, DRAW, true>(a, bwd, groups, s);
-    case SPLAT_ACT_GELU: return launch_one<T, KP, NP, SPLAT_ACT_GELU, DRAW, true>(a, bwd, groups, s);
-    default: return launch_one<T, KP, NP, SPLAT_ACT_NONE, DRAW, true>(a, bwd, groups, s);
+    case SPLAT_ACT_RELU: return launch_one<T, KP, NP, SPLAT_ACT_RELU, DRAW, true>(a, bwd, most, s);
+    case SPLAT_ACT_SILU: return launch_one<T, KP, NP, SPLAT_ACT_SILU, DRAW, true>(a, bwd, most, s);
+    case SPLAT_ACT_GELU: return launch_one<T, KP, NP, SPLAT_ACT_GELU, DRAW, true>(a, bwd, most, s);
+    default: return launch_one<T, KP, NP, SPLAT_ACT_NONE, DRAW, true>(a, bwd, most, s);
   }
 }
 template <typename T, int KP, int NP>
-void by_draw(const RowsArgs &a, bool bwd, int groups, hipStream_t s) {
-  if (a.layer.draw) by_act<T, KP, NP, true>(a, bwd, groups, s);
-  else by_act<T, KP, NP, false>(a, bwd, groups, s);
+int by_draw(const RowsArgs &a, bool bwd, int most, hipStream_t s) {
+  return a.layer.draw ? by_act<T, KP, NP, true>(a, bwd, most, s) : by_act<T, KP, NP, false>(a, bwd, most, s);
 }
+// Workgroups launched.
 template <typename T>
-int by_size(const RowsArgs &a, bool bwd, int groups, hipStream_t s) {
-  if (a.K <= 32 && a.N <= 32) by_draw<T, 1, 1>(a, bwd, groups, s);
-  else if (a.K <= 32) by_draw<T, 1, 2>(a, bwd, groups, s);
-  else if (a.N <= 32) by_draw<T, 2, 1>(a, bwd, groups, s);
-  else by_draw<T, 2, 2>(a, bwd, groups, s);
-  SPLAT_LAUNCH_CHECK();
-  return SPLAT_OK;
+int by_size(const RowsArgs &a, bool bwd, int most, hipStream_t s) {
+  if (a.K <= 32 && a.N <= 32) return by_draw<T, 1, 1>(a, bwd, most, s);
+  if (a.K <= 32) return by_draw<T, 1, 2>(a, bwd, most, s);
+  if (a.N <= 32) return by_draw<T, 2, 1>(a, bwd, most, s);
+  return by_draw<T, 2, 2>(a, bwd, most, s);
 }
 
 RowsArgs rows_args(const splat_dense *d, const void *x, const void *w) {
@@ -599,7 +653,9 @@ int run_rows(const splat_dense *d, const void *x, const void *w, const LayerArgs
   RowsArgs a = rows_args(d, x, w);
   a.y = y;
   a.layer = l;
-  return by_size<T>(a, false, fwd_groups(a.M), stream);
+  by_size<T>(a, false, 0, stream);
+  SPLAT_LAUNCH_CHECK();
+  return SPLAT_OK;
 }
 
 template <typename T>
@@ -612,9 +668,9 @@ int run_rows_bwd(const splat_dense *d, const void *dy, const void *x, const void
   a.want_x = dx != nullptr;
   a.want_w = dw || db;
   a.part = (float *)ws;
-  const int groups = linear_rows_groups(d);
-  int st = by_size<T>(a, true, groups, stream);
-  if (st || !a.want_w) return st;
+  const int groups = by_size<T>(a, true, linear_rows_groups(d), stream);
+  SPLAT_LAUNCH_CHECK();
+  if (!a.want_w) return SPLAT_OK;
   hipLaunchKernelGGL(k_rows_join<T>, dim3((unsigned)(((a.K + 1) * a.N + 31) / 32)), dim3(1024), 0, stream, a.part, groups, a.K,
                      a.N, (T *)dw, d->dw_in_stride, d->dw_out_stride, db, (int)(d->bias_dtype == SPLAT_F32));
   SPLAT_LAUNCH_CHECK();
