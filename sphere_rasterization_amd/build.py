@@ -13,7 +13,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsplat.so")
 SOURCES = ["api.hip", "project.hip", "binsort.hip", "render_fwd.hip", "render_bwd.hip", "assemble.hip",
            "lookup.hip", "group_norm.hip", "orthogonalize.hip", "linear.hip",
-           "linear_rows_f32.hip", "linear_rows_f16.hip", "linear_rows_bf16.hip", "dropout.hip"]
+           "linear_rows_f32.hip", "linear_rows_f16.hip", "linear_rows_bf16.hip",
+           "linear_tiles_f32.hip", "linear_tiles_f16.hip", "linear_tiles_bf16.hip", "dropout.hip"]
 # measurement kernels (sustained clock, copy and LDS bandwidth), a library of their own
 PEAKS_LIB = os.path.join(HERE, "libsplat_peaks.so")
 PEAKS_SOURCES = ["peaks.hip"]

@@ -6,271 +6,9 @@
 // their two axes is contiguous.
 #include "linear_common.h"
 #include "linear_rows.h"
+#include "linear_tiles.h"
 
 namespace {
-
-typedef float float16v __attribute__((ext_vector_type(16)));
-typedef short short4v __attribute__((ext_vector_type(4)));
-
-// What happens to a value on its way to memory.
-enum { OUT_STORE, OUT_LAYER, OUT_PART };
-
-struct Operand {
-  const void *p;                 // [outer][c] with c contiguous, or [c][outer] (transposed)
-  int64_t stride;                // elements between rows of that array
-};
-
-struct ProductArgs {
-  Operand q, p;
-  int64_t I, J, K;               // rows and columns of C, length of the summed axis
-  int64_t ti, tj;                // tiles along I and J
-  int64_t steps, per;            // stages of the summed axis, and of one split
-  void *c;
-  int64_t cs;                    // row stride of C
-  float *part;                   // [splits][I][J] sums
-  LayerArgs layer;
-};
-
-// ---- tiles -------------------------------------------------------------------------------
-
-template <typename T>
-struct Cores;
-template <>
-struct Cores<f16_t> {
-  static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, p), __builtin_bit_cast(half8, q), acc, 0, 0, 0);
-  }
-};
-template <>
-struct Cores<bf16_t> {
-  static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bhalf8, p), __builtin_bit_cast(bhalf8, q), acc, 0, 0, 0);
-  }
-};
-template <>
-struct Cores<float> {
-  static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
-    typedef float float4v __attribute__((ext_vector_type(4)));
-    const float4v a = __builtin_bit_cast(float4v, p), b = __builtin_bit_cast(float4v, q);
-#pragma unroll
-    for (int k = 0; k < 4; k++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[k], b[k], acc, 0, 0, 0);
-  }
-};
-
-// One operand's share of a stage: TL of its outer places by 64 bytes of the summed axis
-// (KE values), 16-byte chunks of its contiguous axis. Not transposed: TL rows of four
-// chunks; chunk c of row r lies at c ^ ((r >> 2) & 3), which spreads the 16 rows that a
-// fragment read serves at once over all banks. Transposed: KE rows of TL values; for
-// 16-bit types the 64-byte units of a row are exchanged by the row's low bits, so that the
-// four rows by 64 bytes which half a transposing read serves lie in different banks.
-template <typename T, int TL, bool TR>
-struct Stage {
-  static constexpr int E = 16 / sizeof(T);           // values per chunk
-  static constexpr int KE = 64 / sizeof(T);          // values of the summed axis per stage
-  static constexpr int LOADS = TL / 64;              // chunks per thread
-  static constexpr int CPR = TL / E;                 // chunks per row, transposed
-  static constexpr int BYTES = TL * 64;
-
-  static __device__ __forceinline__ int unit_swap(int c) { return TL >= 128 ? (c & 3) : ((c >> 1) & 1); }
-
-  // Chunk q of the stage, in LDS order: its place along the outer axis and the summed one.
-  static __device__ __forceinline__ void place(int q, int &outer, int &c) {
-    if constexpr (!TR) {
-      outer = q >> 2;
-      c = ((q & 3) ^ ((outer >> 2) & 3)) * E;
-    } else {
-      c = q / CPR;
-      const int slot = q % CPR;
-      if constexpr (sizeof(T) == 2) outer = ((((slot >> 2) ^ unit_swap(c)) << 2) | (slot & 3)) * E;
-      else outer = slot * E;
-    }
-  }
-
-  // The chunk from memory, zeros beyond the array: any alignment.
-  static __device__ __forceinline__ word4 load(const Operand &o, int64_t outer, int64_t c, int64_t R, int64_t K) {
-    word4 v = {0, 0, 0, 0};
-    const int64_t row = TR ? c : outer, at = TR ? outer : c, rows = TR ? K : R, len = TR ? R : K;
-    if (row < rows && at < len) {
-      const T *s = (const T *)o.p + row * o.stride + at;
-      if (at + E <= len) {
-        v = *reinterpret_cast<const typename Loose<T, E>::type *>(s);
-      } else {
-        Pack<T, E> t = __builtin_bit_cast(Pack<T, E>, v);
-#pragma unroll
-        for (int j = 0; j < E; j++)
-          if (at + j < len) t.v[j] = s[j];
-        v = __builtin_bit_cast(word4, t);
-      }
-    }
-    return v;
-  }
-
-  // Fragment of 32 outer places from `at`, block u (32 bytes) of the stage: a lane holds
-  // place lane % 32 and chunk 2 u + lane / 32 of the summed axis.
-  static __device__ __forceinline__ word4 fragment(const char *l, int at, int u) {
-    const int lane = threadIdx.x & 63, r = at + (lane & 31), k = 2 * u + (lane >> 5);
-    if constexpr (!TR) {
-      return *reinterpret_cast<const word4 *>(l + (r * 4 + (k ^ ((r >> 2) & 3))) * 16);
-    } else if constexpr (sizeof(T) == 4) {
-      word4 v;
-#pragma unroll
-      for (int j = 0; j < 4; j++) v[j] = *reinterpret_cast<const uint32_t *>(l + ((k * 4 + j) * TL + r) * 4);
-      return v;
-    } else {
-      // 16 lanes read 4 rows of 16 columns and each gets a column
-      typedef __attribute__((address_space(3))) short4v *lds4;
-      const int j = lane & 15, col = at + (lane & 16) + (j & 3) * 4;        // first of four columns
-      word4 v;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int c = k * 8 + h * 4 + (j >> 2);
-        const int unit = (col >> 5) ^ unit_swap(c);
-        const short4v t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds4)(short4v *)const_cast<char *>(l + (c * TL + unit * 32 + (col & 31)) * 2));
-        const uint2 w = __builtin_bit_cast(uint2, t);
-        v[2 * h] = w.x;
-        v[2 * h + 1] = w.y;
-      }
-      return v;
-    }
-  }
-};
-
-// TI x TJ tile of C by four waves, a quarter each.
-template <typename T, int TI, int TJ, bool QT, bool PT>
-struct Tile {
-  typedef Stage<T, TI, QT> SQ;
-  typedef Stage<T, TJ, PT> SP;
-  static constexpr int FI = TI / 64, FJ = TJ / 64;   // fragments per side of a wave's quarter
-  static constexpr int STAGE = SQ::BYTES + SP::BYTES;
-  static constexpr int PITCH = 36;                   // floats between rows of the epilogue's patch of 32 x 32
-  static constexpr int LDS = 2 * STAGE > 4 * 32 * PITCH * 4 ? 2 * STAGE : 4 * 32 * PITCH * 4;
-
-  static __device__ __forceinline__ void product(const ProductArgs &a, int64_t i0, int64_t j0, int64_t k0, int64_t k1,
-                                                 char *lds, float16v (&acc)[FI][FJ]) {
-    const int tid = threadIdx.x, w = tid >> 6;
-    const int wi = (w & 1) * (TI / 2), wj = (w >> 1) * (TJ / 2);
-#pragma unroll
-    for (int i = 0; i < FI; i++)
-#pragma unroll
-      for (int j = 0; j < FJ; j++)
-#pragma unroll
-        for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
-    word4 rq[SQ::LOADS], rp[SP::LOADS];
-    auto fetch = [&](int64_t k) {
-#pragma unroll
-      for (int n = 0; n < SQ::LOADS; n++) {
-        int o, c;
-        SQ::place(tid + n * LN_THREADS, o, c);
-        rq[n] = SQ::load(a.q, i0 + o, k * SQ::KE + c, a.I, a.K);
-      }
-#pragma unroll
-      for (int n = 0; n < SP::LOADS; n++) {
-        int o, c;
-        SP::place(tid + n * LN_THREADS, o, c);
-        rp[n] = SP::load(a.p, j0 + o, k * SP::KE + c, a.J, a.K);
-      }
-    };
-    auto keep = [&](int slot) {
-      char *l = lds + slot * STAGE;
-#pragma unroll
-      for (int n = 0; n < SQ::LOADS; n++) *reinterpret_cast<word4 *>(l + (tid + n * LN_THREADS) * 16) = rq[n];
-#pragma unroll
-      for (int n = 0; n < SP::LOADS; n++)
-        *reinterpret_cast<word4 *>(l + SQ::BYTES + (tid + n * LN_THREADS) * 16) = rp[n];
-    };
-    if (k0 < k1) {
-      fetch(k0);
-      keep(0);
-    }
-    __syncthreads();
-    int slot = 0;
-    for (int64_t k = k0; k < k1; k++) {
-      if (k + 1 < k1) fetch(k + 1);
-      const char *l = lds + slot * STAGE;
-#pragma unroll
-      for (int u = 0; u < 2; u++) {
-        word4 fq[FI], fp[FJ];
-#pragma unroll
-        for (int i = 0; i < FI; i++) fq[i] = SQ::fragment(l, wi + i * 32, u);
-#pragma unroll
-        for (int j = 0; j < FJ; j++) fp[j] = SP::fragment(l + SQ::BYTES, wj + j * 32, u);
-#pragma unroll
-        for (int i = 0; i < FI; i++)
-#pragma unroll
-          for (int j = 0; j < FJ; j++) Cores<T>::mul(fp[j], fq[i], acc[i][j]);
-      }
-      if (k + 1 < k1) keep(slot ^ 1);
-      __syncthreads();
-      slot ^= 1;
-    }
-  }
-};
-
-// The tile's values, 32 x 32 at a time, through a patch of LDS: eight neighbours of a row
-// per lane.
-template <typename T, int TI, int TJ, bool QT, bool PT, int OUT>
-__global__ __launch_bounds__(LN_THREADS) void k_product(ProductArgs a) {
-  typedef Tile<T, TI, TJ, QT, PT> Tl;
-  __shared__ __attribute__((aligned(16))) char lds[Tl::LDS];
-  const int64_t t = blockIdx.x, i0 = (t / a.tj) * TI, j0 = (t % a.tj) * TJ;
-  const int64_t k0 = blockIdx.y * a.per, k1 = k0 + a.per < a.steps ? k0 + a.per : a.steps;
-  float16v acc[Tl::FI][Tl::FJ];
-  Tl::product(a, i0, j0, k0, k1, lds, acc);
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t wi = i0 + (w & 1) * (TI / 2), wj = j0 + (w >> 1) * (TJ / 2);
-  float *patch = reinterpret_cast<float *>(lds) + w * 32 * Tl::PITCH;
-  DropKey key = {};
-  if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
-#pragma unroll
-  for (int i = 0; i < Tl::FI; i++)
-#pragma unroll
-    for (int j = 0; j < Tl::FJ; j++) {
-      // a lane holds column lane % 32 of Q's places and places 8 e + 4 (lane / 32) .. + 3 of P's
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        *reinterpret_cast<float4 *>(patch + (lane & 31) * Tl::PITCH + 8 * e + 4 * (lane >> 5)) =
-            make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int r = h * 16 + (lane >> 2), c = (lane & 3) * 8;
-        float v[8];
-        const float4 x = *reinterpret_cast<const float4 *>(patch + r * Tl::PITCH + c);
-        const float4 z = *reinterpret_cast<const float4 *>(patch + r * Tl::PITCH + c + 4);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = z.x; v[5] = z.y; v[6] = z.z; v[7] = z.w;
-        const int64_t row = wi + i * 32 + r, col = wj + j * 32 + c;
-        if (row < a.I && col < a.J) {
-          const int n = a.J - col < 8 ? (int)(a.J - col) : 8;
-          if constexpr (OUT == OUT_PART) store8<float>(a.part + ((int64_t)blockIdx.y * a.I + row) * a.J + col, n, v);
-          else if constexpr (OUT == OUT_STORE) store8<T>((T *)a.c + row * a.cs + col, n, v);
-          else finish_layer<T>(a.layer, key, (T *)a.c, a.cs, a.J, row, col, n, v);
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
-    }
-}
-
-// Adds the splits of a product in order; a thread takes eight neighbours of a row.
-template <typename T, int OUT>
-__global__ __launch_bounds__(LN_THREADS) void k_product_join(ProductArgs a, int splits) {
-  const int64_t per = (a.J + 7) / 8, n = per * a.I;
-  DropKey key = {};
-  if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
-  for (int64_t t = (int64_t)blockIdx.x * LN_THREADS + threadIdx.x; t < n; t += (int64_t)gridDim.x * LN_THREADS) {
-    const int64_t row = t / per, col = (t - row * per) * 8;
-    const int w = a.J - col < 8 ? (int)(a.J - col) : 8;
-    float v[8] = {};
-    for (int s = 0; s < splits; s++) {
-      float x[8];
-      load8<float>(a.part + ((int64_t)s * a.I + row) * a.J + col, w, x);
-#pragma unroll
-      for (int j = 0; j < 8; j++) v[j] += x[j];
-    }
-    if constexpr (OUT == OUT_STORE) store8<T>((T *)a.c + row * a.cs + col, w, v);
-    else finish_layer<T>(a.layer, key, (T *)a.c, a.cs, a.J, row, col, w, v);
-  }
-}
 
 // ---- dz and its column sums ------------------------------------------------------------
 
@@ -342,58 +80,9 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_zero(T *c, int64_t I, int
 
 // ---- host ------------------------------------------------------------------------------
 
-constexpr int TILE_SIDE = 64, ENOUGH = 512;            // workgroups that fill the chip twice
-
-struct Split {
-  int64_t ti, tj, steps, per;
-  int splits;
-};
-Split split_of(int64_t I, int64_t J, int64_t K, int ke) {
-  Split s;
-  s.ti = (I + TILE_SIDE - 1) / TILE_SIDE;
-  s.tj = (J + TILE_SIDE - 1) / TILE_SIDE;
-  s.steps = (K + ke - 1) / ke;
-  const int64_t tiles = s.ti * s.tj;
-  int64_t want = tiles < ENOUGH ? ENOUGH / tiles : 1;
-  if (want > s.steps / 8) want = s.steps / 8;          // at least eight stages each
-  if (want < 1) want = 1;
-  s.per = (s.steps + want - 1) / want;
-  if (s.per < 1) s.per = 1;
-  s.splits = (int)((s.steps + s.per - 1) / s.per);
-  if (s.splits < 1) s.splits = 1;
-  return s;
-}
-int ke_of(int dtype) { return dtype == SPLAT_F32 ? 16 : 32; }
-size_t part_bytes(int64_t I, int64_t J, int64_t K, int dtype) {
-  if (I == 0 || J == 0) return 0;
-  const Split s = split_of(I, J, K, ke_of(dtype));
-  return s.splits > 1 ? ws_align(sizeof(float) * (size_t)s.splits * I * J) : 0;
-}
-
 unsigned blocks_for(int64_t items) {
   const int64_t b = (items + LN_THREADS - 1) / LN_THREADS;
   return (unsigned)(b < 1 ? 1 : b < 65536 ? b : 65536);
-}
-
-template <typename T, bool QT, bool PT, int OUT>
-int run_product(ProductArgs a, hipStream_t stream) {
-  const Split s = split_of(a.I, a.J, a.K, ke_of(sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16));
-  a.ti = s.ti;
-  a.tj = s.tj;
-  a.steps = s.steps;
-  a.per = s.per;
-  const dim3 grid((unsigned)(s.ti * s.tj), (unsigned)s.splits);
-  if (s.splits == 1) {
-    hipLaunchKernelGGL((k_product<T, TILE_SIDE, TILE_SIDE, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
-    SPLAT_LAUNCH_CHECK();
-    return SPLAT_OK;
-  }
-  hipLaunchKernelGGL((k_product<T, TILE_SIDE, TILE_SIDE, QT, PT, OUT_PART>), grid, dim3(LN_THREADS), 0, stream, a);
-  SPLAT_LAUNCH_CHECK();
-  hipLaunchKernelGGL((k_product_join<T, OUT>), dim3(blocks_for(a.I * ((a.J + 7) / 8))), dim3(LN_THREADS), 0, stream, a,
-                     s.splits);
-  SPLAT_LAUNCH_CHECK();
-  return SPLAT_OK;
 }
 
 int64_t slope_chunks(int64_t M, int64_t N) {
@@ -414,15 +103,15 @@ Plan plan_of(const splat_dense *d, bool bwd) {
   const int64_t M = d->rows, N = d->out, K = d->in;
   if (M == 0 || N == 0) return p;
   auto most = [&](size_t v) { if (v > p.part) p.part = v; };
-  most(part_bytes(M, N, K, d->dtype));
+  most(product_part_bytes(M, N, K, d->dtype));
   if (bwd) {
     const size_t e = dtype_bytes(d->dtype);
     if (d->act != SPLAT_ACT_NONE) p.pre = ws_align((size_t)M * N * e);
     if (d->act != SPLAT_ACT_NONE || d->drop.p > 0.0) p.dz = ws_align((size_t)M * N * e);
     p.sums = ws_align(sizeof(float) * (size_t)slope_chunks(M, N) * N);
-    most(part_bytes(M, K, N, d->dtype));
-    most(part_bytes(K, N, M, d->dtype));
-    most(part_bytes(N, K, M, d->dtype));
+    most(product_part_bytes(M, K, N, d->dtype));
+    most(product_part_bytes(K, N, M, d->dtype));
+    most(product_part_bytes(N, K, M, d->dtype));
   }
   p.total = p.pre + p.dz + p.sums + p.part;
   return p;
@@ -442,10 +131,10 @@ int forward(const splat_dense *d, const void *x, const void *w, const LayerArgs 
   a.layer = l;
   if (w_by_out(d->w_in_stride, d->w_out_stride)) {
     a.p = {w, d->w_in_stride};
-    return run_product<T, false, true, OUT_LAYER>(a, stream);
+    return launch_product<T>(a, false, true, OUT_LAYER, stream);
   }
   a.p = {w, d->w_out_stride};
-  return run_product<T, false, false, OUT_LAYER>(a, stream);
+  return launch_product<T>(a, false, false, OUT_LAYER, stream);
 }
 
 template <typename T>
@@ -516,10 +205,10 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     a.part = part;
     if (w_by_out(d->w_in_stride, d->w_out_stride)) {
       a.p = {w, d->w_in_stride};
-      st = run_product<T, false, false, OUT_STORE>(a, stream);
+      st = launch_product<T>(a, false, false, OUT_STORE, stream);
     } else {
       a.p = {w, d->w_out_stride};
-      st = run_product<T, false, true, OUT_STORE>(a, stream);
+      st = launch_product<T>(a, false, true, OUT_STORE, stream);
     }
     if (st) return st;
   }
@@ -534,12 +223,47 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     a.c = dw;
     a.cs = dws;
     a.part = part;
-    return run_product<T, true, true, OUT_STORE>(a, stream);
+    return launch_product<T>(a, true, true, OUT_STORE, stream);
   }
   return SPLAT_OK;
 }
 
 }  // namespace
+
+// The cheapest of the tiles and splits by what a stage (64 bytes of the summed axis of every
+// tile at work) was measured to take, in us: with one workgroup on a CU, and with as many as
+// fit. Splits cost the writing and reading of their sums and a launch.
+Cut product_cut(int64_t I, int64_t J, int64_t K, int dtype) {
+  struct Rate {
+    int fit;
+    double one, all, rest;       // rest: of a tile outside its stages
+  };
+  static constexpr Rate RATES[2][3] = {{{1, 0.99, 0.99, 8.0}, {2, 0.42, 0.64, 5.0}, {3, 0.30, 0.55, 4.0}},
+                                       {{1, 4.40, 4.40, 8.0}, {2, 1.10, 1.95, 5.0}, {3, 0.60, 1.50, 4.0}}};
+  constexpr int CUS = 256;
+  const int f32 = dtype == SPLAT_F32;
+  const int64_t stages = (K + (f32 ? 16 : 32) - 1) / (f32 ? 16 : 32);
+  Cut best = {2, 1};
+  double least = 1e30;
+  for (int t = 0; t < 3; t++) {
+    const Rate &r = RATES[f32][t];
+    const int64_t tiles = ((I + TILES[t].i - 1) / TILES[t].i) * ((J + TILES[t].j - 1) / TILES[t].j);
+    for (int s = 1; s <= 1024; s = s < 4 ? s + 1 : s + s / 2) {
+      if (s > 1 && stages / s < 8) break;
+      const int64_t groups = tiles * s, round = (int64_t)CUS * r.fit, full = groups / round, left = groups - full * round;
+      const int64_t per = (left + CUS - 1) / CUS;    // of a CU in the last round
+      const double last = per == 0 ? 0.0 : per == 1 ? r.one : r.one + (r.all - r.one) * (double)(per - 1) / (r.fit - 1);
+      double us = ((double)full * r.all + last) * (double)((stages + s - 1) / s) + r.rest;
+      if (s > 1) us += 6.0 + 8e-6 / 4.5 * (double)s * (double)I * (double)J;
+      if (us < least) {
+        least = us;
+        best = {t, s};
+      }
+      if (groups > 4 * round) break;
+    }
+  }
+  return best;
+}
 
 bool linear_saves(const splat_dense *d) { return d->act != SPLAT_ACT_NONE && !linear_by_rows(d); }
 

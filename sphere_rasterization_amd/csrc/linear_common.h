@@ -58,22 +58,43 @@ __device__ __forceinline__ void load_bias(const LayerArgs &l, int64_t col, int n
   }
 }
 
+// The residual's eight values from col of one row, as they lie.
+template <typename T>
+__device__ __forceinline__ void load_res(const LayerArgs &l, int64_t row, int64_t col, int n, word4 (&r)[sizeof(T) / 2]) {
+  constexpr int N = 16 / sizeof(T);
+  if (!l.res) return;
+  const T *p = (const T *)l.res + row * l.rs + col;
+  if (n == 8) {
+#pragma unroll
+    for (int m = 0; m < (int)sizeof(T) / 2; m++) r[m] = *reinterpret_cast<const typename Loose<T, N>::type *>(p + m * N);
+  } else {
+    Pack<T, 8> t;
+#pragma unroll
+    for (int j = 0; j < 8; j++) t.v[j] = j < n ? p[j] : (T)0.0f;
+    const Pack<word4, sizeof(T) / 2> q = __builtin_bit_cast(Pack<word4, sizeof(T) / 2>, t);
+#pragma unroll
+    for (int m = 0; m < (int)sizeof(T) / 2; m++) r[m] = q.v[m];
+  }
+}
+
 // z = v + b to y (and pre) for n columns from col of one row.
 template <typename T>
 __device__ __forceinline__ void finish_layer(const LayerArgs &l, const DropKey &key, T *y, int64_t ys, int64_t J,
-                                             int64_t row, int64_t col, int n, float (&v)[8]) {
-  float b[8];
-  load_bias<T>(l, col, n, b);
+                                             int64_t row, int64_t col, int n, const float (&b)[8],
+                                             const word4 (&res)[sizeof(T) / 2], float (&v)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; j++) v[j] += b[j];
   if (l.pre) store8<T>((T *)l.pre + row * J + col, n, v);
   activate<T>(v, l.act);
   if (l.draw) drop8<false>(v, row * J + col, l.drop, key);
   if (l.res) {
-    float r[8];
-    load8<T>((const T *)l.res + row * l.rs + col, n, r);
+    constexpr int N = 16 / sizeof(T);
 #pragma unroll
-    for (int j = 0; j < 8; j++) v[j] += r[j];
+    for (int m = 0; m < (int)sizeof(T) / 2; m++) {
+      const Pack<T, N> r = __builtin_bit_cast(Pack<T, N>, res[m]);
+#pragma unroll
+      for (int j = 0; j < N; j++) v[m * N + j] += (float)r.v[j];
+    }
   }
   store8<T>(y + row * ys + col, n, v);
 }

@@ -1,0 +1,53 @@
+// Products C[i][j] = sum over c of Q[i][c] P[j][c], with j the axis along which C is stored, and
+// what is done to C on its way to memory (linear_tiles_kernels.h, a file for each type).
+#pragma once
+#include "linear_common.h"
+
+// What happens to C: stored, or one layer's bias, activation, dropout and residual first.
+enum { OUT_STORE, OUT_LAYER };
+
+struct Operand {
+  const void *p;                 // [outer][c] with c contiguous, or [c][outer] (transposed)
+  int64_t stride;                // elements between rows of that array
+};
+
+struct ProductArgs {
+  Operand q, p;
+  int64_t I, J, K;               // rows and columns of C, length of the summed axis
+  int64_t ti, tj;                // tiles along I and J
+  int64_t steps, per;            // stages of the summed axis, and of one split
+  void *c;
+  int64_t cs;                    // row stride of C
+  float *part;                   // [splits][I][J] sums where the summed axis is split, else unused
+  int splits;
+  LayerArgs layer;
+};
+
+// How a product is cut: the tile, and pieces of the summed axis that are added by a second
+// launch where tiles alone do not fill the chip.
+struct Cut {
+  int tile;                      // index of the tile's shape
+  int splits;
+};
+struct TileShape {
+  int i, j;
+};
+constexpr TileShape TILES[3] = {{256, 256}, {128, 128}, {64, 128}};
+constexpr int LOOSE_SIDE = 64;   // of arrays that are not whole, aligned chunks
+Cut product_cut(int64_t I, int64_t J, int64_t K, int dtype);
+static inline size_t product_part_bytes(int64_t I, int64_t J, int64_t K, int dtype) {
+  if (I == 0 || J == 0) return 0;
+  const int n = product_cut(I, J, K, dtype).splits;
+  return n > 1 ? ws_align(sizeof(float) * (size_t)n * I * J) : 0;
+}
+
+// qt, pt: whether Q and P lie transposed; not Q alone.
+int launch_product_f32(const ProductArgs &a, bool qt, bool pt, int out, hipStream_t stream);
+int launch_product_f16(const ProductArgs &a, bool qt, bool pt, int out, hipStream_t stream);
+int launch_product_bf16(const ProductArgs &a, bool qt, bool pt, int out, hipStream_t stream);
+template <typename T>
+static inline int launch_product(const ProductArgs &a, bool qt, bool pt, int out, hipStream_t stream) {
+  if constexpr (sizeof(T) == 4) return launch_product_f32(a, qt, pt, out, stream);
+  else if constexpr (__is_same(T, f16_t)) return launch_product_f16(a, qt, pt, out, stream);
+  else return launch_product_bf16(a, qt, pt, out, stream);
+}

@@ -1,0 +1,534 @@
+// Products of any size: tiles on the matrix cores. See linear.hip for which products there are.
+#pragma once
+#include "linear_tiles.h"
+
+namespace {
+
+typedef float float16v __attribute__((ext_vector_type(16)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+
+// What lanes read in the place of chunks beyond an array.
+__device__ const uint4 zero_chunk = {0, 0, 0, 0};
+
+// ---- tiles -------------------------------------------------------------------------------
+
+template <typename T>
+struct Cores;
+template <>
+struct Cores<f16_t> {
+  static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, p), __builtin_bit_cast(half8, q), acc, 0, 0, 0);
+  }
+};
+template <>
+struct Cores<bf16_t> {
+  static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bhalf8, p), __builtin_bit_cast(bhalf8, q), acc, 0, 0, 0);
+  }
+};
+template <>
+struct Cores<float> {
+  static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
+    typedef float float4v __attribute__((ext_vector_type(4)));
+    const float4v a = __builtin_bit_cast(float4v, p), b = __builtin_bit_cast(float4v, q);
+#pragma unroll
+    for (int k = 0; k < 4; k++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[k], b[k], acc, 0, 0, 0);
+  }
+};
+
+// Eight neighbours of a row of C on their way to memory: to the split's sums, or to C.
+template <typename T, int OUT>
+__device__ __forceinline__ void emit8(const ProductArgs &a, const DropKey &key, int64_t row, int64_t col, int n,
+                                      const float (&bias)[8], const word4 (&res)[sizeof(T) / 2], float (&v)[8]) {
+  if (a.splits > 1) store8<float>(a.part + ((int64_t)blockIdx.y * a.I + row) * a.J + col, n, v);
+  else if constexpr (OUT == OUT_STORE) store8<T>((T *)a.c + row * a.cs + col, n, v);
+  else finish_layer<T>(a.layer, key, (T *)a.c, a.cs, a.J, row, col, n, bias, res, v);
+}
+
+// One operand's share of a stage: TL of its outer places by 64 bytes of the summed axis
+// (KE values), 16-byte chunks of its contiguous axis. Not transposed: TL rows of four
+// chunks; chunk c of row r lies at c ^ ((r >> 2) & 3), which spreads the 16 rows that a
+// fragment read serves at once over all banks. Transposed: KE rows of TL values; for
+// 16-bit types the 64-byte units of a row are exchanged by the row's low bits, so that the
+// four rows by 64 bytes which half a transposing read serves lie in different banks.
+template <typename T, int TL, bool TR>
+struct Stage {
+  static constexpr int E = 16 / sizeof(T);           // values per chunk
+  static constexpr int KE = 64 / sizeof(T);          // values of the summed axis per stage
+  static constexpr int LOADS = TL / 64;              // chunks per thread
+  static constexpr int CPR = TL / E;                 // chunks per row, transposed
+  static constexpr int BYTES = TL * 64;
+
+  static __device__ __forceinline__ int unit_swap(int c) { return TL >= 128 ? (c & 3) : ((c >> 1) & 1); }
+
+  // Chunk q of the stage, in LDS order: its place along the outer axis and the summed one.
+  static __device__ __forceinline__ void place(int q, int &outer, int &c) {
+    if constexpr (!TR) {
+      outer = q >> 2;
+      c = ((q & 3) ^ ((outer >> 2) & 3)) * E;
+    } else {
+      c = q / CPR;
+      const int slot = q % CPR;
+      if constexpr (sizeof(T) == 2) outer = ((((slot >> 2) ^ unit_swap(c)) << 2) | (slot & 3)) * E;
+      else outer = slot * E;
+    }
+  }
+
+  // The chunk from memory, zeros beyond the array: any alignment.
+  static __device__ __forceinline__ word4 load(const Operand &o, int64_t outer, int64_t c, int64_t R, int64_t K) {
+    word4 v = {0, 0, 0, 0};
+    const int64_t row = TR ? c : outer, at = TR ? outer : c, rows = TR ? K : R, len = TR ? R : K;
+    if (row < rows && at < len) {
+      const T *s = (const T *)o.p + row * o.stride + at;
+      if (at + E <= len) {
+        v = *reinterpret_cast<const typename Loose<T, E>::type *>(s);
+      } else {
+        Pack<T, E> t = __builtin_bit_cast(Pack<T, E>, v);
+#pragma unroll
+        for (int j = 0; j < E; j++)
+          if (at + j < len) t.v[j] = s[j];
+        v = __builtin_bit_cast(word4, t);
+      }
+    }
+    return v;
+  }
+
+  // Fragment of 32 outer places from `at`, block u (32 bytes) of the stage: a lane holds
+  // place lane % 32 and chunk 2 u + lane / 32 of the summed axis.
+  static __device__ __forceinline__ word4 fragment(const char *l, int at, int u) {
+    const int lane = threadIdx.x & 63, r = at + (lane & 31), k = 2 * u + (lane >> 5);
+    if constexpr (!TR) {
+      return *reinterpret_cast<const word4 *>(l + (r * 4 + (k ^ ((r >> 2) & 3))) * 16);
+    } else if constexpr (sizeof(T) == 4) {
+      word4 v;
+#pragma unroll
+      for (int j = 0; j < 4; j++) v[j] = *reinterpret_cast<const uint32_t *>(l + ((k * 4 + j) * TL + r) * 4);
+      return v;
+    } else {
+      // 16 lanes read 4 rows of 16 columns and each gets a column
+      typedef __attribute__((address_space(3))) short4v *lds4;
+      const int j = lane & 15, col = at + (lane & 16) + (j & 3) * 4;        // first of four columns
+      word4 v;
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int c = k * 8 + h * 4 + (j >> 2);
+        const int unit = (col >> 5) ^ unit_swap(c);
+        const short4v t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4)(short4v *)const_cast<char *>(l + (c * TL + unit * 32 + (col & 31)) * 2));
+        const uint2 w = __builtin_bit_cast(uint2, t);
+        v[2 * h] = w.x;
+        v[2 * h + 1] = w.y;
+      }
+      return v;
+    }
+  }
+};
+
+// TI x TJ tile of C by four waves, a quarter each.
+template <typename T, int TI, int TJ, bool QT, bool PT>
+struct Tile {
+  typedef Stage<T, TI, QT> SQ;
+  typedef Stage<T, TJ, PT> SP;
+  static constexpr int FI = TI / 64, FJ = TJ / 64;   // fragments per side of a wave's quarter
+  static constexpr int STAGE = SQ::BYTES + SP::BYTES;
+  static constexpr int PITCH = 36;                   // floats between rows of the epilogue's patch of 32 x 32
+  static constexpr int LDS = 2 * STAGE > 4 * 32 * PITCH * 4 ? 2 * STAGE : 4 * 32 * PITCH * 4;
+
+  static __device__ __forceinline__ void product(const ProductArgs &a, int64_t i0, int64_t j0, int64_t k0, int64_t k1,
+                                                 char *lds, float16v (&acc)[FI][FJ]) {
+    const int tid = threadIdx.x, w = tid >> 6;
+    const int wi = (w & 1) * (TI / 2), wj = (w >> 1) * (TJ / 2);
+#pragma unroll
+    for (int i = 0; i < FI; i++)
+#pragma unroll
+      for (int j = 0; j < FJ; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+    word4 rq[SQ::LOADS], rp[SP::LOADS];
+    auto fetch = [&](int64_t k) {
+#pragma unroll
+      for (int n = 0; n < SQ::LOADS; n++) {
+        int o, c;
+        SQ::place(tid + n * LN_THREADS, o, c);
+        rq[n] = SQ::load(a.q, i0 + o, k * SQ::KE + c, a.I, a.K);
+      }
+#pragma unroll
+      for (int n = 0; n < SP::LOADS; n++) {
+        int o, c;
+        SP::place(tid + n * LN_THREADS, o, c);
+        rp[n] = SP::load(a.p, j0 + o, k * SP::KE + c, a.J, a.K);
+      }
+    };
+    auto keep = [&](int slot) {
+      char *l = lds + slot * STAGE;
+#pragma unroll
+      for (int n = 0; n < SQ::LOADS; n++) *reinterpret_cast<word4 *>(l + (tid + n * LN_THREADS) * 16) = rq[n];
+#pragma unroll
+      for (int n = 0; n < SP::LOADS; n++)
+        *reinterpret_cast<word4 *>(l + SQ::BYTES + (tid + n * LN_THREADS) * 16) = rp[n];
+    };
+    if (k0 < k1) {
+      fetch(k0);
+      keep(0);
+    }
+    __syncthreads();
+    int slot = 0;
+    for (int64_t k = k0; k < k1; k++) {
+      if (k + 1 < k1) fetch(k + 1);
+      const char *l = lds + slot * STAGE;
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        word4 fq[FI], fp[FJ];
+#pragma unroll
+        for (int i = 0; i < FI; i++) fq[i] = SQ::fragment(l, wi + i * 32, u);
+#pragma unroll
+        for (int j = 0; j < FJ; j++) fp[j] = SP::fragment(l + SQ::BYTES, wj + j * 32, u);
+#pragma unroll
+        for (int i = 0; i < FI; i++)
+#pragma unroll
+          for (int j = 0; j < FJ; j++) Cores<T>::mul(fp[j], fq[i], acc[i][j]);
+      }
+      if (k + 1 < k1) keep(slot ^ 1);
+      __syncthreads();
+      slot ^= 1;
+    }
+  }
+};
+
+// The tile's values, 32 x 32 at a time, through a patch of LDS: eight neighbours of a row
+// per lane.
+template <typename T, int TI, int TJ, bool QT, bool PT, int OUT>
+__global__ __launch_bounds__(LN_THREADS) void k_product(ProductArgs a) {
+  typedef Tile<T, TI, TJ, QT, PT> Tl;
+  __shared__ __attribute__((aligned(16))) char lds[Tl::LDS];
+  const int64_t t = blockIdx.x, i0 = (t / a.tj) * TI, j0 = (t % a.tj) * TJ;
+  const int64_t k0 = blockIdx.y * a.per, k1 = k0 + a.per < a.steps ? k0 + a.per : a.steps;
+  float16v acc[Tl::FI][Tl::FJ];
+  Tl::product(a, i0, j0, k0, k1, lds, acc);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t wi = i0 + (w & 1) * (TI / 2), wj = j0 + (w >> 1) * (TJ / 2);
+  float *patch = reinterpret_cast<float *>(lds) + w * 32 * Tl::PITCH;
+  DropKey key = {};
+  if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
+#pragma unroll
+  for (int i = 0; i < Tl::FI; i++)
+#pragma unroll
+    for (int j = 0; j < Tl::FJ; j++) {
+      // a lane holds column lane % 32 of Q's places and places 8 e + 4 (lane / 32) .. + 3 of P's
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        *reinterpret_cast<float4 *>(patch + (lane & 31) * Tl::PITCH + 8 * e + 4 * (lane >> 5)) =
+            make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const int r = h * 16 + (lane >> 2), c = (lane & 3) * 8;
+        float v[8];
+        load8<float>(patch + r * Tl::PITCH + c, 8, v);
+        const int64_t row = wi + i * 32 + r, col = wj + j * 32 + c;
+        if (row < a.I && col < a.J) {
+          const int n = a.J - col < 8 ? (int)(a.J - col) : 8;
+          float bias[8];
+          word4 res[sizeof(T) / 2];
+          if constexpr (OUT == OUT_LAYER) {
+            load_bias<T>(a.layer, col, n, bias);
+            load_res<T>(a.layer, row, col, n, res);
+          }
+          emit8<T, OUT>(a, key, row, col, n, bias, res, v);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The same product for arrays whose rows are whole, aligned chunks: loads go straight to LDS.
+// WI x WJ waves share a TI x TJ tile; NST stages form a ring in LDS. In step k, after the wait
+// for stage k + 1 and a barrier, stage k (already in registers) is free for stage k + NST, the
+// fragments of stage k + 1 are read, and those of stage k are multiplied: loads have NST - 1
+// steps to arrive, and fragment reads a step.
+// 16 bytes from each lane's address to consecutive places of LDS from `at`, uniform. Written out,
+// because the compiler waits for every load that it knows to be on its way to LDS before it
+// reads LDS by the transposing instruction, which would leave one stage in flight (8192 x 4096
+// by 4096 x 4096 bf16: 359 us).
+__device__ __forceinline__ void to_lds(const void *p, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
+}
+
+template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT>
+struct Direct {
+  typedef Stage<T, TI, QT> SQ;
+  typedef Stage<T, TJ, PT> SP;
+  static constexpr int THREADS = WI * WJ * WAVE;
+  static constexpr int FI = TI / WI / 32, FJ = TJ / WJ / 32;
+  static constexpr int LQ = TI * 4 / THREADS, LP = TJ * 4 / THREADS, LOADS = LQ + LP;
+  static constexpr int STAGE = SQ::BYTES + SP::BYTES;
+  static constexpr int PITCH = 68;                   // floats between rows of the epilogue's patch of 32 x 64
+  static constexpr int PATCH = 32 * PITCH * 4;
+  static constexpr int RING = NST * STAGE;
+  static constexpr int LDS = RING > WI * WJ * PATCH ? RING : WI * WJ * PATCH;
+
+  static __device__ __forceinline__ void product(const ProductArgs &a, int64_t i0, int64_t j0, int k0, int k1, char *lds,
+                                                 float16v (&acc)[FI][FJ]) {
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = (w % WI) * (TI / WI), wj = (w / WI) * (TJ / WJ);
+    const char *src[LOADS];
+    int at[LOADS];                                   // the chunk's place along the summed axis
+    auto aim = [&](const Operand &o, int64_t outer0, int64_t R, bool tr, int outer, int c, int n) {
+      int64_t r = outer0 + outer;
+      if (tr) r = r < R ? r : 0;                     // columns and rows beyond C: any of the array's
+      else r = r < R ? r : R - 1;
+      src[n] = (const char *)o.p + (tr ? c * o.stride + r : r * o.stride + c) * (int64_t)sizeof(T);
+      at[n] = c;
+    };
+#pragma unroll
+    for (int n = 0; n < LQ; n++) {
+      int o, c;
+      SQ::place(tid + n * THREADS, o, c);
+      aim(a.q, i0, a.I, QT, o, c, n);
+    }
+#pragma unroll
+    for (int n = 0; n < LP; n++) {
+      int o, c;
+      SP::place(tid + n * THREADS, o, c);
+      aim(a.p, j0, a.J, PT, o, c, LQ + n);
+    }
+    const uint32_t base = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds + w * (WAVE * 16));
+    const int64_t dq = (QT ? a.q.stride * SQ::KE : SQ::KE) * (int64_t)sizeof(T);
+    const int64_t dp = (PT ? a.p.stride * SP::KE : SP::KE) * (int64_t)sizeof(T);
+    const int last = (int)a.steps - 1, left = (int)(a.K - (int64_t)last * SQ::KE);   // of the last stage
+    // stages past the end load the last one again, so that the count of loads in flight
+    // stays a constant
+    auto fetch = [&](int k, int slot) {
+      const int kk = k < k1 ? k : k1 - 1;
+      const uint32_t l = base + slot * STAGE;
+      const int64_t oq = kk * dq, op = kk * dp;
+      const bool whole = kk < last || left == SQ::KE;
+#pragma unroll
+      for (int n = 0; n < LOADS; n++) {
+        const char *p = src[n] + (n < LQ ? oq : op);
+        if (!whole && at[n] >= left) p = reinterpret_cast<const char *>(&zero_chunk);
+        to_lds(p, l + (n < LQ ? n * THREADS * 16 : SQ::BYTES + (n - LQ) * THREADS * 16));
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < FI; i++)
+#pragma unroll
+      for (int j = 0; j < FJ; j++)
+#pragma unroll
+        for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
+    word4 fq[2][2][FI], fp[2][2][FJ];
+    auto read = [&](int slot, int set) {
+      const char *l = lds + slot * STAGE;
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+#pragma unroll
+        for (int i = 0; i < FI; i++) fq[set][u][i] = SQ::fragment(l, wi + i * 32, u);
+#pragma unroll
+        for (int j = 0; j < FJ; j++) fp[set][u][j] = SP::fragment(l + SQ::BYTES, wj + j * 32, u);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < NST; k++) fetch(k0 + k, k);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NST - 1) * LOADS) : "memory");
+    read(0, 0);
+    int slot = 0;                                    // of stage k
+    auto step = [&](int k, int set) {
+      const int next = slot + 1 == NST ? 0 : slot + 1;
+      // the oldest stage in flight is in LDS for this wave and its own fragment reads
+      // are done (seen by the compiler's own count), then the same of the other waves
+      __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0)
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NST - 2) * LOADS) : "memory");
+      fetch(k + NST, slot);
+      read(next, set ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int i = 0; i < FI; i++)
+#pragma unroll
+          for (int j = 0; j < FJ; j++) Cores<T>::mul(fp[set][u][j], fq[set][u][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+      slot = next;
+    };
+    int k = k0;
+    for (; k + 1 < k1; k += 2) {
+      step(k, 0);
+      step(k + 1, 1);
+    }
+    if (k < k1) step(k, 0);
+    // nothing may land in LDS after this
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+};
+
+// Workgroups go to the eight XCDs in turn. Work item of workgroup b out of n such that each
+// XCD takes a run of neighbouring items, whose operands its own L2 then holds.
+__device__ __forceinline__ int64_t by_xcd(int64_t b, int64_t n) {
+  const int64_t x = b & 7, each = n >> 3, more = n & 7;
+  return x * each + (x < more ? x : more) + (b >> 3);
+}
+
+template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT, int OUT>
+__global__ __launch_bounds__(WI * WJ * WAVE, 2) void k_direct(ProductArgs a) {
+  typedef Direct<T, TI, TJ, WI, WJ, NST, QT, PT> D;
+  __shared__ __attribute__((aligned(16))) char lds[D::LDS];
+  // runs of eight tiles along I by all of J
+  const int64_t t = by_xcd(blockIdx.x, a.ti * a.tj), band = t / (8 * a.tj), in = t - band * 8 * a.tj;
+  const int64_t high = a.ti - band * 8 < 8 ? a.ti - band * 8 : 8;
+  const int64_t i0 = (band * 8 + in % high) * TI, j0 = in / high * TJ;
+  const int k0 = (int)(blockIdx.y * a.per), k1 = k0 + a.per < a.steps ? (int)(k0 + a.per) : (int)a.steps;
+  float16v acc[D::FI][D::FJ];
+  D::product(a, i0, j0, k0, k1, lds, acc);
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t wi = i0 + (w % WI) * (TI / WI), wj = j0 + (w / WI) * (TJ / WJ);
+  float *patch = reinterpret_cast<float *>(lds + w * D::PATCH);
+  DropKey key = {};
+  if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
+  // 32 x 64 values at a time through a patch of LDS: eight neighbours of a row per lane
+  constexpr int FJ2 = D::FJ / 2;
+  const int pr = lane >> 3, pc = (lane & 7) * 8;
+  word4 res[4][sizeof(T) / 2];
+  auto ahead = [&](int b) {                          // the residual of block b
+    if (OUT != OUT_LAYER || !a.layer.res || a.splits > 1) return;
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+      const int64_t row = wi + b % D::FI * 32 + h * 8 + pr, col = wj + b / D::FI * 64 + pc;
+      if (row < a.I && col < a.J) load_res<T>(a.layer, row, col, a.J - col < 8 ? (int)(a.J - col) : 8, res[h]);
+    }
+  };
+  ahead(0);
+  float bias[8];
+#pragma unroll 1
+  for (int b = 0; b < D::FI * FJ2; b++) {
+    const int64_t col = wj + b / D::FI * 64 + pc;
+    const int n = a.J <= col ? 0 : a.J - col < 8 ? (int)(a.J - col) : 8;
+    if (OUT == OUT_LAYER && b % D::FI == 0) load_bias<T>(a.layer, col, n, bias);
+#pragma unroll
+    for (int s = 0; s < D::FI * FJ2; s++)
+      if (s == b) {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const float16v &v = acc[s % D::FI][s / D::FI * 2 + h];
+            *reinterpret_cast<float4 *>(patch + (lane & 31) * D::PITCH + h * 32 + 8 * e + 4 * (lane >> 5)) =
+                make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+      }
+    word4 mine[4][sizeof(T) / 2];
+#pragma unroll
+    for (int h = 0; h < 4; h++)
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; k++) mine[h][k] = res[h][k];
+    if (b + 1 < D::FI * FJ2) ahead(b + 1);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int h = 0; h < 4; h++) {
+      const int64_t row = wi + b % D::FI * 32 + h * 8 + pr;
+      float v[8];
+      load8<float>(patch + (h * 8 + pr) * D::PITCH + pc, 8, v);
+      if (row < a.I && n > 0) emit8<T, OUT>(a, key, row, col, n, bias, mine[h], v);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// Adds the splits of a product in order, eight neighbours of a row at a time, and finishes
+// them. SLICES threads share the splits of the same eight, where there are many for few values.
+template <typename T, int OUT, int SLICES>
+__global__ __launch_bounds__(LN_THREADS) void k_product_join(ProductArgs a, int splits) {
+  constexpr int G = LN_THREADS / SLICES;
+  __shared__ float s[SLICES > 1 ? SLICES * G * 9 : 1];
+  const int64_t per = (a.J + 7) / 8, n = per * a.I;
+  const int g = threadIdx.x % G, l = threadIdx.x / G;
+  DropKey key = {};
+  if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
+  a.splits = 1;
+  for (int64_t t0 = (int64_t)blockIdx.x * G; t0 < n; t0 += (int64_t)gridDim.x * G) {
+    const int64_t t = t0 + g, row = t / per, col = (t - row * per) * 8;
+    const int w = t >= n ? 0 : a.J - col < 8 ? (int)(a.J - col) : 8;
+    float v[8] = {};
+    if (w > 0) {
+#pragma unroll 4
+      for (int k = l; k < splits; k += SLICES) {
+        float x[8];
+        load8<float>(a.part + ((int64_t)k * a.I + row) * a.J + col, w, x);
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] += x[j];
+      }
+    }
+    if constexpr (SLICES > 1) {
+#pragma unroll
+      for (int j = 0; j < 8; j++) s[(l * G + g) * 9 + j] = v[j];
+      __syncthreads();
+      if (l == 0) {
+        for (int k = 1; k < SLICES; k++)
+#pragma unroll
+          for (int j = 0; j < 8; j++) v[j] += s[(k * G + g) * 9 + j];
+      }
+      __syncthreads();
+      if (l > 0) continue;
+    }
+    if (w > 0) {
+      float bias[8];
+      word4 res[sizeof(T) / 2];
+      if constexpr (OUT == OUT_LAYER) {
+        load_bias<T>(a.layer, col, w, bias);
+        load_res<T>(a.layer, row, col, w, res);
+      }
+      emit8<T, OUT>(a, key, row, col, w, bias, res, v);
+    }
+  }
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+// Whether every row is whole chunks at chunk addresses.
+template <typename T>
+bool whole_chunks(const Operand &o, bool tr, int64_t R, int64_t K) {
+  constexpr int E = 16 / sizeof(T);
+  return ((uintptr_t)o.p & 15) == 0 && o.stride % E == 0 && (tr ? R : K) % E == 0;
+}
+
+template <typename T, bool QT, bool PT, int OUT>
+int run_product(ProductArgs a, hipStream_t stream) {
+  constexpr int KE = 64 / sizeof(T);
+  const Cut cut = product_cut(a.I, a.J, a.K, sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16);
+  const bool direct = a.K > 0 && whole_chunks<T>(a.q, QT, a.I, a.K) && whole_chunks<T>(a.p, PT, a.J, a.K);
+  a.steps = (a.K + KE - 1) / KE;
+  a.per = (a.steps + cut.splits - 1) / cut.splits;
+  a.splits = a.per > 0 ? (int)((a.steps + a.per - 1) / a.per) : 1;
+  const int side_i = !direct ? LOOSE_SIDE : TILES[cut.tile].i, side_j = !direct ? LOOSE_SIDE : TILES[cut.tile].j;
+  a.ti = (a.I + side_i - 1) / side_i;
+  a.tj = (a.J + side_j - 1) / side_j;
+  const dim3 grid((unsigned)(a.ti * a.tj), (unsigned)a.splits);
+  if (!direct)
+    hipLaunchKernelGGL((k_product<T, LOOSE_SIDE, LOOSE_SIDE, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
+  else if (cut.tile == 0)
+    hipLaunchKernelGGL((k_direct<T, 256, 256, 2, 4, 4, QT, PT, OUT>), grid, dim3(512), 0, stream, a);
+  else if (cut.tile == 1)
+    hipLaunchKernelGGL((k_direct<T, 128, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_direct<T, 64, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
+  SPLAT_LAUNCH_CHECK();
+  if (a.splits == 1) return SPLAT_OK;
+  const int64_t items = a.I * ((a.J + 7) / 8);
+  auto blocks = [](int64_t n) { return dim3((unsigned)(n < 65536 ? n : 65536)); };
+  if (a.splits >= 16 && items < 65536)
+    hipLaunchKernelGGL((k_product_join<T, OUT, 16>), blocks((items + 15) / 16), dim3(LN_THREADS), 0, stream, a, a.splits);
+  else
+    hipLaunchKernelGGL((k_product_join<T, OUT, 1>), blocks((items + LN_THREADS - 1) / LN_THREADS), dim3(LN_THREADS), 0, stream, a,
+                       a.splits);
+  SPLAT_LAUNCH_CHECK();
+  return SPLAT_OK;
+}
+
+template <typename T>
+int product(const ProductArgs &a, bool qt, bool pt, int out, hipStream_t s) {
+  if (out == OUT_LAYER) return pt ? run_product<T, false, true, OUT_LAYER>(a, s) : run_product<T, false, false, OUT_LAYER>(a, s);
+  if (qt) return run_product<T, true, true, OUT_STORE>(a, s);
+  return pt ? run_product<T, false, true, OUT_STORE>(a, s) : run_product<T, false, false, OUT_STORE>(a, s);
+}
+
+}  // namespace
