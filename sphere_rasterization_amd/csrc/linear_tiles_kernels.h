@@ -254,6 +254,16 @@ __device__ __forceinline__ void to_lds(const void *p, uint32_t at) {
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
 }
 
+// Asks the compiler for the step's fragment reads and matrix instructions in turn.
+template <int R, int READS, int MULS>
+__device__ __forceinline__ void interleave() {
+  if constexpr (R < READS) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, (R + 1) * MULS / READS - R * MULS / READS, 0);
+    interleave<R + 1, READS, MULS>();
+  }
+}
+
 template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT>
 struct Direct {
   typedef Stage<T, TI, QT> SQ;
@@ -265,6 +275,9 @@ struct Direct {
   static constexpr int PITCH = 68;                   // floats between rows of the epilogue's patch of 32 x 64
   static constexpr int PATCH = 32 * PITCH * 4;
   static constexpr int RING = NST * STAGE;
+  // fragment reads and matrix instructions of a step
+  static constexpr int READS = FI * 2 * (!QT ? 1 : sizeof(T) == 2 ? 2 : 4) + FJ * 2 * (!PT ? 1 : sizeof(T) == 2 ? 2 : 4);
+  static constexpr int MULS = FI * FJ * 2 * (sizeof(T) == 2 ? 1 : 4);
   static constexpr int LDS = RING > WI * WJ * PATCH ? RING : WI * WJ * PATCH;
 
   static __device__ __forceinline__ void product(const ProductArgs &a, int64_t i0, int64_t j0, int k0, int k1, char *lds,
@@ -341,13 +354,13 @@ struct Direct {
       asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NST - 2) * LOADS) : "memory");
       fetch(k + NST, slot);
       read(next, set ^ 1);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int i = 0; i < FI; i++)
 #pragma unroll
           for (int j = 0; j < FJ; j++) Cores<T>::mul(fp[set][u][j], fq[set][u][i], acc[i][j]);
+      interleave<0, READS, MULS>();
       __builtin_amdgcn_sched_barrier(0);
       slot = next;
     };
@@ -385,17 +398,15 @@ __global__ __launch_bounds__(WI * WJ * WAVE, 2) void k_direct(ProductArgs a) {
   float *patch = reinterpret_cast<float *>(lds + w * D::PATCH);
   DropKey key = {};
   if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
-  // 32 x 64 values at a time through a patch of LDS: eight neighbours of a row per lane
+  // 32 x 64 values at a time through a patch of LDS, eight neighbours of a row per lane; the
+  // residual of the next eight rows is on its way meanwhile
   constexpr int FJ2 = D::FJ / 2;
   const int pr = lane >> 3, pc = (lane & 7) * 8;
-  word4 res[4][sizeof(T) / 2];
-  auto ahead = [&](int b) {                          // the residual of block b
-    if (OUT != OUT_LAYER || !a.layer.res || a.splits > 1) return;
-#pragma unroll
-    for (int h = 0; h < 4; h++) {
-      const int64_t row = wi + b % D::FI * 32 + h * 8 + pr, col = wj + b / D::FI * 64 + pc;
-      if (row < a.I && col < a.J) load_res<T>(a.layer, row, col, a.J - col < 8 ? (int)(a.J - col) : 8, res[h]);
-    }
+  const bool want_res = OUT == OUT_LAYER && a.layer.res && a.splits == 1;
+  word4 next[sizeof(T) / 2];
+  auto ahead = [&](int at) {                         // rows 8 at .. of the wave's quarter, FI * 4 of them to a column block
+    const int64_t row = wi + at % (D::FI * 4) * 8 + pr, col = wj + at / (D::FI * 4) * 64 + pc;
+    if (want_res && row < a.I && col < a.J) load_res<T>(a.layer, row, col, a.J - col < 8 ? (int)(a.J - col) : 8, next);
   };
   ahead(0);
   float bias[8];
@@ -416,19 +427,17 @@ __global__ __launch_bounds__(WI * WJ * WAVE, 2) void k_direct(ProductArgs a) {
                 make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
       }
-    word4 mine[4][sizeof(T) / 2];
-#pragma unroll
-    for (int h = 0; h < 4; h++)
-#pragma unroll
-      for (int k = 0; k < (int)sizeof(T) / 2; k++) mine[h][k] = res[h][k];
-    if (b + 1 < D::FI * FJ2) ahead(b + 1);
     __builtin_amdgcn_wave_barrier();
-#pragma unroll
+#pragma unroll 1
     for (int h = 0; h < 4; h++) {
       const int64_t row = wi + b % D::FI * 32 + h * 8 + pr;
+      word4 res[sizeof(T) / 2];
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; k++) res[k] = next[k];
+      if (b * 4 + h + 1 < D::FI * FJ2 * 4) ahead(b * 4 + h + 1);
       float v[8];
       load8<float>(patch + (h * 8 + pr) * D::PITCH + pc, 8, v);
-      if (row < a.I && n > 0) emit8<T, OUT>(a, key, row, col, n, bias, mine[h], v);
+      if (row < a.I && n > 0) emit8<T, OUT>(a, key, row, col, n, bias, res, v);
     }
     __builtin_amdgcn_wave_barrier();
   }
