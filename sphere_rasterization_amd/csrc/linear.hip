@@ -34,20 +34,30 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
   DropKey key = {};
   if (a.draw) key = drop_key(a.drop);
   float t[8] = {};
-  if (n > 0)
-    for (int64_t m = m0 + r; m < m1; m += LN_THREADS / 8) {
-      float d[8];
-      load8<T>((const T *)a.dy + m * a.ys + col, n, d);
-      if (a.act != SPLAT_ACT_NONE) {
-        float z[8];
-        load8<T>((const T *)a.z + m * a.N + col, n, z);
-        slope_times<T>(d, z, a.act);
-      }
-      if (a.draw) drop8<false>(d, m * a.N + col, a.drop, key);
-      if (a.dz) store8<T>((T *)a.dz + m * a.N + col, n, d);
+  if (n > 0) {
+    // two rows at once: their loads are on the way together
+    constexpr int AT_ONCE = 2, STEP = LN_THREADS / 8;
+    for (int64_t m = m0 + r; m < m1; m += AT_ONCE * STEP) {
+      float d[AT_ONCE][8], z[AT_ONCE][8];
 #pragma unroll
-      for (int j = 0; j < 8; j++) t[j] += d[j];
+      for (int u = 0; u < AT_ONCE; u++) {
+        const int64_t k = m + u * STEP;
+        const int w = k < m1 ? n : 0;
+        load8<T>((const T *)a.dy + k * a.ys + col, w, d[u]);
+        if (a.act != SPLAT_ACT_NONE) load8<T>((const T *)a.z + k * a.N + col, w, z[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; u++) {
+        const int64_t k = m + u * STEP;
+        if (k >= m1) break;
+        if (a.act != SPLAT_ACT_NONE) slope_times<T>(d[u], z[u], a.act);
+        if (a.draw) drop8<false>(d[u], k * a.N + col, a.drop, key);
+        if (a.dz) store8<T>((T *)a.dz + k * a.N + col, n, d[u]);
+#pragma unroll
+        for (int j = 0; j < 8; j++) t[j] += d[u][j];
+      }
     }
+  }
   if (!a.sums) return;
 #pragma unroll
   for (int j = 0; j < 8; j++) s[r][c + j] = t[j];
@@ -60,13 +70,22 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
   }
 }
 
-// db: the chunks' sums in order, a wave's lanes on neighbouring columns.
+// db: the chunks' sums, 32 columns by 8 slices of the chunks a workgroup, each in order.
 template <typename T>
 __global__ __launch_bounds__(LN_THREADS) void k_linear_bias(const float *sums, int64_t chunks, int64_t N, void *db, int f32) {
-  const int64_t col = (int64_t)blockIdx.x * LN_THREADS + threadIdx.x;
-  if (col >= N) return;
+  __shared__ float s[8][33];
+  const int e = threadIdx.x & 31, l = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + e;
   float v = 0.0f;
-  for (int64_t k = 0; k < chunks; k++) v += sums[k * N + col];
+  if (col < N) {
+#pragma unroll 4
+    for (int64_t k = l; k < chunks; k += 8) v += sums[k * N + col];
+  }
+  s[l][e] = v;
+  __syncthreads();
+  if (l > 0 || col >= N) return;
+#pragma unroll
+  for (int k = 1; k < 8; k++) v += s[k][e];
   if (f32) ((float *)db)[col] = v;
   else ((T *)db)[col] = (T)v;
 }
@@ -188,7 +207,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     hipLaunchKernelGGL(k_linear_slope<T>, grid, dim3(LN_THREADS), 0, stream, s);
     SPLAT_LAUNCH_CHECK();
     if (db) {
-      hipLaunchKernelGGL(k_linear_bias<T>, dim3((unsigned)((N + LN_THREADS - 1) / LN_THREADS)), dim3(LN_THREADS), 0, stream,
+      hipLaunchKernelGGL(k_linear_bias<T>, dim3((unsigned)((N + 31) / 32)), dim3(LN_THREADS), 0, stream,
                          (const float *)sums, (int64_t)grid.y, N, db, d->bias_dtype == SPLAT_F32);
       SPLAT_LAUNCH_CHECK();
     }

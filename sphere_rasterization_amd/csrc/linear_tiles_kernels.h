@@ -383,7 +383,7 @@ __device__ __forceinline__ int64_t by_xcd(int64_t b, int64_t n) {
 }
 
 template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT, int OUT>
-__global__ __launch_bounds__(WI * WJ * WAVE, 2) void k_direct(ProductArgs a) {
+__global__ __launch_bounds__(WI * WJ * WAVE, TI * TJ > 128 * 128 * WI * WJ / 2 ? 1 : 2) void k_direct(ProductArgs a) {
   typedef Direct<T, TI, TJ, WI, WJ, NST, QT, PT> D;
   __shared__ __attribute__((aligned(16))) char lds[D::LDS];
   // runs of eight tiles along I by all of J
@@ -515,7 +515,9 @@ int run_product(ProductArgs a, hipStream_t stream) {
   if (!direct)
     hipLaunchKernelGGL((k_product<T, LOOSE_SIDE, LOOSE_SIDE, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
   else if (cut.tile == 0)
-    hipLaunchKernelGGL((k_direct<T, 256, 256, 2, 4, 4, QT, PT, OUT>), grid, dim3(512), 0, stream, a);
+    // transposing reads bring half as much a cycle: with both operands transposed four waves of
+    // 128 x 128, which read least, beat eight (4096^3 bf16: see DW8)
+    hipLaunchKernelGGL((k_direct<T, 256, 256, 2, QT && PT ? 2 : 4, 4, QT, PT, OUT>), grid, dim3(QT && PT ? 256 : 512), 0, stream, a);
   else if (cut.tile == 1)
     hipLaunchKernelGGL((k_direct<T, 128, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
   else
