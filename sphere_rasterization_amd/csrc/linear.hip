@@ -15,6 +15,7 @@ namespace {
 struct SlopeArgs {
   const void *dy, *z;            // z packed
   void *dz;                      // packed, or NULL: only the sums
+  void *dz2;                     // what dz's rounding lost, or NULL
   float *sums;                   // [chunks][N], or NULL
   int64_t M, N, ys, chunk;       // rows per workgroup
   int act, draw;
@@ -53,6 +54,17 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
         if (a.act != SPLAT_ACT_NONE) slope_times<T>(d[u], z[u], a.act);
         if (a.draw) drop8<false>(d[u], k * a.N + col, a.drop, key);
         if (a.dz) store8<T>((T *)a.dz + k * a.N + col, n, d[u]);
+        if constexpr (sizeof(T) == 2) {
+          if (a.dz2) {
+            word4 hi, lo;
+            float v[8];
+            split8<T>(d[u], hi, lo);
+            const Pack<T, 8> l = __builtin_bit_cast(Pack<T, 8>, lo);
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = (float)l.v[j];
+            store8<T>((T *)a.dz2 + k * a.N + col, n, v);
+          }
+        }
 #pragma unroll
         for (int j = 0; j < 8; j++) t[j] += d[u][j];
       }
@@ -114,6 +126,14 @@ int64_t slope_chunks(int64_t M, int64_t N) {
 // W as [in][out], `out` contiguous, or its transpose.
 bool w_by_out(int64_t si, int64_t so) { return so == 1 && si != 1; }
 
+// Parts of dz. One rounding of it adds as much error to dx and dW as their own rounding: where
+// values are few, with luck more, and the products cost little; where they are many, the two
+// errors together stay at sqrt 2 of the one, and a second part would take twice the time.
+int parts_of(const splat_dense *d) {
+  const bool shaped = d->act != SPLAT_ACT_NONE || d->drop.p > 0.0;
+  return shaped && d->dtype != SPLAT_F32 && d->rows * d->out < (1 << 20) ? 2 : 1;
+}
+
 struct Plan {
   size_t pre, dz, sums, part, total;
 };
@@ -122,15 +142,16 @@ Plan plan_of(const splat_dense *d, bool bwd) {
   const int64_t M = d->rows, N = d->out, K = d->in;
   if (M == 0 || N == 0) return p;
   auto most = [&](size_t v) { if (v > p.part) p.part = v; };
-  most(product_part_bytes(M, N, K, d->dtype));
+  most(product_part_bytes(M, N, K, 1, d->dtype));
   if (bwd) {
     const size_t e = dtype_bytes(d->dtype);
+    const int parts = parts_of(d);
     if (d->act != SPLAT_ACT_NONE) p.pre = ws_align((size_t)M * N * e);
-    if (d->act != SPLAT_ACT_NONE || d->drop.p > 0.0) p.dz = ws_align((size_t)M * N * e);
+    if (d->act != SPLAT_ACT_NONE || d->drop.p > 0.0) p.dz = parts * ws_align((size_t)M * N * e);
     p.sums = ws_align(sizeof(float) * (size_t)slope_chunks(M, N) * N);
-    most(product_part_bytes(M, K, N, d->dtype));
-    most(product_part_bytes(K, N, M, d->dtype));
-    most(product_part_bytes(N, K, M, d->dtype));
+    most(product_part_bytes(M, K, N, parts, d->dtype));
+    most(product_part_bytes(K, N, M, parts, d->dtype));
+    most(product_part_bytes(N, K, M, parts, d->dtype));
   }
   p.total = p.pre + p.dz + p.sums + p.part;
   return p;
@@ -143,16 +164,17 @@ int forward(const splat_dense *d, const void *x, const void *w, const LayerArgs 
   a.I = d->rows;
   a.J = d->out;
   a.K = d->in;
-  a.q = {x, d->x_stride};
+  a.q = {x, d->x_stride, 0};
+  a.parts = 1;
   a.c = y;
   a.cs = ys;
   a.part = part;
   a.layer = l;
   if (w_by_out(d->w_in_stride, d->w_out_stride)) {
-    a.p = {w, d->w_in_stride};
+    a.p = {w, d->w_in_stride, 0};
     return launch_product<T>(a, false, true, OUT_LAYER, stream);
   }
-  a.p = {w, d->w_out_stride};
+  a.p = {w, d->w_out_stride, 0};
   return launch_product<T>(a, false, false, OUT_LAYER, stream);
 }
 
@@ -182,6 +204,8 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
   void *my_pre = at, *dz = at + p.pre;
   float *sums = (float *)(at + p.pre + p.dz), *part = (float *)(at + p.pre + p.dz + p.sums);
   const bool draw = d->drop.p > 0.0, shaped = d->act != SPLAT_ACT_NONE || draw;
+  const int parts = parts_of(d);
+  const int64_t rest = parts == 2 ? (int64_t)(p.dz / 2) : 0;
   if (d->act != SPLAT_ACT_NONE && !pre) {
     LayerArgs l = {};
     l.bias = bias;
@@ -194,6 +218,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     s.dy = dy;
     s.z = pre;
     s.dz = shaped ? dz : nullptr;
+    s.dz2 = parts == 2 ? (char *)dz + rest : nullptr;
     s.sums = db ? sums : nullptr;
     s.M = M;
     s.N = N;
@@ -212,28 +237,30 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
       SPLAT_LAUNCH_CHECK();
     }
   }
-  const Operand z = shaped ? Operand{dz, N} : Operand{dy, d->y_stride};
+  const Operand z = shaped ? Operand{dz, N, rest} : Operand{dy, d->y_stride, 0};
   if (dx && K > 0) {
     ProductArgs a = {};
     a.I = M;
     a.J = K;
     a.K = N;
+    a.parts = parts;
     a.q = z;
     a.c = dx;
     a.cs = d->dx_stride;
     a.part = part;
     if (w_by_out(d->w_in_stride, d->w_out_stride)) {
-      a.p = {w, d->w_in_stride};
+      a.p = {w, d->w_in_stride, 0};
       st = launch_product<T>(a, false, false, OUT_STORE, stream);
     } else {
-      a.p = {w, d->w_out_stride};
+      a.p = {w, d->w_out_stride, 0};
       st = launch_product<T>(a, false, true, OUT_STORE, stream);
     }
     if (st) return st;
   }
   if (dw && K > 0) {
     ProductArgs a = {};
-    const Operand xo = {x, d->x_stride};
+    const Operand xo = {x, d->x_stride, 0};
+    a.parts = parts;
     a.I = by_out ? K : N;
     a.J = by_out ? N : K;
     a.K = M;
@@ -252,7 +279,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
 // The cheapest of the tiles and splits by what a stage (64 bytes of the summed axis of every
 // tile at work) was measured to take, in us: with one workgroup on a CU, and with as many as
 // fit. Splits cost the writing and reading of their sums and a launch.
-Cut product_cut(int64_t I, int64_t J, int64_t K, int dtype) {
+Cut product_cut(int64_t I, int64_t J, int64_t K, int parts, int dtype) {
   struct Rate {
     int fit;
     double one, all, rest;       // rest: of a tile outside its stages
@@ -261,7 +288,7 @@ Cut product_cut(int64_t I, int64_t J, int64_t K, int dtype) {
                                        {{1, 4.40, 4.40, 8.0}, {2, 1.10, 1.95, 5.0}, {3, 0.60, 1.50, 4.0}}};
   constexpr int CUS = 256;
   const int f32 = dtype == SPLAT_F32;
-  const int64_t stages = (K + (f32 ? 16 : 32) - 1) / (f32 ? 16 : 32);
+  const int64_t stages = parts * ((K + (f32 ? 16 : 32) - 1) / (f32 ? 16 : 32));
   Cut best = {2, 1};
   double least = 1e30;
   for (int t = 0; t < 3; t++) {

@@ -98,3 +98,19 @@ __device__ __forceinline__ void finish_layer(const LayerArgs &l, const DropKey &
   }
   store8<T>(y + row * ys + col, n, v);
 }
+
+// dz in one or two parts of T: two of 16-bit types hold it to 16 bits and more, where one
+// would add as much error to dx and dW as their own rounding does. The second part of an
+// infinity is zero.
+template <typename T>
+__device__ __forceinline__ void split8(const float (&d)[8], word4 &hi, word4 &lo) {
+  Pack<T, 8> h, l;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    h.v[j] = (T)d[j];
+    const float f = (float)h.v[j];
+    l.v[j] = (T)(fabsf(f) < INFINITY ? d[j] - f : 0.0f);
+  }
+  hi = __builtin_bit_cast(word4, h);
+  lo = __builtin_bit_cast(word4, l);
+}

@@ -9,13 +9,15 @@ enum { OUT_STORE, OUT_LAYER };
 struct Operand {
   const void *p;                 // [outer][c] with c contiguous, or [c][outer] (transposed)
   int64_t stride;                // elements between rows of that array
+  int64_t rest;                  // bytes from p to what p's rounding lost, an array of its own, or 0
 };
 
 struct ProductArgs {
   Operand q, p;
   int64_t I, J, K;               // rows and columns of C, length of the summed axis
   int64_t ti, tj;                // tiles along I and J
-  int64_t steps, per;            // stages of the summed axis, and of one split
+  int parts;                     // 2: Q or P comes in two parts, and the summed axis is gone through twice
+  int64_t axis, steps, per;      // stages of the summed axis, of all parts, and of one split
   void *c;
   int64_t cs;                    // row stride of C
   float *part;                   // [splits][I][J] sums where the summed axis is split, else unused
@@ -34,10 +36,10 @@ struct TileShape {
 };
 constexpr TileShape TILES[3] = {{256, 256}, {128, 128}, {64, 128}};
 constexpr int LOOSE_SIDE = 64;   // of arrays that are not whole, aligned chunks
-Cut product_cut(int64_t I, int64_t J, int64_t K, int dtype);
-static inline size_t product_part_bytes(int64_t I, int64_t J, int64_t K, int dtype) {
+Cut product_cut(int64_t I, int64_t J, int64_t K, int parts, int dtype);
+static inline size_t product_part_bytes(int64_t I, int64_t J, int64_t K, int parts, int dtype) {
   if (I == 0 || J == 0) return 0;
-  const int n = product_cut(I, J, K, dtype).splits;
+  const int n = product_cut(I, J, K, parts, dtype).splits;
   return n > 1 ? ws_align(sizeof(float) * (size_t)n * I * J) : 0;
 }
 

@@ -145,18 +145,22 @@ struct Tile {
 #pragma unroll
         for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
     word4 rq[SQ::LOADS], rp[SP::LOADS];
-    auto fetch = [&](int64_t k) {
+    auto fetch = [&](int64_t stage) {
+      const bool second = stage >= a.axis;
+      const int64_t k = second ? stage - a.axis : stage;
+      const Operand q = {(const char *)a.q.p + (second ? a.q.rest : 0), a.q.stride, 0};
+      const Operand p = {(const char *)a.p.p + (second ? a.p.rest : 0), a.p.stride, 0};
 #pragma unroll
       for (int n = 0; n < SQ::LOADS; n++) {
         int o, c;
         SQ::place(tid + n * LN_THREADS, o, c);
-        rq[n] = SQ::load(a.q, i0 + o, k * SQ::KE + c, a.I, a.K);
+        rq[n] = SQ::load(q, i0 + o, k * SQ::KE + c, a.I, a.K);
       }
 #pragma unroll
       for (int n = 0; n < SP::LOADS; n++) {
         int o, c;
         SP::place(tid + n * LN_THREADS, o, c);
-        rp[n] = SP::load(a.p, j0 + o, k * SP::KE + c, a.J, a.K);
+        rp[n] = SP::load(p, j0 + o, k * SP::KE + c, a.J, a.K);
       }
     };
     auto keep = [&](int slot) {
@@ -309,13 +313,15 @@ struct Direct {
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds + w * (WAVE * 16));
     const int64_t dq = (QT ? a.q.stride * SQ::KE : SQ::KE) * (int64_t)sizeof(T);
     const int64_t dp = (PT ? a.p.stride * SP::KE : SP::KE) * (int64_t)sizeof(T);
-    const int last = (int)a.steps - 1, left = (int)(a.K - (int64_t)last * SQ::KE);   // of the last stage
+    const int last = (int)a.axis - 1, left = (int)(a.K - (int64_t)last * SQ::KE);    // of the last stage
     // stages past the end load the last one again, so that the count of loads in flight
     // stays a constant
     auto fetch = [&](int k, int slot) {
-      const int kk = k < k1 ? k : k1 - 1;
+      const int stage = k < k1 ? k : k1 - 1;
+      const bool second = stage >= (int)a.axis;
+      const int kk = second ? stage - (int)a.axis : stage;
       const uint32_t l = base + slot * STAGE;
-      const int64_t oq = kk * dq, op = kk * dp;
+      const int64_t oq = kk * dq + (second ? a.q.rest : 0), op = kk * dp + (second ? a.p.rest : 0);
       const bool whole = kk < last || left == SQ::KE;
 #pragma unroll
       for (int n = 0; n < LOADS; n++) {
@@ -503,9 +509,10 @@ bool whole_chunks(const Operand &o, bool tr, int64_t R, int64_t K) {
 template <typename T, bool QT, bool PT, int OUT>
 int run_product(ProductArgs a, hipStream_t stream) {
   constexpr int KE = 64 / sizeof(T);
-  const Cut cut = product_cut(a.I, a.J, a.K, sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16);
+  const Cut cut = product_cut(a.I, a.J, a.K, a.parts, sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16);
   const bool direct = a.K > 0 && whole_chunks<T>(a.q, QT, a.I, a.K) && whole_chunks<T>(a.p, PT, a.J, a.K);
-  a.steps = (a.K + KE - 1) / KE;
+  a.axis = (a.K + KE - 1) / KE;
+  a.steps = a.axis * a.parts;
   a.per = (a.steps + cut.splits - 1) / cut.splits;
   a.splits = a.per > 0 ? (int)((a.steps + a.per - 1) / a.per) : 1;
   const int side_i = !direct ? LOOSE_SIDE : TILES[cut.tile].i, side_j = !direct ? LOOSE_SIDE : TILES[cut.tile].j;
@@ -516,7 +523,7 @@ int run_product(ProductArgs a, hipStream_t stream) {
     hipLaunchKernelGGL((k_product<T, LOOSE_SIDE, LOOSE_SIDE, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
   else if (cut.tile == 0)
     // transposing reads bring half as much a cycle: with both operands transposed four waves of
-    // 128 x 128, which read least, beat eight (4096^3 bf16: see DW8)
+    // 128 x 128, which read least, beat eight (4096 by 4096 by 4096 bf16, forward and backward: 381 us, 407 with eight)
     hipLaunchKernelGGL((k_direct<T, 256, 256, 2, QT && PT ? 2 : 4, 4, QT, PT, OUT>), grid, dim3(QT && PT ? 256 : 512), 0, stream, a);
   else if (cut.tile == 1)
     hipLaunchKernelGGL((k_direct<T, 128, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
