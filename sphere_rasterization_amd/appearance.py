@@ -312,77 +312,81 @@ def _word(name: str, v) -> int:
     return k
 
 
-def _fill_drop(d: L.splat_drop, p: float, rng, ref: torch.Tensor):
-    """Sets d for tensors on ref's device and returns the state to keep (None without one)."""
-    d.p = float(p)
-    if not 0.0 <= d.p <= 1.0:
+_NO_DROP = L.splat_drop()
+
+
+def _drop(p: float, rng, ref: torch.Tensor) -> L.splat_drop:
+    """The descriptor of dropout for tensors on ref's device."""
+    p = float(p)
+    if not 0.0 <= p <= 1.0:
         raise ValueError(f"p: expected a number from 0 to 1, got {p!r}")
     if rng is None:
-        if d.p > 0.0:
+        if p > 0.0:
             raise ValueError("rng: dropout needs (seed, offset) or (state, offset)")
-        return None
+        return _NO_DROP
     if not isinstance(rng, (tuple, list)) or len(rng) != 2:
         raise ValueError("rng: expected (seed, offset) or (state, offset)")
-    seed, d.offset = rng[0], _word("offset", rng[1])
+    seed, offset = rng[0], _word("offset", rng[1])
     if not isinstance(seed, torch.Tensor):
-        d.seed = _word("seed", seed)
-        return None
+        return L.splat_drop(p, _word("seed", seed), offset, None)
     _like("state", seed, ref, (2,), (torch.int64,))
     if seed.stride(0) != 1:
         raise ValueError("state: expected two neighbouring words")
-    d.state = seed.data_ptr()
-    return seed
+    return L.splat_drop(p, 0, offset, seed.data_ptr())
 
 
-def _flat_rows(t: torch.Tensor, width: int) -> torch.Tensor:
-    """t [..., width] as [rows, width] with contiguous rows that do not overlap; a copy where
-    the rows are not evenly spaced."""
-    return _rows(t.reshape(-1, width) if width else t.reshape(t.shape[:-1].numel(), 0))
+def _by_rows(t: torch.Tensor, width: int) -> Tuple[torch.Tensor, int]:
+    """(tensor, row stride) of t [..., width] read as rows that are contiguous and do not overlap;
+    a copy where the rows are not evenly spaced."""
+    if t.is_contiguous():
+        return t, width
+    t = _rows(t.reshape(-1, width) if width else t.reshape(t.shape[:-1].numel(), 0))
+    return t, t.stride(0)
 
 
-def _by_strides(t: torch.Tensor) -> torch.Tensor:
-    """A matrix of which one axis is contiguous and whose rows (or columns) do not overlap."""
+def _by_strides(t: torch.Tensor) -> Tuple[torch.Tensor, int, int]:
+    """(tensor, strides) of a matrix of which one axis is contiguous and whose rows (or columns)
+    do not overlap; a copy of others."""
     r, c = t.shape
-    (si, so), one = t.stride(), r <= 1 or c <= 1
-    if not one and ((so == 1 and si >= c) or (si == 1 and so >= r)):
-        return t
-    return t.contiguous()
+    si, so = t.stride()
+    if r > 1 and c > 1 and ((so == 1 and si >= c) or (si == 1 and so >= r)):
+        return t, si, so
+    return t.contiguous(), c, 1
 
 
-def _dense_desc(x, weight, bias, act: str, p, rng):
-    """(descriptor, state to keep, W as the kernels read it)."""
+def _check_layer(x, weight, bias, act: str) -> Tuple[int, int, int]:
+    """(dtype, inputs, outputs) of a layer whose arguments fit together."""
     if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[0]:
         raise ValueError(f"expected x [..., in] and weight [in, out], got {tuple(x.shape)} and {tuple(weight.shape)}")
     if act not in ACTS:
         raise ValueError(f"act: expected one of {', '.join(ACTS)}, got {act!r}")
-    d = L.splat_dense()
-    d.inputs, d.outputs = _int32("in", weight.shape[0]), _int32("out", weight.shape[1])
-    d.dtype = _dtype("x", x)
-    _like("weight", weight, x, weight.shape, (x.dtype,))
+    k, n = weight.shape
+    k, n = _int32("in", k), _int32("out", n)
+    dt = _dtype("x", x)
+    if weight.dtype != x.dtype or weight.device != x.device:
+        _like("weight", weight, x, weight.shape, (x.dtype,))
     if bias is not None:
-        _like("bias", bias, x, (d.outputs,), (torch.float32, x.dtype))
-    d.bias_dtype = _DTYPES[x.dtype if bias is None else bias.dtype]
-    d.act = ACTS[act]
-    d.rows = math.prod(x.shape[:-1])
-    state = _fill_drop(d.drop, p, rng, x)
-    weight = _by_strides(weight)
-    d.w_in_stride, d.w_out_stride = weight.stride()
-    return d, state, weight
+        _like("bias", bias, x, (n,), (torch.float32, x.dtype))
+    return dt, k, n
 
 
 def _linear(x, weight, bias, act, residual, p, rng, keep: bool):
     """y and, where the backward is faster with it and `keep`, z."""
-    d, _state, weight = _dense_desc(x, weight, bias, act, p, rng)
-    shape = tuple(x.shape[:-1]) + (d.outputs,)
+    dt, k, n = _check_layer(x, weight, bias, act)
+    drop = _drop(p, rng, x)
+    shape = x.shape[:-1] + (n,)
+    rs = 0
     if residual is not None:
         _like("residual", residual, x, shape, (x.dtype,))
-        residual = _flat_rows(residual, d.outputs)
-        d.residual_stride = residual.stride(0)
-    x = _flat_rows(x, d.inputs)
-    d.x_stride, d.y_stride = x.stride(0), d.outputs
+        residual, rs = _by_rows(residual, n)
+    x, xs = _by_rows(x, k)
+    weight, wi, wo = _by_strides(weight)
+    bdt = dt
+    if bias is not None:
+        bdt, bias = _DTYPES[bias.dtype], _flat(bias)
     y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    d = L.splat_dense(dt, bdt, ACTS[act], k, n, math.prod(shape[:-1]), xs, wi, wo, rs, n, 0, 0, 0, drop)
     pre = _packed_like(y) if keep and L.splat_linear_saves(d) else None
-    bias = _flat(bias)
     _keep, ws, nbytes = _workspace(L.splat_linear_workspace_bytes(d, False), x)
     _launch(x, L.splat_linear, d, x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre),
             ws, nbytes)
@@ -405,26 +409,29 @@ def linear_backward(d_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bi
     then computed anew). rng has to draw what the forward's drew: a state's words are read
     again. d_weight is laid out as weight is; d_bias has the type of bias (of x without one)."""
     _no_tangents(d_y, x, weight, bias, pre)
-    d, _state, weight = _dense_desc(x, weight, bias, act, p, rng)
-    _like("d_y", d_y, x, tuple(x.shape[:-1]) + (d.outputs,), (x.dtype,))
+    dt, k, n = _check_layer(x, weight, bias, act)
+    drop = _drop(p, rng, x)
+    shape = x.shape
+    _like("d_y", d_y, x, shape[:-1] + (n,), (x.dtype,))
     if pre is not None:
         _like("pre", pre, x, d_y.shape, (x.dtype,))
         pre = _flat(pre)
-    shape = x.shape
-    x, d_y = _flat_rows(x, d.inputs), _flat_rows(d_y, d.outputs)
-    d.x_stride, d.y_stride, d.dx_stride = x.stride(0), d_y.stride(0), d.inputs
+    x, xs = _by_rows(x, k)
+    d_y, ys = _by_rows(d_y, n)
+    weight, wi, wo = _by_strides(weight)
+    bdt = dt
+    if bias is not None:
+        bdt, bias = _DTYPES[bias.dtype], _flat(bias)
     dx = torch.empty(shape, dtype=x.dtype, device=x.device) if "x" in want else None
-    if d.w_out_stride == 1:
-        dw = torch.empty((d.inputs, d.outputs), dtype=x.dtype, device=x.device)
-    else:
-        dw = torch.empty((d.outputs, d.inputs), dtype=x.dtype, device=x.device).t()
-    d.dw_in_stride, d.dw_out_stride = dw.stride()
-    if "weight" not in want:
-        dw = None
+    dw = None
+    if "weight" in want:
+        dw = torch.empty((k, n), dtype=x.dtype, device=x.device) if wo == 1 else \
+            torch.empty((n, k), dtype=x.dtype, device=x.device).t()
     db = None
     if "bias" in want:
-        db = torch.empty(d.outputs, dtype=x.dtype if bias is None else bias.dtype, device=x.device)
-    bias = _flat(bias)
+        db = torch.empty(n, dtype=x.dtype if bias is None else bias.dtype, device=x.device)
+    dwi, dwo = (n, 1) if wo == 1 else (1, k)
+    d = L.splat_dense(dt, bdt, ACTS[act], k, n, math.prod(shape[:-1]), xs, wi, wo, 0, ys, k, dwi, dwo, drop)
     _keep, ws, nbytes = _workspace(L.splat_linear_workspace_bytes(d, True), x)
     _launch(x, L.splat_linear_bwd, d, d_y.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(pre), _ptr(dx),
             _ptr(dw), _ptr(db), ws, nbytes)
@@ -462,26 +469,27 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     Products of 16-bit values are summed in fp32; the result is rounded once. in and out up
     to 2^20, fewer than 2^31 rows."""
     _no_tangents(x, weight, bias, residual)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, residual)):
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or (bias is not None and bias.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
         return _Linear.apply(x, weight, bias, act, residual, p, rng)
     return _linear(x, weight, bias, act, residual, p, rng, False)[0]
 
 
 def _dropout(x, p, rng, residual):
     dt = _dtype("x", x)
-    d = L.splat_drop()
-    _state = _fill_drop(d, p, rng, x)
+    drop = _drop(p, rng, x)
     if residual is not None:
         _like("residual", residual, x, x.shape, (x.dtype,))
     y = _packed_like(x)
-    cols = x.shape[-1] if x.dim() else 1
     if x.is_contiguous() and (residual is None or residual.is_contiguous()):
         rows, cols, xs, rs = 1, x.numel(), 0, 0
     else:
+        cols, rs = x.shape[-1], 0
         rows = x.numel() // cols if cols else 0
-        x, residual = _flat_rows(x, cols), None if residual is None else _flat_rows(residual, cols)
-        xs, rs = x.stride(0), 0 if residual is None else residual.stride(0)
-    _launch(x, L.splat_dropout, d, dt, rows, cols, x.data_ptr(), xs, _ptr(residual), rs, y.data_ptr(), cols)
+        x, xs = _by_rows(x, cols)
+        if residual is not None:
+            residual, rs = _by_rows(residual, cols)
+    _launch(x, L.splat_dropout, drop, dt, rows, cols, x.data_ptr(), xs, _ptr(residual), rs, y.data_ptr(), cols)
     return y
 
 

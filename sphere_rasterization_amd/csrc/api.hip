@@ -309,6 +309,7 @@ int check_norm(const splat_norm *m, bool bwd, bool writes) {
 }
 
 bool overlap_free_matrix(int64_t in, int64_t out, int64_t si, int64_t so) {
+  if (in == 0 || out == 0) return true;
   if (in <= 1 && out <= 1) return true;
   if (in <= 1) return so >= 1;
   if (out <= 1) return si >= 1;

@@ -37,9 +37,21 @@ struct TileShape {
 constexpr TileShape TILES[3] = {{256, 256}, {128, 128}, {64, 128}};
 constexpr int LOOSE_SIDE = 64;   // of arrays that are not whole, aligned chunks
 Cut product_cut(int64_t I, int64_t J, int64_t K, int parts, int dtype);
+
+// Products of few rows of Q are cut by columns of C (32, or where P lies transposed as many as
+// 16 chunks hold); the axis only where those are too few to fill the chip and every wave keeps
+// eight stages: 8 x 8192 by 8192 x 8192 bf16, P transposed, FEWSPLIT.
+constexpr int FEW = 16;
+static inline int few_splits(int64_t J, int64_t K, bool pt, int dtype) {
+  const int64_t e = dtype == SPLAT_F32 ? 4 : 8, side = pt ? 16 * e : 32, groups = (J + side - 1) / side;
+  const int64_t most = (K + 4 * e - 1) / (4 * e) / 64, want = groups < 256 ? 256 / groups : 1, n = want < most ? want : most;
+  return n < 1 ? 1 : (int)n;
+}
 static inline size_t product_part_bytes(int64_t I, int64_t J, int64_t K, int parts, int dtype) {
   if (I == 0 || J == 0) return 0;
-  const int n = product_cut(I, J, K, parts, dtype).splits;
+  int n = product_cut(I, J, K, parts, dtype).splits;
+  if (I <= FEW)
+    for (int pt = 0; pt < 2; pt++) n = few_splits(J, K, pt, dtype) > n ? few_splits(J, K, pt, dtype) : n;
   return n > 1 ? ws_align(sizeof(float) * (size_t)n * I * J) : 0;
 }
 

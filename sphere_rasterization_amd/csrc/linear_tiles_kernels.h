@@ -5,6 +5,7 @@
 namespace {
 
 typedef float float16v __attribute__((ext_vector_type(16)));
+typedef float float4v __attribute__((ext_vector_type(4)));
 typedef short short4v __attribute__((ext_vector_type(4)));
 
 // What lanes read in the place of chunks beyond an array.
@@ -29,7 +30,6 @@ struct Cores<bf16_t> {
 template <>
 struct Cores<float> {
   static __device__ __forceinline__ void mul(const word4 &p, const word4 &q, float16v &acc) {
-    typedef float float4v __attribute__((ext_vector_type(4)));
     const float4v a = __builtin_bit_cast(float4v, p), b = __builtin_bit_cast(float4v, q);
 #pragma unroll
     for (int k = 0; k < 4; k++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[k], b[k], acc, 0, 0, 0);
@@ -497,6 +497,146 @@ __global__ __launch_bounds__(LN_THREADS) void k_product_join(ProductArgs a, int 
   }
 }
 
+// ---- few rows --------------------------------------------------------------------------
+
+// Products of at most 16 rows of Q, as for single tokens: bound by reading P once. A workgroup
+// takes some columns of C and its waves share the summed axis; P goes from memory straight
+// into the layout of the matrix cores, whose 16 columns are Q's rows.
+//   P by c: 16-byte chunks of 16 rows of P are operands as they lie.
+//   P by j (PT): a lane reads E neighbours of a row of P, for as many rows as a chunk holds
+//   values, and turns them around in registers: fragment e stands for columns E i + e. (fp32
+//   needs no turning: an instruction takes one value a lane.)
+// 1 x 2048 by 2048 x 8192 bf16: see FEWTIME.
+template <typename T, bool PT>
+struct Few {
+  static constexpr int E = 16 / sizeof(T), KE = 64 / sizeof(T);
+  static constexpr int WAVES = 8, THREADS = WAVES * WAVE;
+  static constexpr int TILES_J = PT ? E : 2;         // fragments of 16 columns
+  static constexpr int J = 16 * TILES_J;             // columns of a workgroup
+  static constexpr int PITCH = J + 4;
+  static constexpr int UNROLL = PT ? 2 : 4;          // steps of 64 bytes whose loads are on the way together
+};
+
+// 16 x 16 products of one chunk a lane.
+template <typename T>
+__device__ __forceinline__ float4v few_mul(const word4 &a, const word4 &b, float4v c);
+template <>
+__device__ __forceinline__ float4v few_mul<f16_t>(const word4 &a, const word4 &b, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ float4v few_mul<bf16_t>(const word4 &a, const word4 &b, float4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bhalf8, a), __builtin_bit_cast(bhalf8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ float4v few_mul<float>(const word4 &a, const word4 &b, float4v c) {
+  const float4v x = __builtin_bit_cast(float4v, a), y = __builtin_bit_cast(float4v, b);
+#pragma unroll
+  for (int k = 0; k < 4; k++) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[k], y[k], c, 0, 0, 0);
+  return c;
+}
+
+// Value e of each of the rows' chunks, as one chunk.
+template <typename T>
+__device__ __forceinline__ word4 turn(const word4 (&rows)[16 / sizeof(T)], int e) {
+  word4 v;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 4; k++) v[k] = rows[k][e];
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+      v[k] = __builtin_amdgcn_perm(rows[2 * k + 1][e >> 1], rows[2 * k][e >> 1], e & 1 ? 0x07060302u : 0x05040100u);
+  }
+  return v;
+}
+
+template <typename T, bool PT, int OUT>
+__global__ __launch_bounds__((Few<T, PT>::THREADS)) void k_few(ProductArgs a) {
+  typedef Few<T, PT> F;
+  constexpr int E = F::E, KE = F::KE, NT = F::TILES_J, U = F::UNROLL, LOADS = PT ? E : NT;
+  typedef const typename Loose<T, E>::type *ptr;
+  __shared__ float sums[F::WAVES * 16 * F::PITCH];
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, w = threadIdx.x >> 6;
+  const int64_t j0 = (int64_t)blockIdx.x * F::J;
+  // stages of this workgroup's share of the axis, and of this wave's
+  const int K = (int)a.K, from = (int)(blockIdx.y * a.per), to = from + a.per < a.axis ? (int)(from + a.per) : (int)a.axis;
+  const int per = (to - from + F::WAVES - 1) / F::WAVES;
+  const int s0 = from + w * per, s1 = s0 + per < to ? s0 + per : to;
+  float4v acc[NT];
+#pragma unroll
+  for (int t = 0; t < NT; t++) acc[t] = float4v{0, 0, 0, 0};
+  const T *q = (const T *)a.q.p + i * a.q.stride + g * E, *q2 = (const T *)((const char *)q + a.q.rest);
+  const bool row = i < a.I;
+  for (int s = s0; s < s1; s += U) {
+    word4 p[U][LOADS], x[U], x2[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int c = (s + u) * KE + g * E;            // the lane's chunk of the summed axis
+      const bool on = s + u < s1 && c < K;           // whole: K is whole chunks
+      x[u] = x2[u] = word4{0, 0, 0, 0};
+      if (on && row) {
+        x[u] = *reinterpret_cast<ptr>(q + (int64_t)(s + u) * KE);
+        if (a.parts == 2) x2[u] = *reinterpret_cast<ptr>(q2 + (int64_t)(s + u) * KE);
+      }
+#pragma unroll
+      for (int n = 0; n < LOADS; n++) {
+        const int64_t j = PT ? j0 + i * E : j0 + 16 * n + i;
+        p[u][n] = word4{0, 0, 0, 0};
+        if (on && j < a.J)
+          p[u][n] = *reinterpret_cast<ptr>((const T *)a.p.p + (PT ? (int64_t)(c + n) * a.p.stride + j : j * a.p.stride + c));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+#pragma unroll
+      for (int t = 0; t < NT; t++) {
+        word4 f;
+        if constexpr (PT) f = turn<T>(p[u], t);
+        else f = p[u][t];
+        acc[t] = few_mul<T>(f, x[u], acc[t]);
+        if (a.parts == 2) acc[t] = few_mul<T>(f, x2[u], acc[t]);
+      }
+  }
+  // a lane holds row i of C: of fragment t rows 4 g + r of P's, columns 16 t + 4 g + r of the
+  // tile, or E (4 g + r) + t
+  float *mine = sums + (w * 16 + i) * F::PITCH;
+  if constexpr (!PT) {
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+      *reinterpret_cast<float4 *>(mine + 16 * t + 4 * g) = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+      for (int t = 0; t < NT; t += 4)
+        *reinterpret_cast<float4 *>(mine + E * (4 * g + r) + t) = make_float4(acc[t][r], acc[t + 1][r], acc[t + 2][r], acc[t + 3][r]);
+  }
+  __syncthreads();
+  DropKey key = {};
+  if (OUT == OUT_LAYER && a.layer.draw) key = drop_key(a.layer.drop);
+  for (int t = threadIdx.x; t < (int)a.I * (F::J / 8); t += F::THREADS) {
+    const int r = t / (F::J / 8), c = t % (F::J / 8) * 8;
+    const int64_t col = j0 + c;
+    if (col >= a.J) continue;
+    const int n = a.J - col < 8 ? (int)(a.J - col) : 8;
+    float bias[8], v[8] = {};
+    word4 res[sizeof(T) / 2];
+    if constexpr (OUT == OUT_LAYER) {
+      load_bias<T>(a.layer, col, n, bias);
+      load_res<T>(a.layer, r, col, n, res);
+    }
+#pragma unroll
+    for (int k = 0; k < F::WAVES; k++) {
+      float o[8];
+      load8<float>(sums + (k * 16 + r) * F::PITCH + c, 8, o);
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] += o[j];
+    }
+    emit8<T, OUT>(a, key, r, col, n, bias, res, v);
+  }
+}
+
 // ---- host ----------------------------------------------------------------------------
 
 // Whether every row is whole chunks at chunk addresses.
@@ -506,12 +646,36 @@ bool whole_chunks(const Operand &o, bool tr, int64_t R, int64_t K) {
   return ((uintptr_t)o.p & 15) == 0 && o.stride % E == 0 && (tr ? R : K) % E == 0;
 }
 
+template <typename T, int OUT>
+int join(const ProductArgs &a, hipStream_t stream) {
+  const int64_t items = a.I * ((a.J + 7) / 8);
+  auto blocks = [](int64_t n) { return dim3((unsigned)(n < 65536 ? n : 65536)); };
+  if (a.splits >= 16 && items < 65536)
+    hipLaunchKernelGGL((k_product_join<T, OUT, 16>), blocks((items + 15) / 16), dim3(LN_THREADS), 0, stream, a, a.splits);
+  else
+    hipLaunchKernelGGL((k_product_join<T, OUT, 1>), blocks((items + LN_THREADS - 1) / LN_THREADS), dim3(LN_THREADS), 0, stream, a,
+                       a.splits);
+  SPLAT_LAUNCH_CHECK();
+  return SPLAT_OK;
+}
+
 template <typename T, bool QT, bool PT, int OUT>
 int run_product(ProductArgs a, hipStream_t stream) {
   constexpr int KE = 64 / sizeof(T);
   const Cut cut = product_cut(a.I, a.J, a.K, a.parts, sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16);
-  const bool direct = a.K > 0 && whole_chunks<T>(a.q, QT, a.I, a.K) && whole_chunks<T>(a.p, PT, a.J, a.K);
   a.axis = (a.K + KE - 1) / KE;
+  if constexpr (!QT) {
+    if (a.I <= FEW && a.K > 0 && a.K % (16 / (int)sizeof(T)) == 0 && (!PT || a.J % (16 / (int)sizeof(T)) == 0)) {
+      const int splits = few_splits(a.J, a.K, PT, sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16);
+      a.per = (a.axis + splits - 1) / splits;
+      a.splits = (int)((a.axis + a.per - 1) / a.per);
+      const dim3 grid((unsigned)((a.J + Few<T, PT>::J - 1) / Few<T, PT>::J), (unsigned)a.splits);
+      hipLaunchKernelGGL((k_few<T, PT, OUT>), grid, dim3(Few<T, PT>::THREADS), 0, stream, a);
+      SPLAT_LAUNCH_CHECK();
+      return a.splits > 1 ? join<T, OUT>(a, stream) : SPLAT_OK;
+    }
+  }
+  const bool direct = a.K > 0 && whole_chunks<T>(a.q, QT, a.I, a.K) && whole_chunks<T>(a.p, PT, a.J, a.K);
   a.steps = a.axis * a.parts;
   a.per = (a.steps + cut.splits - 1) / cut.splits;
   a.splits = a.per > 0 ? (int)((a.steps + a.per - 1) / a.per) : 1;
@@ -530,16 +694,7 @@ int run_product(ProductArgs a, hipStream_t stream) {
   else
     hipLaunchKernelGGL((k_direct<T, 64, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
   SPLAT_LAUNCH_CHECK();
-  if (a.splits == 1) return SPLAT_OK;
-  const int64_t items = a.I * ((a.J + 7) / 8);
-  auto blocks = [](int64_t n) { return dim3((unsigned)(n < 65536 ? n : 65536)); };
-  if (a.splits >= 16 && items < 65536)
-    hipLaunchKernelGGL((k_product_join<T, OUT, 16>), blocks((items + 15) / 16), dim3(LN_THREADS), 0, stream, a, a.splits);
-  else
-    hipLaunchKernelGGL((k_product_join<T, OUT, 1>), blocks((items + LN_THREADS - 1) / LN_THREADS), dim3(LN_THREADS), 0, stream, a,
-                       a.splits);
-  SPLAT_LAUNCH_CHECK();
-  return SPLAT_OK;
+  return a.splits > 1 ? join<T, OUT>(a, stream) : SPLAT_OK;
 }
 
 template <typename T>
