@@ -35,7 +35,6 @@ struct TileShape {
   int i, j;
 };
 constexpr TileShape TILES[3] = {{256, 256}, {128, 128}, {64, 128}};
-constexpr int LOOSE_SIDE = 64;   // of arrays that are not whole, aligned chunks
 Cut product_cut(int64_t I, int64_t J, int64_t K, int parts, int dtype);
 
 // Products of few rows of Q are cut by columns of C (32, or where P lies transposed as many as
@@ -44,7 +43,7 @@ Cut product_cut(int64_t I, int64_t J, int64_t K, int parts, int dtype);
 constexpr int FEW = 16;
 static inline int few_splits(int64_t J, int64_t K, bool pt, int dtype) {
   const int64_t e = dtype == SPLAT_F32 ? 4 : 8, side = pt ? 16 * e : 32, groups = (J + side - 1) / side;
-  const int64_t most = (K + 4 * e - 1) / (4 * e) / 64, want = groups < 256 ? 256 / groups : 1, n = want < most ? want : most;
+  const int64_t most = (K + 4 * e - 1) / (4 * e) / 64, want = groups < 128 ? 256 / groups : 1, n = want < most ? want : most;
   return n < 1 ? 1 : (int)n;
 }
 static inline size_t product_part_bytes(int64_t I, int64_t J, int64_t K, int parts, int dtype) {

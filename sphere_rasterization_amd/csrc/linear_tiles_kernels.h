@@ -145,11 +145,40 @@ struct Tile {
 #pragma unroll
         for (int e = 0; e < 16; e++) acc[i][j][e] = 0.0f;
     word4 rq[SQ::LOADS], rp[SP::LOADS];
+    // Where a thread's chunks lie in the first stage. Rows beyond the array: any of its own.
+    // Whole chunks of the summed axis are read as they lie, and past a row's end where that is
+    // C's edge; the last two stages, in which the axis and the array end, value by value.
+    typedef const typename Loose<T, SQ::E>::type *ptr;
+    const T *sq[SQ::LOADS], *sp[SP::LOADS];
+    auto aim = [&](const Operand &o, bool tr, int64_t outer, int64_t R, int c) {
+      const int64_t r = outer < R ? outer : tr ? 0 : R - 1;
+      return (const T *)o.p + (tr ? c * o.stride + r : r * o.stride + c);
+    };
+#pragma unroll
+    for (int n = 0; n < SQ::LOADS; n++) {
+      int o, c;
+      SQ::place(tid + n * LN_THREADS, o, c);
+      sq[n] = aim(a.q, QT, i0 + o, a.I, c);
+    }
+#pragma unroll
+    for (int n = 0; n < SP::LOADS; n++) {
+      int o, c;
+      SP::place(tid + n * LN_THREADS, o, c);
+      sp[n] = aim(a.p, PT, j0 + o, a.J, c);
+    }
+    const int64_t dq = QT ? a.q.stride * SQ::KE : SQ::KE, dp = PT ? a.p.stride * SP::KE : SP::KE;
     auto fetch = [&](int64_t stage) {
       const bool second = stage >= a.axis;
       const int64_t k = second ? stage - a.axis : stage;
-      const Operand q = {(const char *)a.q.p + (second ? a.q.rest : 0), a.q.stride, 0};
-      const Operand p = {(const char *)a.p.p + (second ? a.p.rest : 0), a.p.stride, 0};
+      const int64_t rest_q = second ? a.q.rest : 0, rest_p = second ? a.p.rest : 0;
+      if (k < a.axis - 2) {
+#pragma unroll
+        for (int n = 0; n < SQ::LOADS; n++) rq[n] = *(ptr)((const char *)(sq[n] + k * dq) + rest_q);
+#pragma unroll
+        for (int n = 0; n < SP::LOADS; n++) rp[n] = *(ptr)((const char *)(sp[n] + k * dp) + rest_p);
+        return;
+      }
+      const Operand q = {(const char *)a.q.p + rest_q, a.q.stride, 0}, p = {(const char *)a.p.p + rest_p, a.p.stride, 0};
 #pragma unroll
       for (int n = 0; n < SQ::LOADS; n++) {
         int o, c;
@@ -679,12 +708,15 @@ int run_product(ProductArgs a, hipStream_t stream) {
   a.steps = a.axis * a.parts;
   a.per = (a.steps + cut.splits - 1) / cut.splits;
   a.splits = a.per > 0 ? (int)((a.steps + a.per - 1) / a.per) : 1;
-  const int side_i = !direct ? LOOSE_SIDE : TILES[cut.tile].i, side_j = !direct ? LOOSE_SIDE : TILES[cut.tile].j;
+  // arrays that are not whole, aligned chunks: tiles of 128 or 64 through registers
+  const int loose = cut.tile < 2 ? 128 : 64, side_i = !direct ? loose : TILES[cut.tile].i, side_j = !direct ? loose : TILES[cut.tile].j;
   a.ti = (a.I + side_i - 1) / side_i;
   a.tj = (a.J + side_j - 1) / side_j;
   const dim3 grid((unsigned)(a.ti * a.tj), (unsigned)a.splits);
-  if (!direct)
-    hipLaunchKernelGGL((k_product<T, LOOSE_SIDE, LOOSE_SIDE, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
+  if (!direct && loose == 128)
+    hipLaunchKernelGGL((k_product<T, 128, 128, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
+  else if (!direct)
+    hipLaunchKernelGGL((k_product<T, 64, 64, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
   else if (cut.tile == 0)
     // transposing reads bring half as much a cycle: with both operands transposed four waves of
     // 128 x 128, which read least, beat eight (4096 by 4096 by 4096 bf16, forward and backward: 381 us, 407 with eight)
