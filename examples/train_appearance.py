@@ -1,11 +1,12 @@
 """Train a scene's appearance: a feature table that primitives share, and a shading network.
 
 One step reads every primitive's features from the table, renders them to a feature
-image, shades it by a small channels-last network and compares the colours with a target;
-the gradients run back through all of it, and the network's matrices move by
-orthogonalised momentum.
+image, shades it by a small channels-last network (a dense layer, the normalisation, a
+hidden layer with dropout around which its input is passed, the colours) and compares the
+colours with a target; the gradients run back through all of it, and the network's matrices
+move by orthogonalised momentum.
 
-    python examples/train_appearance.py --steps 50
+    python examples/train_appearance.py --steps 50 --dropout 0.1
 
 The target is the same geometry with colours of its own, so the loss can fall far but not
 to zero: 256 table entries stand for all primitives.
@@ -36,7 +37,15 @@ def target_image(scene, palette, ids, device):
     return rz.view_images()[0].permute(1, 2, 0).contiguous()
 
 
-def train(steps=50, n=30_000, width=320, height=192, lr=0.02, seed=0, device="cuda:0", log=None):
+def shade(img, w1, gain, bias, wh, bh, w2, bias2, dropout=0.0, rng=None):
+    """Colours [..., 3] of a feature image [1, pixels, channels]."""
+    h = A.linear(img, w1)
+    h = A.group_norm(h, GROUPS, gain, bias, act="silu")
+    h = A.linear(h, wh, bh, act="silu", residual=h, p=dropout, rng=rng)
+    return A.linear(h, w2, bias2)
+
+
+def train(steps=50, n=30_000, width=320, height=192, lr=0.02, seed=0, device="cuda:0", log=None, dropout=0.0):
     """Loss of each step."""
     rng = np.random.default_rng(seed)
     torch.manual_seed(seed)
@@ -51,18 +60,19 @@ def train(steps=50, n=30_000, width=320, height=192, lr=0.02, seed=0, device="cu
 
     table = parameter(ENTRIES, CHANNELS, scale=0.5)
     w1, w2 = parameter(CHANNELS, HIDDEN, scale=CHANNELS ** -0.5), parameter(HIDDEN, 3, scale=0.1)
+    wh = parameter(HIDDEN, HIDDEN, scale=0.1 * HIDDEN ** -0.5)
     gain = torch.ones(HIDDEN, device=device, requires_grad=True)
-    bias, bias2 = torch.zeros(HIDDEN, device=device, requires_grad=True), torch.zeros(3, device=device, requires_grad=True)
-    matrices, others = [w1, w2], [table, gain, bias, bias2]
+    bias, bh, bias2 = (torch.zeros(k, device=device, requires_grad=True) for k in (HIDDEN, HIDDEN, 3))
+    matrices, others = [w1, wh, w2], [table, gain, bias, bh, bias2]
     momentum = [torch.zeros_like(m) for m in matrices]
     adam = torch.optim.Adam(others, lr=lr)
     losses = []
     for step in range(steps):
         feat = A.lookup(table, ids, scale=CHANNELS ** -0.5)
         img = render(rz, feat=feat)                                  # [channels][height][width], flat
-        h = rz.view_images(img)[0].permute(1, 2, 0)[None]            # channels last
-        h = A.group_norm(h.reshape(1, height * width, CHANNELS) @ w1, GROUPS, gain, bias, act="silu")
-        rgb = (h @ w2 + bias2).view(height, width, 3)
+        img = rz.view_images(img)[0].permute(1, 2, 0)                # channels last
+        rgb = shade(img.reshape(1, height * width, CHANNELS), w1, gain, bias, wh, bh, w2, bias2, dropout, (seed, step))
+        rgb = rgb.view(height, width, 3)
         loss = (rgb - target).square().mean()
         adam.zero_grad()
         for m in matrices:
@@ -84,5 +94,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--primitives", type=int, default=30_000)
+    ap.add_argument("--dropout", type=float, default=0.0, help="probability in the hidden layer")
     a = ap.parse_args()
-    train(a.steps, n=a.primitives, log=lambda s: print(s, flush=True))
+    train(a.steps, n=a.primitives, dropout=a.dropout, log=lambda s: print(s, flush=True))

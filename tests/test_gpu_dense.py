@@ -528,3 +528,123 @@ def test_refusals(dev):
             call()
     with pytest.raises(L.SplatError):
         A.linear(torch.zeros(1, (1 << 20) + 1, device=dev), torch.zeros((1 << 20) + 1, 1, device=dev))
+
+
+def test_the_example_runs_and_its_gradients_fit(dev):
+    """The example's shading network: dense layers, normalisation and dropout together, against
+    torch's operations and gradients in 64 bits. And its loop, with dropout, for running."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_appearance.py")
+    spec = importlib.util.spec_from_file_location("train_appearance", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    torch.manual_seed(8)
+    leaves = [torch.randn(*s, device=dev) for s in ((1, 777, 16), (16, 32), (32,), (32,), (32, 32), (32,), (32, 3), (3,))]
+    wide = [t.double().requires_grad_() for t in leaves]
+    leaves = [t.requires_grad_() for t in leaves]
+    dy = torch.randn(1, 777, 3, device=dev)
+    got = ex.shade(*leaves, 0.25, (5, 6))
+
+    def ref(img, w1, gain, bias, wh, bh, w2, bias2):
+        h = torch.nn.functional.group_norm((img @ w1).transpose(1, 2), ex.GROUPS, gain, bias).transpose(1, 2)
+        h = torch.nn.functional.silu(h)
+        keep = torch.from_numpy(D.kept((1, 777, 32), 0.25, 5, 6)).to(dev)
+        h = h + torch.nn.functional.silu(h @ wh + bh) * keep / 0.75
+        return h @ w2 + bias2
+
+    want = ref(*wide)
+    # some ten products and sums in fp32, each within a few tens of roundings in the norm
+    assert float((got.double() - want).norm() / want.norm()) <= 1e-5
+    got.backward(dy)
+    want.backward(dy.double())
+    for t, u in zip(leaves, wide):
+        assert float((t.grad.double() - u.grad).norm() / u.grad.norm()) <= 2e-5
+    assert all(np.isfinite(ex.train(steps=3, n=2000, width=64, height=48, dropout=0.1)))
+
+
+EDGES = [  # rows, in, out: around the kernels' own sizes
+    (16, 64, 64), (15, 65, 64), (17, 64, 65), (16, 72, 136), (1, 32, 8), (1, 8, 8), (2, 4, 4), (3, 3, 3), (1, 3, 2),
+    (8, 64, 1), (9, 1, 64), (64, 33, 33), (16, 4096, 40), (3, 2056, 24), (16, 520, 8200), (255, 128, 256), (256, 32, 256),
+    (257, 40, 264), (128, 1000, 128), (129, 96, 384), (513, 72, 72), (2048, 80, 80), (300, 65, 4), (1000, 5000, 70), (70, 67, 3001)]
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("order", ["io", "oi"])
+@pytest.mark.parametrize("m,k,n", EDGES)
+def test_linear_at_its_kernels_edges(dev, m, k, n, order, dt):
+    """Layers around the sizes at which another kernel, tile or split takes over. The activation is
+    none, so that every bound is one of sums and of one rounding."""
+    from sphere_rasterization_amd import appearance as A
+    rng = np.random.default_rng(m + k + n)
+    x, w, b, r, dy = _layer(rng, m, k, n, dt, "same", True, order, dev)
+    xn, wn, bn, rn, dn = (_np(t) for t in (x, w, b, r, dy))
+    f = D.linear(xn, wn, bn, "none", rn)
+    y, pre = A.linear_forward(x, w, b, residual=r)
+    assert pre is None
+    top = lambda v: RO[dt] * np.abs(v) + TINY[dt]
+    _check(y, f["y"], _bounds(xn, wn, bn, f["z"], dt) + 2 * U * (np.abs(f["y"]) + np.abs(rn)) + top(f["y"]), "y")
+    dx, dw, db = A.linear_backward(dy, x, w, b)
+    g = D.linear_backward(dn, xn, wn, bn)
+    _check(dx, g["dx"], 2 * (n + 8) * U * (np.abs(dn) @ np.abs(wn).T) + top(g["dx"]), "dx")
+    _check(dw, g["dw"], 2 * (m + 8) * U * (np.abs(xn).T @ np.abs(dn)) + top(g["dw"]), "dw")
+    _check(db, g["db"], (m + 8) * U * np.abs(dn).sum(0) + top(g["db"]), "db")
+    # with the activation, its gradient against the same formula on the kernels' own z in 64 bits
+    y2, pre = A.linear_forward(x, w, b, act="silu", p=0.3, rng=(1, 2))
+    grads = A.linear_backward(dy, x, w, b, act="silu", pre=pre, p=0.3, rng=(1, 2))
+    g = D.linear_backward(dn, xn, wn, bn, "silu", 0.3, 1, 2)
+    for got, want, what in zip(grads, (g["dx"], g["dw"], g["db"]), ("dx", "dw", "db")):
+        size = np.linalg.norm(want)
+        # rounded once, from terms that carry at most one rounding of z and one of dz (each below RO
+        # of the terms, whose norm is at most the square root of their number times that of the sum's)
+        assert np.linalg.norm(_np(got) - want) <= (2.5 * RO[dt] + 2e-5) * max(size, np.linalg.norm(g["dz"])) + TINY[dt] * want.size ** 0.5, what
+
+
+def test_two_calls_of_one_layer_at_once(dev):
+    """Forward and backward of the same arrays on two streams: each has a workspace of its own."""
+    from sphere_rasterization_amd import appearance as A
+    torch.manual_seed(9)
+    for m, k, n in ((4000, 32, 32), (500, 400, 300), (3, 1000, 600)):
+        x, w, b, dy = (torch.randn(*s, device=dev) for s in ((m, k), (k, n), (n,), (m, n)))
+        run = lambda: (A.linear(x, w, b, act="gelu"),) + A.linear_backward(dy, x, w, b, act="gelu")
+        want = run()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        outs = []
+        for _ in range(5):
+            for s in streams:
+                with torch.cuda.stream(s):
+                    outs.append(run())
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(p, q) for p, q in zip(o, want))
+
+
+def test_c_calls_with_strides_and_given_outputs(dev):
+    """Outputs a stride apart, gradients of W in the other order than W, and the elements between
+    rows left as they were."""
+    import ctypes as C
+    from sphere_rasterization_amd import _lib as L
+    from sphere_rasterization_amd import appearance as A
+    torch.manual_seed(10)
+    stream = torch.cuda.current_stream().cuda_stream
+    for m, k, n in ((300, 24, 40), (200, 136, 264), (100, 65, 77), (5, 320, 96)):
+        x, w, b, dy = (torch.randn(*s, device=dev) for s in ((m, k), (k, n), (n,), (m, n)))
+        y = torch.full((m, n + 5), -7.0, device=dev)
+        dx = torch.full((m, k + 3), -7.0, device=dev)
+        dw = torch.full((n, k + 2), -7.0, device=dev)                  # by outputs
+        db = torch.empty(n, device=dev)
+        d = L.splat_dense(0, 0, L.SPLAT_ACT_SILU, k, n, m, k, n, 1, n, n + 5, k + 3, 1, k + 2, L.splat_drop())
+        nbytes = max(L.splat_linear_workspace_bytes(d, False), L.splat_linear_workspace_bytes(d, True), 16)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        L.splat_linear(d, x.data_ptr(), w.data_ptr(), b.data_ptr(), None, y.data_ptr(), None, ws.data_ptr(), nbytes, stream)
+        ref = A.linear(x, w, b, act="silu")
+        assert torch.equal(y[:, :n], ref) and bool((y[:, n:] == -7.0).all())
+        d.y_stride = n
+        nbytes = max(L.splat_linear_workspace_bytes(d, True), 16)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        L.splat_linear_bwd(d, dy.data_ptr(), x.data_ptr(), w.data_ptr(), b.data_ptr(), None, dx.data_ptr(), dw.data_ptr(),
+                           db.data_ptr(), ws.data_ptr(), nbytes, stream)
+        gx, gw, gb = A.linear_backward(dy, x, w, b, act="silu")
+        assert torch.equal(dx[:, :k], gx) and bool((dx[:, k:] == -7.0).all()) and torch.equal(db, gb)
+        assert float((dw[:, :k].t() - gw).norm() / gw.norm()) <= 1e-5 and bool((dw[:, k:] == -7.0).all())
