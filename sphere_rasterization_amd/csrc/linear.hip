@@ -127,11 +127,13 @@ int64_t slope_chunks(int64_t M, int64_t N) {
 bool w_by_out(int64_t si, int64_t so) { return so == 1 && si != 1; }
 
 // Parts of dz. One rounding of it adds as much error to dx and dW as their own rounding: where
-// values are few, with luck more, and the products cost little; where they are many, the two
-// errors together stay at sqrt 2 of the one, and a second part would take twice the time.
+// dz or a gradient has few values, with luck more, and the products cost little. Where all are
+// many the two errors (and that of z, read back rounded) stay at 1.45 to 1.46 of the one, and a
+// second part would take up to twice the time (8191 x 1024 to 4096 bf16: 144 us of products).
 int parts_of(const splat_dense *d) {
   const bool shaped = d->act != SPLAT_ACT_NONE || d->drop.p > 0.0;
-  return shaped && d->dtype != SPLAT_F32 && d->rows * d->out < (1 << 20) ? 2 : 1;
+  const bool many = d->rows * d->out >= (1 << 20) && d->rows * d->in >= (1 << 18) && (int64_t)d->in * d->out >= (1 << 18);
+  return shaped && d->dtype != SPLAT_F32 && !many ? 2 : 1;
 }
 
 struct Plan {

@@ -535,7 +535,7 @@ __global__ __launch_bounds__(LN_THREADS) void k_product_join(ProductArgs a, int 
 //   P by j (PT): a lane reads E neighbours of a row of P, for as many rows as a chunk holds
 //   values, and turns them around in registers: fragment e stands for columns E i + e. (fp32
 //   needs no turning: an instruction takes one value a lane.)
-// 1 x 2048 by 2048 x 8192 bf16: see FEWTIME.
+// 1 x 2048 by 2048 x 8192 bf16: 8.3 us, 4.0 TB/s; by 64 x 64 tiles and a join of splits 15.
 template <typename T, bool PT>
 struct Few {
   static constexpr int E = 16 / sizeof(T), KE = 64 / sizeof(T);
