@@ -9,6 +9,11 @@
 // dealt to the fragments so that the eight are neighbours. That is what one 16-byte access
 // of 16-bit values and one draw of the generator take, and the layout in which dz is the
 // operand of dx = dz W^T. Only dW, summed over rows, turns x and dz around, through LDS.
+//
+// Measured on one MI355X. 2M rows of 32 to 64 fp16 with silu: 80 us, 5.0 TB/s. 1M rows of 32
+// to 32 fp32 with silu and residual: forward 78 us, 5.2 TB/s, backward 97 and a join of 5, 4.2.
+// 5.5M rows of 24 to 32 bf16 with gelu and dropout: forward 183 to 200 us, backward 273 to
+// 302, both bound by gelu's and the generator's instructions rather than by memory (103 and 147).
 #pragma once
 #include "linear_rows.h"
 

@@ -417,6 +417,11 @@ __device__ __forceinline__ int64_t by_xcd(int64_t b, int64_t n) {
   return x * each + (x < more ? x : more) + (b >> 3);
 }
 
+// 8192 x 4096 by 4096 x 4096 bf16: 244 to 255 us, 1.1 PFLOP/s with 256 x 256 tiles, whose fragment
+// reads and loads take LDS as long as the matrix cores take (a library product 211, 1.3);
+// with 128 x 128 tiles 320 to 340, with 64 x 128 390 to 440. 8191 x 1024 by 1024 x 4096 bf16 with
+// gelu: 92 to 99 us, a third of it the epilogue, in which the matrix cores rest. 4095 x 1536 by
+// 1536 x 1000 fp32: 107 to 122 us, 103 to 117 TFLOP/s of the 154 of a large library product.
 template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT, int OUT>
 __global__ __launch_bounds__(WI * WJ * WAVE, TI * TJ > 128 * 128 * WI * WJ / 2 ? 1 : 2) void k_direct(ProductArgs a) {
   typedef Direct<T, TI, TJ, WI, WJ, NST, QT, PT> D;
