@@ -133,7 +133,7 @@ bool w_by_out(int64_t si, int64_t so) { return so == 1 && si != 1; }
 // second part would take up to twice the time (8191 x 1024 to 4096 bf16: 144 us of products).
 int parts_of(const splat_dense *d) {
   const bool shaped = d->act != SPLAT_ACT_NONE || d->drop.p > 0.0;
-  const bool many = d->rows * d->out >= (1 << 20) && d->rows * d->in >= (1 << 18) && (int64_t)d->in * d->out >= (1 << 18);
+  const bool many = d->rows * d->out >= (1 << 20) && d->rows * d->in >= (1 << 18) && (int64_t)d->in * d->out >= (1 << 15);
   return shaped && d->dtype != SPLAT_F32 && !many ? 2 : 1;
 }
 
