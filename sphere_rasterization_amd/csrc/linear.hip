@@ -325,7 +325,7 @@ size_t linear_workspace_bytes(const splat_dense *d, bool bwd) {
 int launch_linear(const splat_dense *d, const void *x, const void *w, const void *bias, const void *res, void *y,
                   void *pre, void *ws, hipStream_t stream) {
   LayerArgs l = {bias, res, pre, d->residual_stride, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, drop_args(&d->drop)};
-  if (linear_by_rows(d) && !pre) {
+  if (linear_forward_by_rows(d)) {
     if (d->dtype == SPLAT_F32) return launch_linear_rows_f32(d, x, w, l, y, stream);
     if (d->dtype == SPLAT_F16) return launch_linear_rows_f16(d, x, w, l, y, stream);
     return launch_linear_rows_bf16(d, x, w, l, y, stream);

@@ -27,7 +27,8 @@ struct RowsArgs {
   const void *x, *w, *bias, *dy;
   void *y, *dx;
   int64_t M, xs, ys, dxs, wi, wo;    // rows; strides of x, y or dy, dx; of W along in and out
-  int K, N;
+  int K, N;                          // N: of a slice of at most 64 outputs, one for each blockIdx.y (forward)
+  int full;                          // outputs of the layer
   int want_x, want_w;                // want_w: dW or db
   float *part;                       // [workgroups][K + 1][N]: sums of dW, then of db
   LayerArgs layer;
@@ -71,8 +72,9 @@ template <typename T>
 struct RowEnd {
   const T *end;
   int len;
-  __device__ RowEnd(const void *p, int64_t rows, int64_t stride, int n)
-      : end((const T *)p + (rows - 1) * stride + n), len(n) {}
+  // n: of the row's values from p on that are read; all: that are there
+  __device__ RowEnd(const void *p, int64_t rows, int64_t stride, int n, int all)
+      : end((const T *)p + (rows - 1) * stride + all), len(n) {}
 };
 
 // Values at .. of the row, zeros beyond it.
@@ -265,11 +267,19 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 2 ? 4 : KP * NP < 4 ? 3 : 
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int64_t step = (int64_t)gridDim.x * (LN_THREADS / WAVE) * 16;
   int64_t base = ((int64_t)blockIdx.x * (LN_THREADS / WAVE) + (threadIdx.x >> 6)) * 16;
+  // this slice of the outputs
+  const int c0 = blockIdx.y * 64;
+  a.N = a.full - c0 < 64 ? a.full - c0 : 64;
+  a.w = (const T *)a.w + c0 * a.wo;
+  a.y = (T *)a.y + c0;
+  if (a.layer.res) a.layer.res = (const T *)a.layer.res + c0;
+  if (a.layer.pre) a.layer.pre = (T *)a.layer.pre + c0;
+  if (a.layer.bias) a.layer.bias = (const char *)a.layer.bias + (int64_t)c0 * (a.layer.bias_f32 ? 4 : sizeof(T));
   const T *px = (const T *)a.x + (base + i) * a.xs, *pr = (const T *)a.layer.res + (base + i) * a.layer.rs;
   T *py = (T *)a.y + (base + (BOUNCE ? 0 : i)) * a.ys;
   word4 nx[R::AHEAD][R::KC], nr[R::AHEAD][NP][R::DC];
   int64_t ahead = base + i;                      // the row that is loaded next
-  const RowEnd<T> ex(a.x, a.M, a.xs, a.K), er(a.layer.res, a.M, a.layer.rs, a.N);
+  const RowEnd<T> ex(a.x, a.M, a.xs, a.K, a.K), er(a.layer.res, a.M, a.layer.rs, a.N, a.full - c0);
   auto load = [&](int d) {
     R::load_x(px, ex, ahead < a.M, nx[d]);
     if (a.layer.res) R::load_out(pr, er, ahead < a.M, nr[d]);
@@ -307,9 +317,10 @@ __global__ __launch_bounds__(LN_THREADS, sizeof(T) == 2 ? 4 : KP * NP < 4 ? 3 : 
         if (in && n[p] > 0) {
 #pragma unroll
           for (int j = 0; j < 8; j++) v[j] += b[p][j];
+          if (a.layer.pre) store8<T>((T *)a.layer.pre + (base + i) * a.full + 32 * p + 8 * g, EASY ? 8 : n[p], v);
           if constexpr (ACT == ANY_ACT) activate<T>(v, a.layer.act);
           else activate8<T, ACT>(v);
-          if (DRAW) drop8<EASY>(v, (base + i) * a.N + 32 * p + 8 * g, a.layer.drop, key);
+          if (DRAW) drop8<EASY>(v, (base + i) * a.full + c0 + 32 * p + 8 * g, a.layer.drop, key);
           if (a.layer.res) {
             float q[8];
             R::widen(r[p], q);
@@ -348,7 +359,7 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
   T *po = (T *)a.dx + (base + i) * a.dxs;
   word4 nx[R::AHEAD][R::KC], nd[R::AHEAD][NP][R::DC];
   int64_t ahead = base + i;
-  const RowEnd<T> ex(a.x, a.M, a.xs, a.K), ed(a.dy, a.M, a.ys, a.N);
+  const RowEnd<T> ex(a.x, a.M, a.xs, a.K, a.K), ed(a.dy, a.M, a.ys, a.N, a.N);
   auto load = [&](int d) {
     R::load_x(px, ex, ahead < a.M, nx[d]);
     R::load_out(pd, ed, ahead < a.M, nd[d]);
@@ -593,14 +604,14 @@ int launch_one(const RowsArgs &a, bool bwd, int most, hipStream_t s) {
     return groups;
   }
   static const int fit = resident(k_rows<T, KP, NP, ACT, DRAW, EASY>);
-  const int groups = need < fit ? (int)need : fit;
-  hipLaunchKernelGGL((k_rows<T, KP, NP, ACT, DRAW, EASY>), dim3((unsigned)groups), dim3(LN_THREADS), 0, s, a);
+  const int slices = (a.full + 63) / 64, share = (fit + slices - 1) / slices, groups = need < share ? (int)need : share;
+  hipLaunchKernelGGL((k_rows<T, KP, NP, ACT, DRAW, EASY>), dim3((unsigned)groups, (unsigned)slices), dim3(LN_THREADS), 0, s, a);
   return groups;
 }
 template <typename T, int KP, int NP, bool DRAW>
 int by_act(const RowsArgs &a, bool bwd, int most, hipStream_t s) {
   // rows of whole chunks and of whole draws; for others one kernel serves all activations
-  const bool easy = a.K % (16 / (int)sizeof(T)) == 0 && a.N % 8 == 0;
+  const bool easy = a.K % (16 / (int)sizeof(T)) == 0 && a.full % 8 == 0;
   if (!easy) return launch_one<T, KP, NP, ANY_ACT, DRAW, false>(a, bwd, most, s);
   switch (a.layer.act) {
     case SPLAT_ACT_RELU: return launch_one<T, KP, NP, SPLAT_ACT_RELU, DRAW, true>(a, bwd, most, s);
@@ -628,7 +639,7 @@ RowsArgs rows_args(const splat_dense *d, const void *x, const void *w) {
   a.w = w;
   a.M = d->rows;
   a.K = d->in;
-  a.N = d->out;
+  a.N = a.full = d->out;
   a.xs = d->x_stride;
   a.ys = d->y_stride;
   a.dxs = d->dx_stride;

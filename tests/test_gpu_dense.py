@@ -648,3 +648,36 @@ def test_c_calls_with_strides_and_given_outputs(dev):
         gx, gw, gb = A.linear_backward(dy, x, w, b, act="silu")
         assert torch.equal(dx[:, :k], gx) and bool((dx[:, k:] == -7.0).all()) and torch.equal(db, gb)
         assert float((dw[:, :k].t() - gw).norm() / gw.norm()) <= 1e-5 and bool((dw[:, k:] == -7.0).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,k,n", [(65536, 24, 72), (70000, 33, 100), (66001, 64, 256), (66500, 7, 129), (65535, 48, 65)])
+def test_many_rows_of_more_outputs(dev, m, k, n, dt):
+    """Many rows of few inputs and 65 to 256 outputs, which are taken in slices of them, with and
+    without what goes with the product; dropout over them is that of dropout alone."""
+    from sphere_rasterization_amd import appearance as A
+    rng = np.random.default_rng(n)
+    x, w, b, r, dy = _layer(rng, m, k, n, dt, "same", True, "io", dev)
+    y, pre = A.linear_forward(x, w, b, act="gelu", residual=r)
+    xn, wn, bn, rn = _np(x), _np(w), _np(b), _np(r)
+    f = D.linear(xn, wn, bn, "gelu", rn)
+    e_z = _bounds(xn, wn, bn, f["z"], dt)
+    _check(pre, f["z"], e_z + RO[dt] * np.abs(f["z"]) + TINY[dt], "pre")
+    e_y = 1.13 * e_z + _e_act(f["z"], "gelu", dt) + 4 * U * np.abs(f["z"]) + 2 * U * np.abs(rn) + 0.2 * RO[dt] * np.abs(f["y"] - rn)
+    _check(y, f["y"], e_y + (RO[dt] + 2 * U) * np.abs(f["y"]) + TINY[dt], "y")
+    assert torch.equal(y, A.linear(x, w, b, act="gelu", residual=r))
+    assert torch.equal(y, A.linear(x, w.t().contiguous().t(), b, act="gelu", residual=r))
+    plain = A.linear(x, w)
+    _check(plain, xn @ wn, _bounds(xn, wn, None, None, dt) + RO[dt] * np.abs(xn @ wn) + TINY[dt], "product")
+    got = A.linear(x, w, p=0.2, rng=(SEED, OFFSET))
+    # another kernel's sums, so that a kept value may round to zero in one and not in the other
+    keep = A.dropout(torch.ones_like(plain), 0.2, (SEED, OFFSET)) != 0
+    assert bool((got[~keep] == 0).all())
+    want = plain.float()[keep] * 1.25
+    assert float((got.float()[keep] - want).norm()) <= (3 * RO[dt] + 1e-6) * float(want.norm())
+    dx, dw, db = A.linear_backward(dy, x, w, b, act="gelu", pre=pre)
+    wide = [t.double().requires_grad_() for t in (x, w, b)]
+    torch.nn.functional.gelu(wide[0] @ wide[1] + wide[2]).backward(dy.double())
+    # rounded once, with z and dz each rounded once below it; fp32: sums of m terms in parts
+    for g, t, what in zip((dx, dw, db), wide, ("dx", "dw", "db")):
+        assert float((g.double() - t.grad).norm() / t.grad.norm()) <= 3 * RO[dt] + 1e-5, what
