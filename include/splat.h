@@ -434,7 +434,8 @@ int splat_linear(const splat_dense *dense, const void *x, const void *w, const v
 /* Gradients w.r.t. x, W and b given d_y (overwritten; a NULL output is not computed):
  * dz = drop'(d_y) act'(z), d_x = dz W^T, d_W = x^T dz, d_b = column sums of dz; the
  * residual's gradient is d_y itself. pre: what the forward wrote, or NULL: z is then
- * computed anew from x, W and b. drop has to be the forward's, the state's words too.
+ * computed anew from x, W and b. act' of an infinite z is its limit, 0 or 1 (z of fp16 layers
+ * may pass 65504 and then reads back infinite). drop has to be the forward's, the state's words too.
  * 16-bit layers with an activation or dropout multiply dz in two parts of dtype, or, with
  * many rows and large W, rounded to dtype; in two parts an infinite x or W may give NaN in
  * the place of an infinite gradient. */

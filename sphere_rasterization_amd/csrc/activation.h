@@ -109,27 +109,35 @@ __device__ __forceinline__ float act_of(float z) {
   return z;
 }
 
-template <int ACT, bool EXACT>
+// LIMIT: an infinite z gets the slope's limit, 0 or 1, where the formula is 0 times infinity (a z
+// read back from 16 bits may have become infinite there). The factor is held to a range beyond
+// which the other one is zero, in one instruction that keeps a finite z's result; a NaN stays one
+// by the other factor.
+template <bool LIMIT>
+__device__ __forceinline__ float slope_factor(float z) {
+  return LIMIT ? __builtin_amdgcn_fmed3f(z, -150.0f, 150.0f) : z;
+}
+template <int ACT, bool EXACT, bool LIMIT = false>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == SPLAT_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if constexpr (ACT == SPLAT_ACT_SILU) {
     if constexpr (EXACT) {
       float t, rest;
       logistic_f32(z, t, rest);
-      return t * __builtin_fmaf(z, rest, 1.0f);
+      return t * __builtin_fmaf(slope_factor<LIMIT>(z), rest, 1.0f);
     }
     const float t = fast_rcp(1.0f + __expf(-z));
-    return t * __builtin_fmaf(z, 1.0f - t, 1.0f);
+    return t * __builtin_fmaf(slope_factor<LIMIT>(z), 1.0f - t, 1.0f);
   }
   if constexpr (ACT == SPLAT_ACT_GELU) {
     float a, density;
     if constexpr (EXACT) {
       normal_f32(z, a, density);
-      return __builtin_fmaf(z, density, a);
+      return __builtin_fmaf(slope_factor<LIMIT>(z), density, a);
     }
     density = normal_density(z);
     a = normal_tail<true>(z, density);
-    return __builtin_fmaf(z, density, z < 0.0f ? a : 1.0f - a);
+    return __builtin_fmaf(slope_factor<LIMIT>(z), density, z < 0.0f ? a : 1.0f - a);
   }
   return 1.0f;
 }

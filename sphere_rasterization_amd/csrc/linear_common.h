@@ -30,7 +30,7 @@ __device__ __forceinline__ void activate8(float (&v)[8]) {
 template <typename T, int ACT>
 __device__ __forceinline__ void slope8(float (&d)[8], const float (&z)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; j++) d[j] *= act_slope<ACT, sizeof(T) == 4>(z[j]);
+  for (int j = 0; j < 8; j++) d[j] *= act_slope<ACT, sizeof(T) == 4, true>(z[j]);
 }
 constexpr int ANY_ACT = -1;      // the activation is the launch's
 template <typename T>
