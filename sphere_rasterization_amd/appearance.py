@@ -408,8 +408,8 @@ def linear_backward(d_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bi
     out. The residual's gradient is d_y. pre: what `linear_forward` returned, or None (it is
     then computed anew). rng has to draw what the forward's drew: a state's words are read
     again. d_weight is laid out as weight is; d_bias has the type of bias (of x without one).
-    With 16-bit types, an activation or dropout, and an infinite x or weight, a gradient may
-    be NaN where the formula has an infinity."""
+    With 16-bit types, silu or gelu, and an infinite x or weight, a gradient may be NaN where
+    the formula has an infinity."""
     _no_tangents(d_y, x, weight, bias, pre)
     dt, k, n = _check_layer(x, weight, bias, act)
     drop = _drop(p, rng, x)

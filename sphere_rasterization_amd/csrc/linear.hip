@@ -19,6 +19,7 @@ struct SlopeArgs {
   float *sums;                   // [chunks][N], or NULL
   int64_t M, N, ys, chunk;       // rows per workgroup
   int act, draw;
+  float part;                    // of dz that is stored
   DropArgs drop;
 };
 
@@ -54,7 +55,12 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
         if (k >= m1) break;
         if (a.act != SPLAT_ACT_NONE) slope_times<T>(d[u], z[u], a.act);
         if (a.draw) drop8<false>(d[u], k * a.N + col, a.drop, key);
-        if (a.dz) store8<T>((T *)a.dz + k * a.N + col, n, d[u]);
+        if (a.dz) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; j++) v[j] = d[u][j] * a.part;
+          store8<T>((T *)a.dz + k * a.N + col, n, v);
+        }
         if constexpr (sizeof(T) == 2) {
           if (a.dz2) {
             word4 hi, lo;
@@ -85,7 +91,8 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
 
 // db: the chunks' sums, 32 columns by 8 slices of the chunks a workgroup, each in order.
 template <typename T>
-__global__ __launch_bounds__(LN_THREADS) void k_linear_bias(const float *sums, int64_t chunks, int64_t N, void *db, int f32) {
+__global__ __launch_bounds__(LN_THREADS) void k_linear_bias(const float *sums, int64_t chunks, int64_t N, void *db, int f32,
+                                                            float scale) {
   __shared__ float s[8][33];
   const int e = threadIdx.x & 31, l = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + e;
@@ -99,6 +106,7 @@ __global__ __launch_bounds__(LN_THREADS) void k_linear_bias(const float *sums, i
   if (l > 0 || col >= N) return;
 #pragma unroll
   for (int k = 1; k < 8; k++) v += s[k][e];
+  v *= scale;
   if (f32) ((float *)db)[col] = v;
   else ((T *)db)[col] = (T)v;
 }
@@ -127,14 +135,13 @@ int64_t slope_chunks(int64_t M, int64_t N) {
 // W as [in][out], `out` contiguous, or its transpose.
 bool w_by_out(int64_t si, int64_t so) { return so == 1 && si != 1; }
 
-// Parts of dz. One rounding of it adds as much error to dx and dW as their own rounding: where
+// Parts of dz with silu's or gelu's slope. One rounding of it adds as much error to dx and dW as their own rounding: where
 // dz or a gradient has few values, with luck more, and the products cost little. Where all are
 // many the two errors (and that of z, read back rounded) stay at 1.45 to 1.46 of the one, and a
 // second part would take up to twice the time (8191 x 1024 to 4096 bf16: 144 us of products).
 int parts_of(const splat_dense *d) {
-  const bool shaped = d->act != SPLAT_ACT_NONE || d->drop.p > 0.0;
   const bool many = d->rows * d->out >= (1 << 20) && d->rows * d->in >= (1 << 18) && (int64_t)d->in * d->out >= (1 << 15);
-  return shaped && d->dtype != SPLAT_F32 && !many ? 2 : 1;
+  return !slope_of_bits(d->act) && d->dtype != SPLAT_F32 && !many ? 2 : 1;
 }
 
 struct Plan {
@@ -208,6 +215,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
   float *sums = (float *)(at + p.pre + p.dz), *part = (float *)(at + p.pre + p.dz + p.sums);
   const bool draw = d->drop.p > 0.0, shaped = d->act != SPLAT_ACT_NONE || draw;
   const int parts = parts_of(d);
+  const float drop_scale = drop_args(&d->drop).scale, scale = drop_scale / dz_part(d);
   const int64_t rest = parts == 2 ? (int64_t)(p.dz / 2) : 0;
   if (d->act != SPLAT_ACT_NONE && !pre) {
     LayerArgs l = {};
@@ -228,7 +236,8 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     s.ys = d->y_stride;
     s.act = d->act;
     s.draw = draw;
-    s.drop = drop_args(&d->drop);
+    s.part = dz_part(d);
+    s.drop = mask_args(&d->drop);
     const int64_t chunks = slope_chunks(M, N);
     s.chunk = (M + chunks - 1) / chunks;
     const dim3 grid((unsigned)((N + SL_COLS - 1) / SL_COLS), (unsigned)((M + s.chunk - 1) / s.chunk));
@@ -236,7 +245,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     SPLAT_LAUNCH_CHECK();
     if (db) {
       hipLaunchKernelGGL(k_linear_bias<T>, dim3((unsigned)((N + 31) / 32)), dim3(LN_THREADS), 0, stream,
-                         (const float *)sums, (int64_t)grid.y, N, db, d->bias_dtype == SPLAT_F32);
+                         (const float *)sums, (int64_t)grid.y, N, db, (int)(d->bias_dtype == SPLAT_F32), drop_scale);
       SPLAT_LAUNCH_CHECK();
     }
   }
@@ -247,6 +256,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     a.J = K;
     a.K = N;
     a.parts = parts;
+    a.scale = scale;
     a.q = z;
     a.c = dx;
     a.cs = d->dx_stride;
@@ -264,6 +274,7 @@ int backward(const splat_dense *d, const void *dy, const void *x, const void *w,
     ProductArgs a = {};
     const Operand xo = {x, d->x_stride, 0};
     a.parts = parts;
+    a.scale = scale;
     a.I = by_out ? K : N;
     a.J = by_out ? N : K;
     a.K = M;
@@ -338,7 +349,7 @@ int launch_linear(const splat_dense *d, const void *x, const void *w, const void
 int launch_linear_bwd(const splat_dense *d, const void *dy, const void *x, const void *w, const void *bias, const void *pre,
                       void *dx, void *dw, void *db, void *ws, hipStream_t stream) {
   if (linear_by_rows(d) && d->rows > 0 && d->out > 0) {
-    const LayerArgs l = {bias, nullptr, nullptr, 0, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, drop_args(&d->drop)};
+    const LayerArgs l = {bias, nullptr, nullptr, 0, d->bias_dtype == SPLAT_F32, d->act, d->drop.p > 0.0, mask_args(&d->drop)};
     if (d->dtype == SPLAT_F32) return launch_linear_rows_bwd_f32(d, dy, x, w, l, dx, dw, db, ws, stream);
     if (d->dtype == SPLAT_F16) return launch_linear_rows_bwd_f16(d, dy, x, w, l, dx, dw, db, ws, stream);
     return launch_linear_rows_bwd_bf16(d, dy, x, w, l, dx, dw, db, ws, stream);

@@ -99,17 +99,35 @@ __device__ __forceinline__ void finish_layer(const LayerArgs &l, const DropKey &
   store8<T>(y + row * ys + col, n, v);
 }
 
-// dz in one or two parts of T: two of 16-bit types hold it to 16 bits and more, where one
-// would add as much error to dx and dW as their own rounding does. The second part of an
+// dz as it is multiplied: m act'(z) dy without dropout's factor, by which the sums are multiplied
+// in fp32, so that no finite dy leaves the type's range by it. Where the slope is 0 or 1 (none,
+// relu) that is dy or 0, exact in the arrays' type. silu's and gelu's slopes pass 1 (1.10 and 1.13):
+// of fp16 half of dz is taken, and twice the sums.
+__host__ __device__ __forceinline__ bool slope_of_bits(int act) { return act == SPLAT_ACT_NONE || act == SPLAT_ACT_RELU; }
+template <typename T>
+constexpr float DZ_PART = __is_same(T, f16_t) ? 0.5f : 1.0f;
+static inline float dz_part(const splat_dense *d) {
+  return d->dtype == SPLAT_F16 && !slope_of_bits(d->act) ? DZ_PART<f16_t> : 1.0f;
+}
+template <typename T>
+__device__ __forceinline__ word4 pack8(const float (&d)[8]) {
+  Pack<T, 8> t;
+#pragma unroll
+  for (int j = 0; j < 8; j++) t.v[j] = (T)d[j];
+  return __builtin_bit_cast(word4, t);
+}
+// dz of silu or gelu in one or two parts of T: two of 16-bit types hold it to 16 bits and more, where
+// one would add as much error to dx and dW as their own rounding does. The second part of an
 // infinity is zero.
 template <typename T>
 __device__ __forceinline__ void split8(const float (&d)[8], word4 &hi, word4 &lo) {
   Pack<T, 8> h, l;
 #pragma unroll
   for (int j = 0; j < 8; j++) {
-    h.v[j] = (T)d[j];
+    const float v = d[j] * DZ_PART<T>;
+    h.v[j] = (T)v;
     const float f = (float)h.v[j];
-    l.v[j] = (T)(fabsf(f) < INFINITY ? d[j] - f : 0.0f);
+    l.v[j] = (T)(fabsf(f) < INFINITY ? v - f : 0.0f);
   }
   hi = __builtin_bit_cast(word4, h);
   lo = __builtin_bit_cast(word4, l);

@@ -31,6 +31,7 @@ struct RowsArgs {
   int full;                          // outputs of the layer
   int want_x, want_w;                // want_w: dW or db
   float *part;                       // [workgroups][K + 1][N]: sums of dW, then of db
+  float scale;                       // of the sums of dx
   LayerArgs layer;
 };
 
@@ -354,7 +355,9 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, w = threadIdx.x >> 6;
   const int64_t step = (int64_t)gridDim.x * WAVES * 16;
   int64_t base = ((int64_t)blockIdx.x * WAVES + w) * 16;
-  const bool slope = ACT == ANY_ACT ? a.layer.act != SPLAT_ACT_NONE : ACT != SPLAT_ACT_NONE, shaped = slope || DRAW;
+  const int act = ACT == ANY_ACT ? a.layer.act : ACT;
+  const bool slope = act != SPLAT_ACT_NONE, shaped = slope || DRAW;
+  const bool two = sizeof(T) == 2 && !slope_of_bits(act);    // parts of dz
   const T *px = (const T *)a.x + (base + i) * a.xs, *pd = (const T *)a.dy + (base + i) * a.ys;
   T *po = (T *)a.dx + (base + i) * a.dxs;
   word4 nx[R::AHEAD][R::KC], nd[R::AHEAD][NP][R::DC];
@@ -420,7 +423,7 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
           R::product(f, x, p, z);
 #pragma unroll
           for (int j = 0; j < 8; j++) z[j] += b[p][j];
-          if constexpr (ACT == ANY_ACT) slope_times<T>(v, z, a.layer.act);
+          if constexpr (ACT == ANY_ACT) slope_times<T>(v, z, act);
           else slope8<T, ACT>(v, z);
         }
         if (DRAW) drop8<EASY>(v, (base + i) * a.N + 32 * p + 8 * g, a.layer.drop, key);
@@ -431,9 +434,11 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
 #pragma unroll
         for (int j = 0; j < 8; j++) db[p][j] += v[j];
         if constexpr (sizeof(T) == 2) {
-          if (shaped) {
+          if (two) {
             split8<T>(v, dz[p][0], dz2[p]);
             *reinterpret_cast<word4 *>(zt2 + i * R::ZP + p * 64 + g * 16) = dz2[p];
+          } else if (shaped) {
+            dz[p][0] = pack8<T>(v);
           } else {
             dz[p][0] = dy[p][0];
           }
@@ -459,7 +464,7 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
               hi = mul16<T>(ft[q][1][p][c], dz[p][c], hi);
             }
             if constexpr (sizeof(T) == 2) {
-              if (shaped) {
+              if (two) {
                 lo = mul16<T>(ft[q][0][p][0], dz2[p], lo);
                 hi = mul16<T>(ft[q][1][p][0], dz2[p], hi);
               }
@@ -467,7 +472,12 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
           }
           const int col = 32 * q + 8 * g, left = a.K - col;
           if (in && left > 0) {
-            const float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+              v[j] = lo[j] * a.scale;
+              v[4 + j] = hi[j] * a.scale;
+            }
             store8<T>(po + col, EASY && sizeof(T) == 2 || left > 8 ? 8 : left, v);
           }
         }
@@ -485,7 +495,7 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
 #pragma unroll
             for (int k = 0; k < 2 * KP; k++) dw[k][q] = mul16_short<T>(xf[k], zf, dw[k][q]);
           }
-          if (shaped) {
+          if (two) {
 #pragma unroll
             for (int q = 0; q < 2 * NP; q++) {
               const uint2 zf = R::turned(zt2, R::ZP, 16 * q);
@@ -554,10 +564,11 @@ __global__ __launch_bounds__(LN_THREADS, KP * NP > 1 ? 2 : 3) void k_rows_bwd(Ro
   }
 }
 
-// The workgroups' sums in order: 32 values by 32 slices of the workgroups per workgroup.
+// The workgroups' sums in order: 32 values by 32 slices of the workgroups per workgroup. scale and
+// db_scale: of the sums of dW and of db.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_rows_join(const float *part, int groups, int K, int N, T *dw, int64_t di, int64_t dn,
-                                                    void *db, int f32) {
+                                                    void *db, int f32, float scale, float db_scale) {
   __shared__ float s[32][33];
   const int e = threadIdx.x & 31, l = threadIdx.x >> 5, size = (K + 1) * N, at = blockIdx.x * 32 + e;
   float v = 0.0f;
@@ -573,8 +584,9 @@ __global__ __launch_bounds__(1024) void k_rows_join(const float *part, int group
   for (int k = 0; k < 32; k++) v += s[k][e];
   const int k = at / N, n = at - k * N;
   if (k < K) {
-    if (dw) dw[k * di + n * dn] = (T)v;
+    if (dw) dw[k * di + n * dn] = (T)(v * scale);
   } else if (db) {
+    v *= db_scale;
     if (f32) ((float *)db)[n] = v;
     else ((T *)db)[n] = (T)v;
   }
@@ -668,11 +680,13 @@ int run_rows_bwd(const splat_dense *d, const void *dy, const void *x, const void
   a.want_x = dx != nullptr;
   a.want_w = dw || db;
   a.part = (float *)ws;
+  const float drop_scale = drop_args(&d->drop).scale;
+  a.scale = drop_scale / dz_part(d);
   const int groups = by_size<T>(a, true, linear_rows_groups(d), stream);
   SPLAT_LAUNCH_CHECK();
   if (!a.want_w) return SPLAT_OK;
   hipLaunchKernelGGL(k_rows_join<T>, dim3((unsigned)(((a.K + 1) * a.N + 31) / 32)), dim3(1024), 0, stream, a.part, groups, a.K,
-                     a.N, (T *)dw, d->dw_in_stride, d->dw_out_stride, db, (int)(d->bias_dtype == SPLAT_F32));
+                     a.N, (T *)dw, d->dw_in_stride, d->dw_out_stride, db, (int)(d->bias_dtype == SPLAT_F32), a.scale, drop_scale);
   SPLAT_LAUNCH_CHECK();
   return SPLAT_OK;
 }

@@ -20,6 +20,7 @@ struct ProductArgs {
   int64_t axis, steps, per;      // stages of the summed axis, of all parts, and of one split
   void *c;
   int64_t cs;                    // row stride of C
+  float scale;                   // of the sums, where C is stored as it is
   float *part;                   // [splits][I][J] sums where the summed axis is split, else unused
   int splits;
   LayerArgs layer;

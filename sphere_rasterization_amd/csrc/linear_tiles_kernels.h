@@ -41,8 +41,11 @@ template <typename T, int OUT>
 __device__ __forceinline__ void emit8(const ProductArgs &a, const DropKey &key, int64_t row, int64_t col, int n,
                                       const float (&bias)[8], const word4 (&res)[sizeof(T) / 2], float (&v)[8]) {
   if (a.splits > 1) store8<float>(a.part + ((int64_t)blockIdx.y * a.I + row) * a.J + col, n, v);
-  else if constexpr (OUT == OUT_STORE) store8<T>((T *)a.c + row * a.cs + col, n, v);
-  else finish_layer<T>(a.layer, key, (T *)a.c, a.cs, a.J, row, col, n, bias, res, v);
+  else if constexpr (OUT == OUT_STORE) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) v[j] *= a.scale;
+    store8<T>((T *)a.c + row * a.cs + col, n, v);
+  } else finish_layer<T>(a.layer, key, (T *)a.c, a.cs, a.J, row, col, n, bias, res, v);
 }
 
 // One operand's share of a stage: TL of its outer places by 64 bytes of the summed axis

@@ -103,3 +103,9 @@ static inline DropArgs drop_args(const splat_drop *d) {
   a.scale = d->p < 1.0 ? (float)(1.0 / (1.0 - d->p)) : 0.0f;
   return a;
 }
+// The same choice without its factor.
+static inline DropArgs mask_args(const splat_drop *d) {
+  DropArgs a = drop_args(d);
+  a.scale = 1.0f;
+  return a;
+}

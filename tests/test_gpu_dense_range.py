@@ -107,3 +107,28 @@ def test_z_beyond_the_range_of_16_bits(dev, m, k, n, act, dt):
         y = A.linear(x, w, b, act=act)[row]
         assert bool((y[torch.from_numpy(z < -70000).to(dev)] == 0).all()) and bool(torch.isinf(y[torch.from_numpy(z > 70000).to(dev)]).all())
     _gradients(dt, act, 0.0, x, w, b, dy, (RO[dt], TINY[dt]), act)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("m,k,n", LAYERS)
+def test_large_gradients(dev, m, k, n, act, dt):
+    """dz beyond fp16's range, by dropout's factor and by slopes past 1, under gradients that are
+    inside it. dz is exact where the slope is 0 or 1, and held in two parts otherwise."""
+    rng = np.random.default_rng(m + k + n)
+    x, w = (_put(0.005 * rng.standard_normal(s), dt, dev) for s in ((m, k), (k, n)))
+    b = _put(1.5 * rng.standard_normal(n), "f32", dev)
+    dy = _put(rng.uniform(40000.0, 60000.0, (m, n)) * np.where(rng.random((m, n)) < 0.5, 1.0, -1.0), dt, dev)
+    rel = 0.0 if act in ("none", "relu") else RO[dt] ** 2
+    for p in (0.0, 0.5):
+        _gradients(dt, act, p, x, w, b, dy, (rel, TINY[dt]), f"{act} p {p}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("m,k,n", LAYERS)
+def test_gradients_of_nothing_kept(dev, m, k, n, dt):
+    from sphere_rasterization_amd import appearance as A
+    x, w, dy = (torch.randn(*s, device=dev).to(DT[dt]) for s in ((m, k), (k, n), (m, n)))
+    for act in ("none", "gelu"):
+        for g in A.linear_backward(dy, x, w, act=act, p=1.0, rng=(1, 2)):
+            assert torch.equal(g, torch.zeros_like(g))
