@@ -437,9 +437,10 @@ int splat_linear(const splat_dense *dense, const void *x, const void *w, const v
  * computed anew from x, W and b. act' of an infinite z is its limit, 0 or 1 (z of fp16 layers
  * may pass 65504 and then reads back infinite). drop has to be the forward's, the state's words too.
  * What is multiplied is dz (1 - p), the fp32 sums take the factor: a finite d_y overflows no
- * product. 16-bit layers multiply it in two parts of dtype with silu or gelu, or, with many rows
- * and large W, rounded to dtype (with none and relu it is exact in dtype); in two parts an infinite
- * x or W may give NaN in the place of an infinite gradient. */
+ * product. 16-bit layers multiply it in two parts of dtype with silu or gelu (fp16: to 2^-22 of
+ * itself and 2^-35; bf16: to 2^-16 of itself, but rounded to bf16 with many rows and large W);
+ * with none and relu it is exact in dtype. In two parts an infinite x or W may give NaN in the
+ * place of an infinite gradient. */
 int splat_linear_bwd(const splat_dense *dense, const void *d_y, const void *x, const void *w, const void *bias,
                      const void *pre, void *d_x, void *d_w, void *d_bias, void *workspace, size_t ws_bytes,
                      hipStream_t stream);

@@ -138,10 +138,11 @@ bool w_by_out(int64_t si, int64_t so) { return so == 1 && si != 1; }
 // Parts of dz with silu's or gelu's slope. One rounding of it adds as much error to dx and dW as their own rounding: where
 // dz or a gradient has few values, with luck more, and the products cost little. Where all are
 // many the two errors (and that of z, read back rounded) stay at 1.45 to 1.46 of the one, and a
-// second part would take up to twice the time (8191 x 1024 to 4096 bf16: 144 us of products).
+// second part would take up to twice the time (8191 x 1024 to 4096 bf16: 144 us of products). fp16
+// has not the range for one part.
 int parts_of(const splat_dense *d) {
   const bool many = d->rows * d->out >= (1 << 20) && d->rows * d->in >= (1 << 18) && (int64_t)d->in * d->out >= (1 << 15);
-  return !slope_of_bits(d->act) && d->dtype != SPLAT_F32 && !many ? 2 : 1;
+  return !slope_of_bits(d->act) && (d->dtype == SPLAT_F16 || (d->dtype == SPLAT_BF16 && !many)) ? 2 : 1;
 }
 
 struct Plan {

@@ -103,7 +103,7 @@ __device__ __forceinline__ void finish_layer(const LayerArgs &l, const DropKey &
 // in fp32, so that no finite dy leaves the type's range by it. Where the slope is 0 or 1 (none,
 // relu) that is dy or 0, exact in the arrays' type. silu's and gelu's slopes pass 1 (1.10 and 1.13):
 // of fp16 half of dz is taken, and twice the sums.
-__host__ __device__ __forceinline__ bool slope_of_bits(int act) { return act == SPLAT_ACT_NONE || act == SPLAT_ACT_RELU; }
+__host__ __device__ constexpr bool slope_of_bits(int act) { return act == SPLAT_ACT_NONE || act == SPLAT_ACT_RELU; }
 template <typename T>
 constexpr float DZ_PART = __is_same(T, f16_t) ? 0.5f : 1.0f;
 static inline float dz_part(const splat_dense *d) {
@@ -116,9 +116,13 @@ __device__ __forceinline__ word4 pack8(const float (&d)[8]) {
   for (int j = 0; j < 8; j++) t.v[j] = (T)d[j];
   return __builtin_bit_cast(word4, t);
 }
-// dz of silu or gelu in one or two parts of T: two of 16-bit types hold it to 16 bits and more, where
-// one would add as much error to dx and dW as their own rounding does. The second part of an
-// infinity is zero.
+// dz of silu or gelu in two parts of T, which hold it to twice the type's bits: one would add as much
+// error to dx and dW as their own rounding does. fp16 has no room below a small first part: its
+// second part is stored times 2^11, the most that cannot overflow, and summed apart, so that
+// the two hold dz to 2^-35 from fp16's smallest d_y on (without the factor d_y near 2^-22 was held to
+// 3 bits, and below 2^-25 dz was lost). The second part of an infinity is zero.
+template <typename T>
+constexpr float REST = __is_same(T, f16_t) ? 0x1p-11f : 1.0f;    // what the second part's sums are multiplied by
 template <typename T>
 __device__ __forceinline__ void split8(const float (&d)[8], word4 &hi, word4 &lo) {
   Pack<T, 8> h, l;
@@ -127,7 +131,7 @@ __device__ __forceinline__ void split8(const float (&d)[8], word4 &hi, word4 &lo
     const float v = d[j] * DZ_PART<T>;
     h.v[j] = (T)v;
     const float f = (float)h.v[j];
-    l.v[j] = (T)(fabsf(f) < INFINITY ? v - f : 0.0f);
+    l.v[j] = (T)(fabsf(f) < INFINITY ? (v - f) * (1.0f / REST<T>) : 0.0f);
   }
   hi = __builtin_bit_cast(word4, h);
   lo = __builtin_bit_cast(word4, l);

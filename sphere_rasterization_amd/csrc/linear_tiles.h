@@ -3,8 +3,9 @@
 #pragma once
 #include "linear_common.h"
 
-// What happens to C: stored, or one layer's bias, activation, dropout and residual first.
-enum { OUT_STORE, OUT_LAYER };
+// What happens to C: stored, or one layer's bias, activation, dropout and residual first, or stored
+// from an operand's two parts of which the second's sums are multiplied by REST (fp16).
+enum { OUT_STORE, OUT_LAYER, OUT_PARTS };
 
 struct Operand {
   const void *p;                 // [outer][c] with c contiguous, or [c][outer] (transposed)
@@ -16,7 +17,8 @@ struct ProductArgs {
   Operand q, p;
   int64_t I, J, K;               // rows and columns of C, length of the summed axis
   int64_t ti, tj;                // tiles along I and J
-  int parts;                     // 2: Q or P comes in two parts, and the summed axis is gone through twice
+  int parts;                     // 2: Q or P comes in two parts, and the summed axis is gone through twice, first with
+                                 // what the rounding lost
   int64_t axis, steps, per;      // stages of the summed axis, of all parts, and of one split
   void *c;
   int64_t cs;                    // row stride of C

@@ -41,7 +41,7 @@ template <typename T, int OUT>
 __device__ __forceinline__ void emit8(const ProductArgs &a, const DropKey &key, int64_t row, int64_t col, int n,
                                       const float (&bias)[8], const word4 (&res)[sizeof(T) / 2], float (&v)[8]) {
   if (a.splits > 1) store8<float>(a.part + ((int64_t)blockIdx.y * a.I + row) * a.J + col, n, v);
-  else if constexpr (OUT == OUT_STORE) {
+  else if constexpr (OUT != OUT_LAYER) {
 #pragma unroll
     for (int j = 0; j < 8; j++) v[j] *= a.scale;
     store8<T>((T *)a.c + row * a.cs + col, n, v);
@@ -128,7 +128,18 @@ struct Stage {
 };
 
 // TI x TJ tile of C by four waves, a quarter each.
-template <typename T, int TI, int TJ, bool QT, bool PT>
+// The sums of second parts, once all of them are in.
+template <typename T, int FI, int FJ>
+__device__ __forceinline__ void take_rest(float16v (&acc)[FI][FJ]) {
+#pragma unroll
+  for (int i = 0; i < FI; i++)
+#pragma unroll
+    for (int j = 0; j < FJ; j++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) acc[i][j][e] *= REST<T>;
+}
+
+template <typename T, int TI, int TJ, bool QT, bool PT, int OUT>
 struct Tile {
   typedef Stage<T, TI, QT> SQ;
   typedef Stage<T, TJ, PT> SP;
@@ -171,8 +182,8 @@ struct Tile {
     }
     const int64_t dq = QT ? a.q.stride * SQ::KE : SQ::KE, dp = PT ? a.p.stride * SP::KE : SP::KE;
     auto fetch = [&](int64_t stage) {
-      const bool second = stage >= a.axis;
-      const int64_t k = second ? stage - a.axis : stage;
+      const bool first = stage >= a.axis, second = a.parts == 2 && !first;
+      const int64_t k = first ? stage - a.axis : stage;
       const int64_t rest_q = second ? a.q.rest : 0, rest_p = second ? a.p.rest : 0;
       if (k < a.axis - 2) {
 #pragma unroll
@@ -210,6 +221,7 @@ struct Tile {
     __syncthreads();
     int slot = 0;
     for (int64_t k = k0; k < k1; k++) {
+      if (OUT == OUT_PARTS && k == a.axis) take_rest<T>(acc);
       if (k + 1 < k1) fetch(k + 1);
       const char *l = lds + slot * STAGE;
 #pragma unroll
@@ -228,6 +240,7 @@ struct Tile {
       __syncthreads();
       slot ^= 1;
     }
+    if (OUT == OUT_PARTS && k1 <= a.axis) take_rest<T>(acc);
   }
 };
 
@@ -235,7 +248,7 @@ struct Tile {
 // per lane.
 template <typename T, int TI, int TJ, bool QT, bool PT, int OUT>
 __global__ __launch_bounds__(LN_THREADS) void k_product(ProductArgs a) {
-  typedef Tile<T, TI, TJ, QT, PT> Tl;
+  typedef Tile<T, TI, TJ, QT, PT, OUT> Tl;
   __shared__ __attribute__((aligned(16))) char lds[Tl::LDS];
   const int64_t t = blockIdx.x, i0 = (t / a.tj) * TI, j0 = (t % a.tj) * TJ;
   const int64_t k0 = blockIdx.y * a.per, k1 = k0 + a.per < a.steps ? k0 + a.per : a.steps;
@@ -300,7 +313,7 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT>
+template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT, int OUT>
 struct Direct {
   typedef Stage<T, TI, QT> SQ;
   typedef Stage<T, TJ, PT> SP;
@@ -345,20 +358,21 @@ struct Direct {
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds + w * (WAVE * 16));
     const int64_t dq = (QT ? a.q.stride * SQ::KE : SQ::KE) * (int64_t)sizeof(T);
     const int64_t dp = (PT ? a.p.stride * SP::KE : SP::KE) * (int64_t)sizeof(T);
-    const int last = (int)a.axis - 1, left = (int)(a.K - (int64_t)last * SQ::KE);    // of the last stage
+    // the last stage; one more may follow it, of zeros, so that the stages of a part are even
+    const int last = (int)((a.K - 1) / SQ::KE), left = (int)(a.K - (int64_t)last * SQ::KE);
     // stages past the end load the last one again, so that the count of loads in flight
     // stays a constant
     auto fetch = [&](int k, int slot) {
       const int stage = k < k1 ? k : k1 - 1;
-      const bool second = stage >= (int)a.axis;
-      const int kk = second ? stage - (int)a.axis : stage;
+      const bool first = stage >= (int)a.axis, second = a.parts == 2 && !first;
+      const int kk = first ? stage - (int)a.axis : stage;
       const uint32_t l = base + slot * STAGE;
       const int64_t oq = kk * dq + (second ? a.q.rest : 0), op = kk * dp + (second ? a.p.rest : 0);
-      const bool whole = kk < last || left == SQ::KE;
+      const int there = kk < last ? SQ::KE : kk == last ? left : 0;
 #pragma unroll
       for (int n = 0; n < LOADS; n++) {
         const char *p = src[n] + (n < LQ ? oq : op);
-        if (!whole && at[n] >= left) p = reinterpret_cast<const char *>(&zero_chunk);
+        if (there < SQ::KE && at[n] >= there) p = reinterpret_cast<const char *>(&zero_chunk);
         to_lds(p, l + (n < LQ ? n * THREADS * 16 : SQ::BYTES + (n - LQ) * THREADS * 16));
       }
     };
@@ -404,10 +418,13 @@ struct Direct {
     };
     int k = k0;
     for (; k + 1 < k1; k += 2) {
+      // a workgroup has an even number of the second parts' stages
+      if (OUT == OUT_PARTS && k == (int)a.axis) take_rest<T>(acc);
       step(k, 0);
       step(k + 1, 1);
     }
     if (k < k1) step(k, 0);
+    if (OUT == OUT_PARTS && k1 <= (int)a.axis) take_rest<T>(acc);
     // nothing may land in LDS after this
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
@@ -427,7 +444,7 @@ __device__ __forceinline__ int64_t by_xcd(int64_t b, int64_t n) {
 // 1536 x 1000 fp32: 107 to 122 us, 103 to 117 TFLOP/s of the 154 of a large library product.
 template <typename T, int TI, int TJ, int WI, int WJ, int NST, bool QT, bool PT, int OUT>
 __global__ __launch_bounds__(WI * WJ * WAVE, TI * TJ > 128 * 128 * WI * WJ / 2 ? 1 : 2) void k_direct(ProductArgs a) {
-  typedef Direct<T, TI, TJ, WI, WJ, NST, QT, PT> D;
+  typedef Direct<T, TI, TJ, WI, WJ, NST, QT, PT, OUT> D;
   __shared__ __attribute__((aligned(16))) char lds[D::LDS];
   // runs of eight tiles along I by all of J
   const int64_t t = by_xcd(blockIdx.x, a.ti * a.tj), band = t / (8 * a.tj), in = t - band * 8 * a.tj;
@@ -600,9 +617,13 @@ __global__ __launch_bounds__((Few<T, PT>::THREADS)) void k_few(ProductArgs a) {
   const int K = (int)a.K, from = (int)(blockIdx.y * a.per), to = from + a.per < a.axis ? (int)(from + a.per) : (int)a.axis;
   const int per = (to - from + F::WAVES - 1) / F::WAVES;
   const int s0 = from + w * per, s1 = s0 + per < to ? s0 + per : to;
-  float4v acc[NT];
+  constexpr bool REST_APART = OUT == OUT_PARTS;
+  float4v acc[NT], acc2[REST_APART ? NT : 1];
 #pragma unroll
-  for (int t = 0; t < NT; t++) acc[t] = float4v{0, 0, 0, 0};
+  for (int t = 0; t < NT; t++) {
+    acc[t] = float4v{0, 0, 0, 0};
+    if constexpr (REST_APART) acc2[t] = float4v{0, 0, 0, 0};
+  }
   const T *q = (const T *)a.q.p + i * a.q.stride + g * E, *q2 = (const T *)((const char *)q + a.q.rest);
   const bool row = i < a.I;
   for (int s = s0; s < s1; s += U) {
@@ -632,8 +653,15 @@ __global__ __launch_bounds__((Few<T, PT>::THREADS)) void k_few(ProductArgs a) {
         if constexpr (PT) f = turn<T>(p[u], t);
         else f = p[u][t];
         acc[t] = few_mul<T>(f, x[u], acc[t]);
-        if (a.parts == 2) acc[t] = few_mul<T>(f, x2[u], acc[t]);
+        float4v &sum = REST_APART ? acc2[REST_APART ? t : 0] : acc[t];
+        if (a.parts == 2) sum = few_mul<T>(f, x2[u], sum);
       }
+  }
+  if constexpr (REST_APART) {
+#pragma unroll
+    for (int t = 0; t < NT; t++)
+#pragma unroll
+      for (int r = 0; r < 4; r++) acc[t][r] = __builtin_fmaf(acc2[t][r], REST<T>, acc[t][r]);
   }
   // a lane holds row i of C: of fragment t rows 4 g + r of P's, columns 16 t + 4 g + r of the
   // tile, or E (4 g + r) + t
@@ -685,12 +713,13 @@ bool whole_chunks(const Operand &o, bool tr, int64_t R, int64_t K) {
 
 template <typename T, int OUT>
 int join(const ProductArgs &a, hipStream_t stream) {
+  constexpr int TO = OUT == OUT_LAYER ? OUT_LAYER : OUT_STORE;
   const int64_t items = a.I * ((a.J + 7) / 8);
   auto blocks = [](int64_t n) { return dim3((unsigned)(n < 65536 ? n : 65536)); };
   if (a.splits >= 16 && items < 65536)
-    hipLaunchKernelGGL((k_product_join<T, OUT, 16>), blocks((items + 15) / 16), dim3(LN_THREADS), 0, stream, a, a.splits);
+    hipLaunchKernelGGL((k_product_join<T, TO, 16>), blocks((items + 15) / 16), dim3(LN_THREADS), 0, stream, a, a.splits);
   else
-    hipLaunchKernelGGL((k_product_join<T, OUT, 1>), blocks((items + LN_THREADS - 1) / LN_THREADS), dim3(LN_THREADS), 0, stream, a,
+    hipLaunchKernelGGL((k_product_join<T, TO, 1>), blocks((items + LN_THREADS - 1) / LN_THREADS), dim3(LN_THREADS), 0, stream, a,
                        a.splits);
   SPLAT_LAUNCH_CHECK();
   return SPLAT_OK;
@@ -699,6 +728,7 @@ int join(const ProductArgs &a, hipStream_t stream) {
 template <typename T, bool QT, bool PT, int OUT>
 int run_product(ProductArgs a, hipStream_t stream) {
   constexpr int KE = 64 / sizeof(T);
+  constexpr bool FOUR = QT && PT && OUT != OUT_PARTS;    // waves of the largest tiles, or eight
   const Cut cut = product_cut(a.I, a.J, a.K, a.parts, sizeof(T) == 4 ? SPLAT_F32 : SPLAT_F16);
   a.axis = (a.K + KE - 1) / KE;
   if constexpr (!QT) {
@@ -712,9 +742,11 @@ int run_product(ProductArgs a, hipStream_t stream) {
       return a.splits > 1 ? join<T, OUT>(a, stream) : SPLAT_OK;
     }
   }
-  const bool direct = a.K > 0 && whole_chunks<T>(a.q, QT, a.I, a.K) && whole_chunks<T>(a.p, PT, a.J, a.K);
+  const bool direct = a.K > 0 && whole_chunks<T>(a.q, QT, a.I, a.K) && whole_chunks<T>(a.p, PT, a.J, a.K), even = direct && OUT == OUT_PARTS;
+  if (even) a.axis += a.axis & 1;
   a.steps = a.axis * a.parts;
   a.per = (a.steps + cut.splits - 1) / cut.splits;
+  if (even) a.per += a.per & 1;
   a.splits = a.per > 0 ? (int)((a.steps + a.per - 1) / a.per) : 1;
   // arrays that are not whole, aligned chunks: tiles of 128 or 64 through registers; of 16-bit
   // types 128 wherever they fill the chip (4001 x 999 to 1501 bf16: 43 us, 61 with 64)
@@ -729,8 +761,9 @@ int run_product(ProductArgs a, hipStream_t stream) {
     hipLaunchKernelGGL((k_product<T, 64, 64, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
   else if (cut.tile == 0)
     // transposing reads bring half as much a cycle: with both operands transposed four waves of
-    // 128 x 128, which read least, beat eight (4096 by 4096 by 4096 bf16, forward and backward: 381 us, 407 with eight)
-    hipLaunchKernelGGL((k_direct<T, 256, 256, 2, QT && PT ? 2 : 4, 4, QT, PT, OUT>), grid, dim3(QT && PT ? 256 : 512), 0, stream, a);
+    // 128 x 128, which read least, beat eight (4096 by 4096 by 4096 bf16, forward and backward: 381 us, 407 with eight).
+    // With sums to multiply on the way their registers do not suffice (532 bytes a lane spill)
+    hipLaunchKernelGGL((k_direct<T, 256, 256, 2, FOUR ? 2 : 4, 4, QT, PT, OUT>), grid, dim3(FOUR ? 256 : 512), 0, stream, a);
   else if (cut.tile == 1)
     hipLaunchKernelGGL((k_direct<T, 128, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
   else
@@ -742,6 +775,12 @@ int run_product(ProductArgs a, hipStream_t stream) {
 template <typename T>
 int product(const ProductArgs &a, bool qt, bool pt, int out, hipStream_t s) {
   if (out == OUT_LAYER) return pt ? run_product<T, false, true, OUT_LAYER>(a, s) : run_product<T, false, false, OUT_LAYER>(a, s);
+  if constexpr (REST<T> != 1.0f) {
+    if (a.parts == 2) {
+      if (qt) return run_product<T, true, true, OUT_PARTS>(a, s);
+      return pt ? run_product<T, false, true, OUT_PARTS>(a, s) : run_product<T, false, false, OUT_PARTS>(a, s);
+    }
+  }
   if (qt) return run_product<T, true, true, OUT_STORE>(a, s);
   return pt ? run_product<T, false, true, OUT_STORE>(a, s) : run_product<T, false, false, OUT_STORE>(a, s);
 }

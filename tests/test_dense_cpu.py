@@ -163,3 +163,16 @@ def test_forward_mode_is_refused():
                      lambda: A.dropout_backward(dual(x), 0.5, (1, 2))):
             with pytest.raises(NotImplementedError, match="forward-mode"):
                 call()
+
+
+def test_the_large_layers_reach_every_tile():
+    """The layers that the GPU tests hold value by value are cut in every way that there is."""
+    from tests.dense_layers import LARGE, cut
+    products = dict(y=lambda m, k, n: [(m, n, k)], d_x=lambda m, k, n: [(m, k, n)], d_W=lambda m, k, n: [(k, n, m), (n, k, m)])
+    for f32, parts, tiles in ((False, 1, {0, 1, 2}), (False, 2, {0, 1, 2}), (True, 1, {1, 2})):
+        got = {name: {cut(*size, parts, f32) for c in LARGE for size in sizes(*c)} for name, sizes in products.items()
+               if name != "y" or parts == 1}
+        for name, cuts in got.items():
+            assert {t for t, _ in cuts} == tiles, (name, f32, parts)
+        whole, split = ({t for cuts in got.values() for t, s in cuts if (s > 1) == k} for k in (False, True))
+        assert whole == tiles and split == tiles, (f32, parts)

@@ -13,6 +13,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from oracle import dense as D
+from tests.dense_layers import LARGE
 
 U = 2.0 ** -24
 RO = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
@@ -132,3 +133,98 @@ def test_gradients_of_nothing_kept(dev, m, k, n, dt):
     for act in ("none", "gelu"):
         for g in A.linear_backward(dy, x, w, act=act, p=1.0, rng=(1, 2)):
             assert torch.equal(g, torch.zeros_like(g))
+
+
+@pytest.mark.parametrize("large", ["x", "w"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("m,k,n", LAYERS)
+def test_small_gradients_of_fp16(dev, m, k, n, act, large):
+    """d_y down to fp16's smallest step: dz is held to 2^-22 of itself and to 2^-35, whatever the
+    others' size. x or W is large, so that the gradients' own steps do not hide it."""
+    rng = np.random.default_rng(m + k + n)
+    xn, wn = rng.standard_normal((m, k)), rng.standard_normal((k, n)) * k ** -0.5
+    xn, wn = (4.0 * xn, wn / 4.0) if large == "x" else (xn * k ** -0.5 / 4.0, 4.0 * wn * k ** 0.5)
+    x, w, b = _put(xn, "f16", dev), _put(wn, "f16", dev), _put(0.3 * rng.standard_normal(n), "f32", dev)
+    for scale in (2.0 ** -16, 2.0 ** -20, 2.0 ** -22, 2.0 ** -24, 0.0):
+        # 0: every row has a size of its own, from the smallest step to a hundred
+        by = scale if scale else 2.0 ** rng.integers(-24, 8, (m, 1))
+        dy = _put(by * rng.standard_normal((m, n)), "f16", dev)
+        for p in (0.0, 0.25):
+            _gradients("f16", act, p, x, w, b, dy, (2.0 ** -22, 2.0 ** -35), f"{act} {scale} p {p}")
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("order", ["io", "oi"])
+@pytest.mark.parametrize("m,k,n", LARGE)
+def test_large_layers(dev, m, k, n, order, dt):
+    """Every tile of the products, whole and split, at ends inside tiles and stages, with all that
+    goes with the forward, value by value against torch in 64 bits. dz of bf16 may be rounded once."""
+    from sphere_rasterization_amd import appearance as A
+    gen = torch.Generator(device=dev).manual_seed(m + k + n)
+    randn = lambda *s: torch.randn(*s, generator=gen, device=dev)
+    x, r, dy = (randn(*s).to(DT[dt]) for s in ((m, k), (m, n), (m, n)))
+    w = (randn(k, n) * k ** -0.5).to(DT[dt]) if order == "io" else (randn(n, k) * k ** -0.5).to(DT[dt]).t()
+    b, p = randn(n).to(DT[dt]), 0.1
+    more = dict(act="gelu", p=p, rng=(5, 6))
+    y, pre = A.linear_forward(x, w, b, residual=r, **more)
+    dx, dw, db = A.linear_backward(dy, x, w, b, pre=pre, **more)
+    keep = A.dropout(torch.ones_like(y), p, (5, 6)) != 0
+    wide = lambda t: t.double().contiguous()
+    x, w, b, r, dy = (wide(t) for t in (x, w, b, r, dy))
+    mm = lambda a, c: a @ c.contiguous()
+    s = keep / (1.0 - p)
+    z = mm(x, w) + b
+    e_z = 2 * (k + 8) * U * (mm(x.abs(), w.abs()) + b.abs())
+    cdf, density = torch.special.ndtr(z), torch.exp(-0.5 * z * z) * 0.3989422804014327
+    want = r + s * z * cdf
+    # gelu of 16-bit results is off by 1.9e-6 and a fifth of a rounding more
+    e_y = s * (1.13 * e_z + 2e-6 + 8 * U * z.abs()) + 4 * U * (want.abs() + r.abs()) + 1.2 * RO[dt] * want.abs() + TINY[dt]
+    e_pre = RO[dt] * z.abs() + TINY[dt]
+
+    def check(got, ref, tol, what):
+        bad = ~((got.double() - ref).abs() <= tol)
+        assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((got.double() - ref).abs().max()):.3e}"
+
+    check(y, want, e_y, "y")
+    check(pre, z, e_z + e_pre, "pre")
+    dz = s * dy * (cdf + z * density)
+    rel = dict(f32=0.0, f16=RO["f16"] ** 2, bf16=RO["bf16"])[dt]
+    e_dz = s * dy.abs() * (e_z + e_pre + 2e-7 + 8 * U) + (rel + 4 * U) * dz.abs() + TINY[dt] ** 2
+    a = dz.abs() + e_dz
+    top = lambda v: RO[dt] * v.abs() + TINY[dt]
+    ref = mm(dz, w.t())
+    check(dx, ref, mm(e_dz, w.abs().t()) + 2 * (2 * n + 8) * U * mm(a, w.abs().t()) + top(ref), "d_x")
+    ref = mm(x.t(), dz)
+    check(dw, ref, mm(x.abs().t(), e_dz) + 2 * (2 * m + 8) * U * mm(x.abs().t(), a) + top(ref), "d_W")
+    ref = dz.sum(0)
+    check(db, ref, e_dz.sum(0) + 2 * (m + 8) * U * a.sum(0) + top(ref), "d_b")
+    # and in the norm, where the roundings' signs cancel: those of z, of dz and of the result, at most RO each
+    for got, ref in ((dx, mm(dz, w.t())), (dw, mm(x.t(), dz))):
+        assert float((got.double() - ref).norm() / ref.norm()) <= 3 * RO[dt] + 2e-6
+
+
+@pytest.mark.parametrize("m,k,n", LARGE)
+def test_small_gradients_of_large_fp16_layers(dev, m, k, n):
+    """d_y of a few of fp16's smallest steps: dz is held to 2^-35 on every tile and across splits
+    that hold parts of both of its parts. x is large and z exact, so that nothing else counts."""
+    from sphere_rasterization_amd import appearance as A
+    gen = torch.Generator(device=dev).manual_seed(m + k + n)
+    randn = lambda *s: torch.randn(*s, generator=gen, device=dev)
+    x, dy = (8.0 * torch.sign(randn(m, k))).half(), (2.0 ** -23 * randn(m, n)).half()
+    w = torch.zeros(k, n, device=dev)
+    w[torch.randint(0, k, (n,), generator=gen, device=dev), torch.arange(n, device=dev)] = 0.0625 * torch.sign(randn(n))
+    w = w.half()
+    dx, dw, db = A.linear_backward(dy, x, w, act="silu", pre=A.linear_forward(x, w, act="silu")[1])
+    x, w, dy = x.double(), w.double(), dy.double()
+    z = x @ w
+    assert bool(((z.abs() == 0.5) | (z == 0.0)).all())        # a normal number may be 0, and its sign then
+    dz = dy * (torch.sigmoid(z) + z * torch.sigmoid(z) * torch.sigmoid(-z))
+    e_dz = (2e-7 + 8 * U) * dy.abs() + 2.0 ** -22 * dz.abs() + 2.0 ** -35
+    for got, ref, e, size in ((dx, dz @ w.t().contiguous(), e_dz @ w.abs().t().contiguous(), dz.abs() @ w.abs().t().contiguous()),
+                              (dw, x.t().contiguous() @ dz, x.abs().t().contiguous() @ e_dz, x.abs().t().contiguous() @ dz.abs())):
+        bad = ~((got.double() - ref).abs() <= e + 2 * (2 * max(m, n) + 8) * U * size + RO["f16"] * ref.abs() + TINY["f16"])
+        assert not bool(bad.any()), (int(bad.sum()), float((got.double() - ref).abs().max()))
+        # in the norm: errors of dz of 2^-35 at most add up as independent ones, beside one rounding
+        err, most = float((got.double() - ref).norm()), float((ref.half().double() - ref).norm())
+        count = float(n if got is dx else m)
+        assert err <= 1.1 * most + 2.0 ** -35 * (8.0 if got is dw else 0.0625) * (count * got.numel()) ** 0.5 + 4e-6 * float(ref.norm())
