@@ -358,21 +358,24 @@ struct Direct {
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds + w * (WAVE * 16));
     const int64_t dq = (QT ? a.q.stride * SQ::KE : SQ::KE) * (int64_t)sizeof(T);
     const int64_t dp = (PT ? a.p.stride * SP::KE : SP::KE) * (int64_t)sizeof(T);
-    // the last stage; one more may follow it, of zeros, so that the stages of a part are even
+    const int skip = a.parts == 2 ? (int)a.axis : 0;
+    // the last stage; with OUT_PARTS one more may follow it, of zeros, so that a part's are even
     const int last = (int)((a.K - 1) / SQ::KE), left = (int)(a.K - (int64_t)last * SQ::KE);
     // stages past the end load the last one again, so that the count of loads in flight
     // stays a constant
     auto fetch = [&](int k, int slot) {
       const int stage = k < k1 ? k : k1 - 1;
-      const bool first = stage >= (int)a.axis, second = a.parts == 2 && !first;
-      const int kk = first ? stage - (int)a.axis : stage;
+      // second parts come first
+      const bool second = OUT != OUT_LAYER && a.parts == 2 && stage < (int)a.axis;
+      const int kk = OUT == OUT_LAYER || second ? stage : stage - skip;
       const uint32_t l = base + slot * STAGE;
       const int64_t oq = kk * dq + (second ? a.q.rest : 0), op = kk * dp + (second ? a.p.rest : 0);
-      const int there = kk < last ? SQ::KE : kk == last ? left : 0;
+      const bool whole = kk < last || (left == SQ::KE && (OUT != OUT_PARTS || kk == last));
+      const int there = OUT == OUT_PARTS && kk > last ? 0 : left;
 #pragma unroll
       for (int n = 0; n < LOADS; n++) {
         const char *p = src[n] + (n < LQ ? oq : op);
-        if (there < SQ::KE && at[n] >= there) p = reinterpret_cast<const char *>(&zero_chunk);
+        if (!whole && at[n] >= there) p = reinterpret_cast<const char *>(&zero_chunk);
         to_lds(p, l + (n < LQ ? n * THREADS * 16 : SQ::BYTES + (n - LQ) * THREADS * 16));
       }
     };
