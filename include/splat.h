@@ -438,9 +438,9 @@ int splat_linear(const splat_dense *dense, const void *x, const void *w, const v
  * may pass 65504 and then reads back infinite). drop has to be the forward's, the state's words too.
  * What is multiplied is dz (1 - p), the fp32 sums take the factor: a finite d_y overflows no
  * product. 16-bit layers multiply it in two parts of dtype with silu or gelu (fp16: to 2^-22 of
- * itself and 2^-35; bf16: to 2^-16 of itself, but rounded to bf16 with many rows and large W);
- * with none and relu it is exact in dtype. In two parts an infinite x or W may give NaN in the
- * place of an infinite gradient. */
+ * itself and 2^-35; bf16: to 2^-16 of itself, but rounded to bf16, and multiplied once, where in x out
+ * is 2^15 or more and rows x in x out 2^31 or more); with none and relu it is exact in dtype. In two
+ * parts an infinite x or W may give NaN in the place of an infinite gradient. */
 int splat_linear_bwd(const splat_dense *dense, const void *d_y, const void *x, const void *w, const void *bias,
                      const void *pre, void *d_x, void *d_w, void *d_bias, void *workspace, size_t ws_bytes,
                      hipStream_t stream);

@@ -135,14 +135,17 @@ int64_t slope_chunks(int64_t M, int64_t N) {
 // W as [in][out], `out` contiguous, or its transpose.
 bool w_by_out(int64_t si, int64_t so) { return so == 1 && si != 1; }
 
-// Parts of dz with silu's or gelu's slope. One rounding of it adds as much error to dx and dW as their own rounding: where
-// dz or a gradient has few values, with luck more, and the products cost little. Where all are
-// many the two errors (and that of z, read back rounded) stay at 1.45 to 1.46 of the one, and a
-// second part would take up to twice the time (8191 x 1024 to 4096 bf16: 144 us of products). fp16
-// has not the range for one part.
+// Parts of dz. None's and relu's is exact in one. With silu or gelu one rounding of it adds as much
+// error to dx and dW as their own rounding does (1.41 times it in all), and a second part doubles the
+// products' operations. fp16 has not the range for one part. bf16 takes two as long as the second costs
+// 15 us at most, and one for larger layers (2048 x 512 to 512: 38 us of backward and 31 with one; 2048 x
+// 1024 to 1024 55 and 41; 8192 x 1024 to 2048 208 and 125), and two where W is small and dW's few values
+// are sums over long arrays, at any length (1M x 100 to 72: 508 and 371).
 int parts_of(const splat_dense *d) {
-  const bool many = d->rows * d->out >= (1 << 20) && d->rows * d->in >= (1 << 18) && (int64_t)d->in * d->out >= (1 << 15);
-  return !slope_of_bits(d->act) && (d->dtype == SPLAT_F16 || (d->dtype == SPLAT_BF16 && !many)) ? 2 : 1;
+  if (slope_of_bits(d->act) || d->dtype == SPLAT_F32) return 1;
+  const int64_t weights = (int64_t)d->in * d->out;
+  const bool large = weights >= (1 << 15) && d->rows >= ((1ll << 31) + weights - 1) / weights;
+  return d->dtype == SPLAT_BF16 && large ? 1 : 2;
 }
 
 struct Plan {

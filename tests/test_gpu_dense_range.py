@@ -228,3 +228,39 @@ def test_small_gradients_of_large_fp16_layers(dev, m, k, n):
         err, most = float((got.double() - ref).norm()), float((ref.half().double() - ref).norm())
         count = float(n if got is dx else m)
         assert err <= 1.1 * most + 2.0 ** -35 * (8.0 if got is dw else 0.0625) * (count * got.numel()) ** 0.5 + 4e-6 * float(ref.norm())
+
+
+TWO_PARTS = [("bf16", *s) for s in ((2000, 24, 32), (2000, 64, 64), (2001, 33, 45), (1000, 264, 392), (1001, 203, 131), (16, 2048, 520),
+                                    (9, 304, 264), (4100, 504, 1032), (70_000, 160, 200))]
+TWO_PARTS += [("f16", *s) for s in ((2000, 24, 32), (2001, 33, 45), (1001, 203, 131), (9, 304, 264), (4200, 520, 1000), (8191, 1024, 2056))]
+ONE_PART = [("bf16", *s) for s in ((4200, 520, 1000), (65_536, 160, 208), (4199, 521, 1001), (600, 1024, 4096))]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu", "none"])
+@pytest.mark.parametrize("dt,m,k,n", TWO_PARTS + ONE_PART)
+def test_parts_of_dz(dev, dt, m, k, n, act):
+    """How dz is held, by the error of the gradients over that of rounding them once: 1 where dz is
+    exact or in two parts, and the square root of 2 where one more rounding of the same size goes in.
+    z is exact in the type (sums of 1/16), so that only dz counts. Both errors are norms over more than
+    2000 values of one distribution, steady to a few in a hundred."""
+    from sphere_rasterization_amd import appearance as A
+    gen = torch.Generator(device=dev).manual_seed(m + k + n)
+    sign = lambda *s: torch.where(torch.rand(*s, generator=gen, device=dev) < 0.5, 1.0, -1.0)
+    x, w = sign(m, k).to(DT[dt]), (sign(k, n) / 16).to(DT[dt])
+    dy = torch.randn(m, n, generator=gen, device=dev).to(DT[dt])
+    _, pre = A.linear_forward(x, w, act=act)
+    got = A.linear_backward(dy, x, w, act=act, pre=pre, p=0.25, rng=(5, 6))
+    keep = A.dropout(torch.ones_like(dy), 0.25, (5, 6)) != 0
+    x, w, dz = x.double(), w.double(), dy.double() * keep / 0.75
+    z = x @ w
+    if act == "silu":
+        dz = dz * (torch.sigmoid(z) + z * torch.sigmoid(z) * torch.sigmoid(-z))
+    elif act == "gelu":
+        dz = dz * (torch.special.ndtr(z) + z * torch.exp(-0.5 * z * z) * 0.3989422804014327)
+    elif act == "relu":
+        dz = dz * (z > 0)
+    one = (dt, m, k, n) in ONE_PART and act in ("silu", "gelu")
+    for what, g, ref in (("d_x", got[0], dz @ w.t().contiguous()), ("d_W", got[1], x.t().contiguous() @ dz)):
+        once = float((ref.to(DT[dt]).double() - ref).norm())
+        ratio = float((g.double() - ref).norm()) / once
+        assert (1.2 <= ratio <= 1.6) if one else ratio <= 1.1, (what, ratio)
