@@ -300,7 +300,7 @@ __global__ __launch_bounds__(LN_THREADS) void k_product(ProductArgs a) {
 // reads LDS by the transposing instruction, which would leave one stage in flight (8192 x 4096
 // by 4096 x 4096 bf16: 359 us).
 __device__ __forceinline__ void to_lds(const void *p, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "m0", "memory");
 }
 
 // Asks the compiler for the step's fragment reads and matrix instructions in turn.
