@@ -613,7 +613,7 @@ __global__ __launch_bounds__((Few<T, PT>::THREADS)) void k_few(ProductArgs a) {
   typedef Few<T, PT> F;
   constexpr int E = F::E, KE = F::KE, NT = F::TILES_J, U = F::UNROLL, LOADS = PT ? E : NT;
   typedef const typename Loose<T, E>::type *ptr;
-  __shared__ float sums[F::WAVES * 16 * F::PITCH];
+  __shared__ __attribute__((aligned(16))) float sums[F::WAVES * 16 * F::PITCH];
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4, w = threadIdx.x >> 6;
   const int64_t j0 = (int64_t)blockIdx.x * F::J;
   // stages of this workgroup's share of the axis, and of this wave's
