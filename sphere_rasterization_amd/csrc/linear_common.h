@@ -19,6 +19,12 @@ struct LayerArgs {
   DropArgs drop;
 };
 
+// Orders a wave's own LDS accesses: the hardware keeps them in program order.
+__device__ __forceinline__ void wave_lds_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---- the end of a value's way ---------------------------------------------------------
 
 template <typename T, int ACT>

@@ -110,12 +110,6 @@ __device__ __forceinline__ word4 load_chunk(const T *row, int at, const RowEnd<T
   return v;
 }
 
-// Orders a wave's own LDS accesses: the hardware keeps them in program order.
-__device__ __forceinline__ void wave_lds_order() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_wave_barrier();
-}
-
 template <typename T, int KP, int NP, bool EASY>
 struct Rows {
   static constexpr int E = 16 / sizeof(T);            // values per chunk

@@ -268,7 +268,7 @@ __global__ __launch_bounds__(LN_THREADS) void k_product(ProductArgs a) {
       for (int e = 0; e < 4; e++)
         *reinterpret_cast<float4 *>(patch + (lane & 31) * Tl::PITCH + 8 * e + 4 * (lane >> 5)) =
             make_float4(acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]);
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         const int r = h * 16 + (lane >> 2), c = (lane & 3) * 8;
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(LN_THREADS) void k_product(ProductArgs a) {
           emit8<T, OUT>(a, key, row, col, n, bias, res, v);
         }
       }
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
     }
 }
 
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(WI * WJ * WAVE, TI * TJ > 128 * 128 * WI * WJ / 2 ?
                 make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
           }
       }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
 #pragma unroll 1
     for (int h = 0; h < 4; h++) {
       const int64_t row = wi + b % D::FI * 32 + h * 8 + pr;
@@ -502,7 +502,7 @@ __global__ __launch_bounds__(WI * WJ * WAVE, TI * TJ > 128 * 128 * WI * WJ / 2 ?
       load8<float>(patch + (h * 8 + pr) * D::PITCH + pc, 8, v);
       if (row < a.I && n > 0) emit8<T, OUT>(a, key, row, col, n, bias, res, v);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
   }
 }
 
