@@ -302,15 +302,16 @@ Cut product_cut(int64_t I, int64_t J, int64_t K, int parts, int dtype) {
     int fit;
     double one, all, rest;       // rest: of a tile outside its stages
   };
-  static constexpr Rate RATES[2][3] = {{{1, 0.99, 0.99, 8.0}, {2, 0.42, 0.64, 5.0}, {3, 0.30, 0.55, 4.0}},
-                                       {{1, 4.40, 4.40, 8.0}, {2, 1.10, 1.95, 5.0}, {3, 0.60, 1.50, 4.0}}};
+  // fp32 has no tiles of 256: four of 128 take 3.9 us a stage on a CU, one of 256 took 4.4
+  static constexpr Rate RATES[3] = {{1, 0.99, 0.99, 8.0}, {2, 0.42, 0.64, 5.0}, {3, 0.30, 0.55, 4.0}},
+                        RATES_F32[2] = {{2, 1.10, 1.95, 5.0}, {3, 0.60, 1.50, 4.0}};
   constexpr int CUS = 256;
   const int f32 = dtype == SPLAT_F32;
   const int64_t stages = parts * ((K + (f32 ? 16 : 32) - 1) / (f32 ? 16 : 32));
   Cut best = {2, 1};
   double least = 1e30;
-  for (int t = 0; t < 3; t++) {
-    const Rate &r = RATES[f32][t];
+  for (int t = f32; t < 3; t++) {
+    const Rate &r = f32 ? RATES_F32[t - 1] : RATES[t];
     const int64_t tiles = ((I + TILES[t].i - 1) / TILES[t].i) * ((J + TILES[t].j - 1) / TILES[t].j);
     for (int s = 1; s <= 1024; s = s < 4 ? s + 1 : s + s / 2) {
       if (s > 1 && stages / s < 8) break;

@@ -762,12 +762,13 @@ int run_product(ProductArgs a, hipStream_t stream) {
     hipLaunchKernelGGL((k_product<T, 128, 128, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
   else if (!direct)
     hipLaunchKernelGGL((k_product<T, 64, 64, QT, PT, OUT>), grid, dim3(LN_THREADS), 0, stream, a);
-  else if (cut.tile == 0)
+  else if (cut.tile == 0) {                          // 16-bit types alone
     // transposing reads bring half as much a cycle: with both operands transposed four waves of
     // 128 x 128, which read least, beat eight (4096 by 4096 by 4096 bf16, forward and backward: 381 us, 407 with eight).
     // With sums to multiply on the way their registers do not suffice (532 bytes a lane spill)
-    hipLaunchKernelGGL((k_direct<T, 256, 256, 2, FOUR ? 2 : 4, 4, QT, PT, OUT>), grid, dim3(FOUR ? 256 : 512), 0, stream, a);
-  else if (cut.tile == 1)
+    if constexpr (sizeof(T) == 2)
+      hipLaunchKernelGGL((k_direct<T, 256, 256, 2, FOUR ? 2 : 4, 4, QT, PT, OUT>), grid, dim3(FOUR ? 256 : 512), 0, stream, a);
+  } else if (cut.tile == 1)
     hipLaunchKernelGGL((k_direct<T, 128, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
   else
     hipLaunchKernelGGL((k_direct<T, 64, 128, 2, 2, 4, QT, PT, OUT>), grid, dim3(256), 0, stream, a);
