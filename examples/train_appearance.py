@@ -1,7 +1,7 @@
 """Train a scene's appearance: a feature table that primitives share, and a shading network.
 
-One step reads every primitive's features from the table, renders them to a feature
-image, shades it by a small channels-last network (a dense layer, the normalisation, a
+One step reads every primitive's features from the table, drops some of them, renders them to a
+feature image, shades it by a small channels-last network (a dense layer, the normalisation, a
 hidden layer with dropout around which its input is passed, the colours) and compares the
 colours with a target; the gradients run back through all of it, and the network's matrices
 move by orthogonalised momentum.
@@ -69,6 +69,8 @@ def train(steps=50, n=30_000, width=320, height=192, lr=0.02, seed=0, device="cu
     losses = []
     for step in range(steps):
         feat = A.lookup(table, ids, scale=CHANNELS ** -0.5)
+        if dropout > 0.0:                                            # an offset of its own beside the hidden layer's
+            feat = A.dropout(feat, dropout, (seed, steps + step))
         img = render(rz, feat=feat)                                  # [channels][height][width], flat
         img = rz.view_images(img)[0].permute(1, 2, 0)                # channels last
         rgb = shade(img.reshape(1, height * width, CHANNELS), w1, gain, bias, wh, bh, w2, bias2, dropout, (seed, step))
@@ -94,6 +96,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--primitives", type=int, default=30_000)
-    ap.add_argument("--dropout", type=float, default=0.0, help="probability in the hidden layer")
+    ap.add_argument("--dropout", type=float, default=0.0, help="probability in the features and in the hidden layer")
     a = ap.parse_args()
     train(a.steps, n=a.primitives, dropout=a.dropout, log=lambda s: print(s, flush=True))

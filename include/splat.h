@@ -431,8 +431,8 @@ size_t splat_linear_workspace_bytes(const splat_dense *dense, int backward);
 int splat_linear(const splat_dense *dense, const void *x, const void *w, const void *bias, const void *residual,
                  void *y, void *pre, void *workspace, size_t ws_bytes, hipStream_t stream);
 
-/* Gradients w.r.t. x, W and b given d_y (overwritten; a NULL output is not computed):
- * dz = drop'(d_y) act'(z), d_x = dz W^T, d_W = x^T dz, d_b = column sums of dz; the
+/* Gradients w.r.t. x, W and b given d_y (overwritten; a NULL output is not computed; they
+ * overlap no input and each other nowhere): dz = drop'(d_y) act'(z), d_x = dz W^T, d_W = x^T dz, d_b = column sums of dz; the
  * residual's gradient is d_y itself. pre: what the forward wrote, or NULL: z is then
  * computed anew from x, W and b. act' of an infinite z is its limit, 0 or 1 (z of fp16 layers
  * may pass 65504 and then reads back infinite). drop has to be the forward's, the state's words too.
