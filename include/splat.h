@@ -432,10 +432,12 @@ int splat_linear(const splat_dense *dense, const void *x, const void *w, const v
                  void *y, void *pre, void *workspace, size_t ws_bytes, hipStream_t stream);
 
 /* Gradients w.r.t. x, W and b given d_y (overwritten; a NULL output is not computed; they
- * overlap no input and each other nowhere): dz = drop'(d_y) act'(z), d_x = dz W^T, d_W = x^T dz, d_b = column sums of dz; the
- * residual's gradient is d_y itself. pre: what the forward wrote, or NULL: z is then
- * computed anew from x, W and b. act' of an infinite z is its limit, 0 or 1 (z of fp16 layers
- * may pass 65504 and then reads back infinite). drop has to be the forward's, the state's words too.
+ * overlap no input and each other nowhere): dz = drop'(d_y) act'(z), d_x = dz W^T,
+ * d_W = x^T dz, d_b = column sums of dz; the residual's gradient is d_y itself. pre: what the
+ * forward wrote, or NULL: z is then computed anew from x, W and b. Layers of more than 64 inputs or
+ * outputs, or of fewer than 8 values a side, take act' at z rounded to dtype either way: relu's is 0
+ * where fp16 rounds a small z to 0, and of an infinite z (beyond 65504 in fp16) it is the limit,
+ * 0 or 1. drop has to be the forward's, the state's words too.
  * What is multiplied is dz (1 - p), the fp32 sums take the factor: a finite d_y overflows no
  * product. 16-bit layers multiply it in two parts of dtype with silu or gelu (fp16: to 2^-22 of
  * itself and 2^-35; bf16: to 2^-16 of itself, but rounded to bf16, and multiplied once, where in x out

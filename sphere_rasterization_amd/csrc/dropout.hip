@@ -3,8 +3,9 @@
 //
 // Bound by memory: 2 (with a residual 3) accesses an element, beside one Philox draw of ten
 // rounds per eight elements: 20 products of 32 x 32 to 64 bits, which issue at a quarter of
-// the rate, and 20 three-way exclusive ors. 66M fp16 elements with a residual: 60 us, 6.6 TB/s
-// (70 us when the second draw, for ties, was made by all).
+// the rate, and 20 three-way exclusive ors. 66M fp16 elements with a residual: 68 us, 5.9 TB/s,
+// with inputs that change from call to call; 60 us with the same ones, part of which the caches
+// hold (70 when the second draw, for ties, was made by all).
 #include "eight.h"
 #include "random.h"
 

@@ -26,7 +26,7 @@ struct SlopeArgs {
 constexpr int SL_COLS = 64;      // columns per workgroup: eight threads a row, 32 rows at once
 
 // dz = drop'(dy) act'(z) for some rows by 64 columns, and the columns' sums over them. 8191 x
-// 4096 bf16 with gelu and dropout: 52 us, 3.8 TB/s; some 50 instructions a value take 45 of them.
+// 4096 bf16 with gelu and dropout: 54 us, 3.7 TB/s; some 50 instructions a value take 45 of them.
 template <typename T>
 __global__ __launch_bounds__(LN_THREADS) void k_linear_slope(SlopeArgs a) {
   __shared__ float s[LN_THREADS / 8][SL_COLS + 1];
