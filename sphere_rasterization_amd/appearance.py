@@ -13,11 +13,12 @@
 `dropout_backward` are the same kernels without it. Forward-mode derivatives are refused:
 a tensor with a tangent raises NotImplementedError. Every step runs in libsplat's HIP
 kernels (csrc/lookup.hip, csrc/linear.hip, csrc/dropout.hip, csrc/group_norm.hip,
-csrc/orthogonalize.hip); torch provides device memory and the stream. Tensors are float32, float16 or bfloat16 on one GPU, and
-work is enqueued on that GPU's current stream. Arithmetic is fp32 with one rounding at
-the end, sums run in a fixed order (equal inputs give equal bits), and no call waits for
-the device. Tensors whose last axis is not contiguous, or whose pixels are not evenly
-spaced, are copied first; everything else is read in place.
+csrc/orthogonalize.hip); torch provides device memory and the stream. Tensors are float32,
+float16 or bfloat16 on one GPU, and work is enqueued on that GPU's current stream. Arithmetic
+is fp32 with one rounding at the end (`linear_backward` says what else is rounded there), sums
+run in a fixed order (equal inputs give equal bits), and no call waits for the device. Tensors
+whose last axis is not contiguous, or whose pixels are not evenly spaced, are copied first;
+everything else is read in place.
 """
 from __future__ import annotations
 
@@ -408,8 +409,9 @@ def linear_backward(d_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, bi
     out. The residual's gradient is d_y. pre: what `linear_forward` returned, or None (it is
     then computed anew). rng has to draw what the forward's drew: a state's words are read
     again. d_weight is laid out as weight is; d_bias has the type of bias (of x without one).
-    With 16-bit types, silu or gelu, and an infinite x or weight, a gradient may be NaN where
-    the formula has an infinity."""
+    With 16-bit types and silu or gelu, the gradient at z is multiplied in two parts of that
+    type, or, of bfloat16 with in * out >= 2^15 and rows * in * out >= 2^31, rounded to it; an
+    infinite x or weight may then give NaN where the formula has an infinity."""
     _no_tangents(d_y, x, weight, bias, pre)
     dt, k, n = _check_layer(x, weight, bias, act)
     drop = _drop(p, rng, x)
